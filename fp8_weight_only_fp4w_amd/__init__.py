@@ -31,6 +31,12 @@ The functions carry the C ABI's names (include/fp4w.h):
   block_size=16)``: that activation times the FP4 weights (W4A4);
   ``fp4w_matmul_w4a4_noalloc(...)``: the same with the activation staged in
   the library's own device scratch, for callers that cannot allocate.
+* ``fp4w_moe(A, ids, weights, w13, w13_scale, w13_scale_2, w2, w2_scale,
+  w2_scale_2)`` and ``fp8w_moe(A, ids, weights, w13, w13_scale, w2, w2_scale)``:
+  a whole mixture-of-experts layer for a few tokens on such weights;
+  ``fp4w_moe_route(logits, topk)``: its ids and weights from router logits;
+  ``fp4w_block_norm(x, residual, pre_weight, ...)``: the norms after one block
+  and before the next, with gate and residual scale.
 
 A keeps any leading dimensions; Y has A's leading dimensions, last dimension
 N and A's dtype.
@@ -55,16 +61,22 @@ PATH_QDQ_VEC, PATH_QDQ_GENERIC = 10, 11
 PATH_FP4_SKINNY, PATH_FP8_SKINNY = 12, 13
 PATH_FP8_DEQUANT_VEC, PATH_FP8_DEQUANT_GENERIC = 14, 15
 PATH_NVFP4_VEC, PATH_NVFP4_GENERIC = 16, 17
+PATH_MOE_FP4_GENERIC, PATH_MOE_FP8_GENERIC = 19, 21
 # operations (fp4w_op)
 OP_FP4_MATMUL, OP_FP8_MATMUL, OP_FP4_DEQUANT, OP_FP8_QDQ, OP_FP8_DEQUANT, OP_NVFP4_ACT = 0, 1, 2, 3, 4, 5
 # dtypes (fp4w_dtype)
-F16, BF16 = 0, 1
+F16, BF16, F32 = 0, 1, 2
+# scores (fp4w_score) and activations (fp4w_activation) by name
+SCORES = {"softmax": 0, "sigmoid": 1}
+ACTIVATIONS = {"silu": 0, "gelu": 1}
+MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_MAX_ASSIGNMENTS = 1024, 64, 4096
 
 EXPORTED = (
     "fp4w_matmul", "fp4w_matmul_ex", "fp8w_matmul", "fp8w_matmul_ex", "fp4w_dequant",
     "fp4w_dequant_ex", "fp8w_dequant", "fp8w_dequant_ex", "fp8w_qdq_activation", "fp8w_qdq_activation_ex", "fp8w_matmul_w8a8",
     "fp4w_quantize_activation", "fp4w_quantize_activation_ex", "fp4w_qdq_activation", "fp4w_qdq_activation_ex",
     "fp4w_matmul_w4a4", "fp4w_matmul_w4a4_noalloc",
+    "fp4w_block_norm", "fp4w_moe_route", "fp4w_moe_workspace", "fp4w_moe", "fp4w_moe_ex", "fp8w_moe", "fp8w_moe_ex",
     "fp4w_select_path", "fp4w_status_string", "fp4w_path_name",
 )
 
@@ -121,6 +133,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fp4w_matmul_w4a4.restype = i32
     lib.fp4w_matmul_w4a4_noalloc.argtypes = [vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, vp, i32, vp]
     lib.fp4w_matmul_w4a4_noalloc.restype = i32
+    f32 = ctypes.c_float
+    lib.fp4w_block_norm.argtypes = [vp, i64, i64, vp, vp, i64, f32, vp, vp, f32, f32, vp, vp, i32, vp]
+    lib.fp4w_block_norm.restype = i32
+    lib.fp4w_moe_route.argtypes = [vp, i64, i64, i64, i32, vp, i32, f32, vp, vp, i32, vp]
+    lib.fp4w_moe_route.restype = i32
+    lib.fp4w_moe_workspace.argtypes = [i64, i64, i64, i64]
+    lib.fp4w_moe_workspace.restype = i64
+    moe = [vp, i64, i64, vp, vp, i64, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp, i32, vp]
+    lib.fp4w_moe.argtypes, lib.fp4w_moe.restype = moe, i32
+    lib.fp4w_moe_ex.argtypes, lib.fp4w_moe_ex.restype = moe + [i32], i32
+    moe = [vp, i64, i64, vp, vp, i64, vp, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp, i32, vp]
+    lib.fp8w_moe.argtypes, lib.fp8w_moe.restype = moe, i32
+    lib.fp8w_moe_ex.argtypes, lib.fp8w_moe_ex.restype = moe + [i32], i32
     lib.fp4w_select_path.argtypes = [i32, i64, i64, i64, i64, i64]
     lib.fp4w_select_path.restype = i32
     lib.fp4w_status_string.argtypes = [i32]
@@ -459,3 +484,215 @@ def fp4w_matmul_w4a4_noalloc(A: torch.Tensor, B: torch.Tensor, weight_scale: tor
                                       _dtype_code(A.dtype), _stream(dev))
     _check(st, "fp4w_matmul_w4a4_noalloc")
     return out
+
+
+# ---------------------------------------------------------------- around a mixture-of-experts block
+
+def _call(device: torch.device, f, what: str, *args):
+    """Call f(*args, stream) on the device's current stream, with that device current."""
+    stream = torch.cuda.current_stream(device)
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            status = f(*args, stream.cuda_stream)
+    else:
+        status = f(*args, stream.cuda_stream)
+    if status != OK:
+        raise FP4WError(status, what)
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
+
+
+def _like(t: torch.Tensor, name: str, A: torch.Tensor, shape):
+    """t is contiguous, on A's device, of A's type and of this shape."""
+    if t.shape != shape or t.dtype != A.dtype:
+        raise ValueError(f"{name} must be {tuple(shape)} with the type {A.dtype}, got {tuple(t.shape)} {t.dtype}")
+    _need(t, name, A.device)
+
+
+def _typed(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: torch.device):
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    _need(t, name, device)
+
+
+def fp4w_block_norm(x: torch.Tensor, residual: torch.Tensor = None, pre_weight: torch.Tensor = None,
+                    post_weight: torch.Tensor = None, gate: torch.Tensor = None, scale: float = 1.0,
+                    eps: float = 1e-6, weight_offset: float = 0.0, residual_out: torch.Tensor = None,
+                    out: torch.Tensor = None, write_residual: bool = True):
+    """The norms after one block and before the next: (residual_out, out) with
+
+        b = x, or rms_norm(x) * (weight_offset + post_weight)
+        residual_out = residual + scale * gate * b
+        out = rms_norm(residual_out, unrounded) * (weight_offset + pre_weight)
+
+    ``gate`` is [K] (or [1, K]), or x's shape.  ``out`` is None without
+    ``pre_weight``; with ``write_residual=False`` residual_out is neither
+    written nor returned.  ``residual_out`` and ``out`` may be x or residual."""
+    lib = load_library()
+    K = x.shape[-1] if x.dim() else 1
+    M = x.numel() // K if K else 0
+    code = _dtype_code(x.dtype)
+    _need(x, "x", x.device)
+    if residual is not None:
+        _like(residual, "residual", x, x.shape)
+    for t, name in ((pre_weight, "pre_weight"), (post_weight, "post_weight")):
+        if t is not None:
+            _like(t, name, x, (K,))
+    gate_rows = 1
+    if gate is not None:
+        if gate.shape == x.shape:
+            gate_rows = M
+            _like(gate, "gate", x, x.shape)
+        elif gate.dim() <= 2 and gate.numel() == K:
+            _like(gate, "gate", x, gate.shape)
+        else:
+            raise ValueError(f"gate must be [{K}] or {tuple(x.shape)}, got {tuple(gate.shape)}")
+    if not write_residual:
+        if residual_out is not None or pre_weight is None:
+            raise ValueError("write_residual=False goes with a pre_weight and without a residual_out")
+    elif residual_out is None:
+        residual_out = torch.empty_like(x)
+    else:
+        _like(residual_out, "residual_out", x, x.shape)
+    if pre_weight is None:
+        if out is not None:
+            raise ValueError("out needs a pre_weight")
+    elif out is None:
+        out = torch.empty_like(x)
+    else:
+        _like(out, "out", x, x.shape)
+    _call(x.device, lib.fp4w_block_norm, "fp4w_block_norm", x.data_ptr(), M, K, _data(post_weight), _data(gate),
+          gate_rows, scale, _data(residual), _data(pre_weight), weight_offset, eps, _data(residual_out), _data(out),
+          code)
+    return residual_out, out
+
+
+def fp4w_moe_route(logits: torch.Tensor, topk: int, score: str = "softmax", select_bias: torch.Tensor = None,
+                   renormalize: bool = True, scale: float = 1.0, ids: torch.Tensor = None,
+                   weights: torch.Tensor = None):
+    """(ids int32, weights float32), each [..., topk], of router logits
+    [..., E] in float16, bfloat16 or float32: the topk experts of each token,
+    best first, ties to the lowest index, and scale * their scores
+    (renormalised to a sum of scale by default).  ``select_bias`` (float32
+    [E]) takes part in the choice only.  Experts with a logit of -inf or NaN
+    are never chosen; places left over get id -1 and weight 0."""
+    lib = load_library()
+    dev = logits.device
+    code = F32 if logits.dtype == torch.float32 else _dtype_code(logits.dtype)
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    _need(logits, "logits", dev)
+    if logits.dim() < 1:
+        raise ValueError("logits must be [..., E]")
+    E, lead = logits.shape[-1], logits.shape[:-1]
+    M = lead.numel()
+    if select_bias is not None:
+        _typed(select_bias, "select_bias", torch.float32, (E,), dev)
+    if topk < 0:
+        raise ValueError("topk must not be negative")
+    shape = (*lead, topk)
+    if ids is None:
+        ids = torch.empty(shape, dtype=torch.int32, device=dev)
+    else:
+        _typed(ids, "ids", torch.int32, shape, dev)
+    if weights is None:
+        weights = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        _typed(weights, "weights", torch.float32, shape, dev)
+    _call(dev, lib.fp4w_moe_route, "fp4w_moe_route", logits.data_ptr(), M, E, topk, SCORES[score],
+          _data(select_bias), int(renormalize), scale, ids.data_ptr(), weights.data_ptr(), code)
+    return ids, weights
+
+
+def fp4w_moe_workspace(M: int, topk: int, K: int, I: int) -> int:  # noqa: E741
+    """Bytes of workspace that fp4w_moe and fp8w_moe need."""
+    n = int(load_library().fp4w_moe_workspace(M, topk, K, I))
+    if n < 0:
+        raise FP4WError(n, "fp4w_moe_workspace")
+    return n
+
+
+def _moe(fp8, A, ids, weights, w13, s13, g13, w2, s2, g2, block_size, activation, out, workspace, path):
+    lib = load_library()
+    dev = A.device
+    what = "fp8w_moe" if fp8 else "fp4w_moe"
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}, got {activation!r}")
+    code = _dtype_code(A.dtype)
+    if block_size < 1:
+        raise FP4WError(ERR_BLOCK, what)
+    if w13.dtype != torch.uint8 or w2.dtype != torch.uint8:
+        w13, w2 = _bytes(w13), _bytes(w2)
+    K = A.shape[-1]
+    lead = A.shape[:-1]
+    M = lead.numel()
+    topk = ids.shape[-1]
+    if w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("w13 must be [E, 2 I, K] and w2 [E, K, I] (FP4: two codes per byte)")
+    E, half = w2.shape[0], 1 if fp8 else 2
+    I = w2.shape[2] * half  # noqa: E741
+    if K % half or w13.shape != (E, 2 * I, K // half) or w2.shape[1] != K:
+        raise ValueError(f"w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not fit A's K = {K}")
+    _need(A, "A", dev)
+    _typed(ids, "ids", torch.int32, (*lead, topk), dev)
+    _typed(weights, "weights", torch.float32, (*lead, topk), dev)
+    _need(w13, "w13", dev)
+    _need(w2, "w2", dev)
+    scale_type = torch.float32 if fp8 else torch.uint8
+    if not fp8 and (s13.dtype != torch.uint8 or s2.dtype != torch.uint8):
+        s13, s2 = _bytes(s13), _bytes(s2)
+    _typed(s13, "w13_scale", scale_type, (E, 2 * I, -(-K // block_size)), dev)
+    _typed(s2, "w2_scale", scale_type, (E, K, -(-I // block_size)), dev)
+    if not fp8:
+        _typed(g13, "w13_scale_2", torch.float32, (E,), dev)
+        _typed(g2, "w2_scale_2", torch.float32, (E,), dev)
+    if workspace is None:
+        need = fp4w_moe_workspace(M, topk, K, I)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", dev)
+    if out is None:
+        out = torch.empty_like(A)
+    else:
+        _like(out, "out", A, A.shape)
+    args = [A.data_ptr(), M, K, ids.data_ptr(), weights.data_ptr(), topk, w13.data_ptr(), s13.data_ptr()]
+    if not fp8:
+        args.append(g13.data_ptr())
+    args += [w2.data_ptr(), s2.data_ptr()]
+    if not fp8:
+        args.append(g2.data_ptr())
+    args += [E, I, block_size, ACTIVATIONS[activation], workspace.data_ptr(),
+             workspace.numel() * workspace.element_size(), out.data_ptr(), code]
+    f = lib.fp8w_moe_ex if fp8 else lib.fp4w_moe_ex
+    _call(dev, lambda *a: f(*a, path), what, *args)
+    return out
+
+
+def fp4w_moe(A: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torch.Tensor, w13_scale: torch.Tensor,
+             w13_scale_2: torch.Tensor, w2: torch.Tensor, w2_scale: torch.Tensor, w2_scale_2: torch.Tensor,
+             block_size: int = 16, activation: str = "silu", out: torch.Tensor = None,
+             workspace: torch.Tensor = None, path: int = PATH_AUTO) -> torch.Tensor:
+    """A whole mixture-of-experts layer on FP4 weights, for a few tokens: for
+    each token the sum over its choices j, e = ids[..., j], of
+
+        weights[..., j] * ((act(A w13[e, :I]^T) * (A w13[e, I:]^T)) w2[e]^T)
+
+    ``ids`` int32 and ``weights`` float32 are [..., topk] with A's leading
+    dimensions (fp4w_moe_route's outputs); an id outside [0, E) contributes
+    nothing.  ``w13`` [E, 2 I, K/2], ``w2`` [E, K, I/2] packed E2M1 with E4M3
+    scales per block and one float32 scale per expert.  ``workspace`` holds
+    ``fp4w_moe_workspace(M, topk, K, I)`` bytes; it is allocated here when not
+    given."""
+    return _moe(False, A, ids, weights, w13, w13_scale, w13_scale_2, w2, w2_scale, w2_scale_2, block_size, activation,
+                out, workspace, path)
+
+
+def fp8w_moe(A: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: torch.Tensor, w13_scale: torch.Tensor,
+             w2: torch.Tensor, w2_scale: torch.Tensor, block_size: int = 128, activation: str = "silu",
+             out: torch.Tensor = None, workspace: torch.Tensor = None, path: int = PATH_AUTO) -> torch.Tensor:
+    """fp4w_moe on FP8 weights: ``w13`` E4M3 [E, 2 I, K], ``w2`` [E, K, I],
+    float32 scales per ``block_size`` values of a row."""
+    return _moe(True, A, ids, weights, w13, w13_scale, None, w2, w2_scale, None, block_size, activation, out,
+                workspace, path)

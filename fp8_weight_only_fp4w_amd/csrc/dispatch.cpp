@@ -11,34 +11,21 @@
 #include <stdint.h>
 
 #include "../../include/fp4w.h"
+#include "arg_checks.h"
 #include "launch.h"
 
 namespace {
 
 using fp4w::Act;
+using fp4w::aligned;
+using fp4w::ceil_div;
 using fp4w::DequantArgs;
 using fp4w::Fp8DequantArgs;
 using fp4w::MatmulArgs;
+using fp4w::mul_ok;
 using fp4w::Nvfp4Args;
+using fp4w::overlaps;
 using fp4w::QdqArgs;
-
-// Element counts (M * K, N * K, M * N, N * scale_cols) are capped at 2^60, so
-// every byte count derived from them (at most 4 bytes per element) stays
-// below 2^63.
-constexpr int64_t kMaxElems = int64_t(1) << 60;
-
-bool mul_ok(int64_t a, int64_t b) { return a == 0 || b <= kMaxElems / a; }
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
-
-// [lo, lo + bytes) and [lo2, lo2 + bytes2) overlap?
-bool overlaps(const void* a, int64_t abytes, const void* b, int64_t bbytes) {
-  if (a == nullptr || b == nullptr || abytes <= 0 || bbytes <= 0) return false;
-  uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + static_cast<uintptr_t>(bbytes) && b0 < a0 + static_cast<uintptr_t>(abytes);
-}
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Shape rules shared by every op.  Returns FP4W_OK or an error status.
 int check_shape(int op, int64_t M, int64_t N, int64_t K, int64_t bs, int64_t cols) {
@@ -542,8 +529,8 @@ const char* fp4w_status_string(int status) {
   switch (status) {
     case FP4W_OK: return "ok";
     case FP4W_ERR_NULL: return "a required pointer is NULL";
-    case FP4W_ERR_SHAPE: return "invalid shape (negative size, odd K for FP4, bad scale_cols or overflow)";
-    case FP4W_ERR_DTYPE: return "dtype must be FP4W_F16 or FP4W_BF16";
+    case FP4W_ERR_SHAPE: return "invalid shape (negative size, odd K for FP4, bad scale_cols, a size past its limit or overflow)";
+    case FP4W_ERR_DTYPE: return "dtype must be FP4W_F16 or FP4W_BF16 (or the activation or score is unknown)";
     case FP4W_ERR_BLOCK: return "block_size must be >= 1";
     case FP4W_ERR_PATH: return "the requested kernel path does not apply to these arguments";
     case FP4W_ERR_LAUNCH: return "HIP reported an error when enqueuing the kernel";
@@ -572,6 +559,8 @@ const char* fp4w_path_name(int path) {
     case FP4W_PATH_FP8_DEQUANT_GENERIC: return "fp8_dequant_generic";
     case FP4W_PATH_NVFP4_VEC: return "nvfp4_vec";
     case FP4W_PATH_NVFP4_GENERIC: return "nvfp4_generic";
+    case FP4W_PATH_MOE_FP4_GENERIC: return "moe_fp4_generic";
+    case FP4W_PATH_MOE_FP8_GENERIC: return "moe_fp8_generic";
     default: return "unknown";
   }
 }

@@ -66,6 +66,57 @@ struct Nvfp4Args {
   void* stream;
 };
 
+// Norms around a block with its gate and residual (fp4w_block_norm); absent
+// parts are null.  gate_rows is 1 (one row for all) or M.
+struct BlockNormArgs {
+  const void* x;
+  const void* post_weight;
+  const void* gate;
+  const void* residual;
+  const void* pre_weight;
+  void* residual_out;
+  void* y;
+  int64_t M, K, gate_rows;
+  float scale, weight_offset, eps;
+  Act act;
+  void* stream;
+};
+
+// Routing of tokens to experts (fp4w_moe_route).  `logits_dtype`: an
+// fp4w_dtype, FP4W_F32 included.
+struct MoeRouteArgs {
+  const void* logits;
+  const float* select_bias;
+  int32_t* ids;
+  float* weights;
+  int64_t M, E, topk;
+  bool sigmoid, renormalize;
+  float scale;
+  int logits_dtype;
+  void* stream;
+};
+
+// One mixture-of-experts layer after validation (fp4w_moe, fp8w_moe).
+// s13 / s2: E4M3 bytes (FP4) or floats (FP8); g13 / g2: FP32 per expert (FP4
+// only).  `work` holds fp4w_moe_workspace() bytes.
+struct MoeArgs {
+  const void* A;
+  const int32_t* ids;
+  const float* weights;
+  const uint8_t* w13;
+  const void* s13;
+  const float* g13;
+  const uint8_t* w2;
+  const void* s2;
+  const float* g2;
+  void* work;
+  void* Y;
+  int64_t M, K, topk, E, I, block_size;
+  int activation;
+  Act act;
+  void* stream;
+};
+
 // Each launcher enqueues its kernel(s) and returns 0, or -1 when HIP reports
 // an error at enqueue time.  Preconditions (checked by the dispatcher, never
 // by the launcher) are stated next to each.
@@ -149,5 +200,15 @@ int launch_nvfp4_qdq(const Nvfp4Args& a, bool vec);
 // provide it.
 constexpr int64_t kStaticScratchBytes = int64_t(32) << 20;
 int static_scratch(void** out);
+
+// M, K > 0.  vec: K % 8 == 0 and every pointer 16-byte aligned.
+int launch_block_norm(const BlockNormArgs& a, bool vec);
+
+// M, topk > 0, topk <= 64, E <= 1024.
+int launch_moe_route(const MoeRouteArgs& a);
+
+// any validated arguments with M, K > 0 (E, topk and I may be 0)
+int launch_moe_fp4_generic(const MoeArgs& a);
+int launch_moe_fp8_generic(const MoeArgs& a);
 
 }  // namespace fp4w

@@ -45,13 +45,14 @@
 extern "C" {
 #endif
 
-typedef enum { FP4W_F16 = 0, FP4W_BF16 = 1 } fp4w_dtype;
+/* FP4W_F32 is only a type of router logits (fp4w_moe_route). */
+typedef enum { FP4W_F16 = 0, FP4W_BF16 = 1, FP4W_F32 = 2 } fp4w_dtype;
 
 typedef enum {
   FP4W_OK = 0,
   FP4W_ERR_NULL = -1,   /* a required pointer is NULL */
   FP4W_ERR_SHAPE = -2,  /* negative size, odd K for FP4, bad scale_cols, size overflow */
-  FP4W_ERR_DTYPE = -3,  /* dtype is not FP4W_F16 / FP4W_BF16 */
+  FP4W_ERR_DTYPE = -3,  /* dtype is not FP4W_F16 / FP4W_BF16 (or an unknown activation or score) */
   FP4W_ERR_BLOCK = -4,  /* block_size < 1 */
   FP4W_ERR_PATH = -5,   /* a forced path (the *_ex calls) does not apply to these arguments */
   FP4W_ERR_LAUNCH = -6, /* HIP reported an error when the kernel was enqueued */
@@ -77,7 +78,9 @@ typedef enum {
   FP4W_PATH_FP8_DEQUANT_VEC = 14,    /* vectorised FP8 dequant: K % 16 == 0, block_size % 16 == 0 */
   FP4W_PATH_FP8_DEQUANT_GENERIC = 15, /* any legal FP8 dequant arguments */
   FP4W_PATH_NVFP4_VEC = 16,     /* NVFP4 activation quantize / QDQ, 16-byte loads (aligned pointers) */
-  FP4W_PATH_NVFP4_GENERIC = 17  /* any legal NVFP4 activation arguments */
+  FP4W_PATH_NVFP4_GENERIC = 17, /* any legal NVFP4 activation arguments */
+  FP4W_PATH_MOE_FP4_GENERIC = 19, /* any legal fp4w_moe arguments */
+  FP4W_PATH_MOE_FP8_GENERIC = 21  /* any legal fp8w_moe arguments */
 } fp4w_path;
 
 /* Operation selector for fp4w_select_path. */
@@ -317,6 +320,145 @@ int fp8w_matmul_w8a8(const void* A, int64_t M, int64_t K, const uint8_t* B, int6
                      const float* b_scale, int64_t scale_cols, int64_t block_size,
                      const float* a_scale, const void* bias, void* A_work, void* Y, int dtype,
                      void* stream);
+
+/* ------------------------------------------------------------------------
+ * Around a mixture-of-experts block: the norm between blocks, the routing of
+ * tokens to experts, and the expert layer on FP4 or FP8 weights.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * fp4w_block_norm - the norms after one block and before the next, with the
+ * block's gate and the residual scale, in one pass over x:
+ *   b = x                                                       (post_weight NULL)
+ *     = x * rsqrt(mean(x^2) + eps) * (weight_offset + post_weight)
+ *   r = residual + scale * gate * b                             (residual_out)
+ *   y = r * rsqrt(mean(r^2) + eps) * (weight_offset + pre_weight)
+ * Means are over a row's K values.  Everything is FP32; residual_out and y
+ * are each rounded once, y from the unrounded r.
+ *
+ *   x             T[M, K]: a block's output (or, alone, an embedding).
+ *   post_weight   T[K] or NULL: no norm of x.
+ *   gate          T[gate_rows, K] or NULL (a gate of one); gate_rows is 1
+ *                 (one row for every token) or M.
+ *   residual      T[M, K] or NULL (zero).
+ *   pre_weight    T[K]; NULL exactly when y is NULL.
+ *   residual_out  T[M, K] (written) or NULL; not NULL together with y.
+ *   y             T[M, K] (written) or NULL.
+ * residual_out == x, residual_out == residual, y == x and y == residual are
+ * allowed (in place); any other overlap is FP4W_ERR_ALIAS.  M == 0 or K == 0:
+ * FP4W_OK, nothing launched.  Errors: FP4W_ERR_NULL, FP4W_ERR_SHAPE,
+ * FP4W_ERR_DTYPE, FP4W_ERR_ALIAS, FP4W_ERR_LAUNCH.
+ */
+int fp4w_block_norm(const void* x, int64_t M, int64_t K, const void* post_weight, const void* gate,
+                    int64_t gate_rows, float scale, const void* residual, const void* pre_weight,
+                    float weight_offset, float eps, void* residual_out, void* y, int dtype,
+                    void* stream);
+
+#define FP4W_MOE_MAX_EXPERTS 1024
+#define FP4W_MOE_MAX_TOPK 64
+#define FP4W_MOE_MAX_ASSIGNMENTS 4096 /* M * topk of one fp4w_moe / fp8w_moe call */
+
+typedef enum { FP4W_SCORE_SOFTMAX = 0, FP4W_SCORE_SIGMOID = 1 } fp4w_score;
+typedef enum { FP4W_ACT_SILU = 0, FP4W_ACT_GELU_TANH = 1 } fp4w_activation;
+
+/*
+ * fp4w_moe_route - the experts of each token and their weights:
+ *   score   = softmax(logits) over the E experts, or sigmoid(logits)
+ *   key     = logits (select_bias NULL), or score + select_bias in FP64
+ *   ids     = the topk largest keys in falling order, ties to the lowest index
+ *   weights = scale * score[ids], divided by the sum of the topk scores when
+ *             `renormalize` is nonzero (0 where that sum is 0)
+ * The bias only takes part in the choice.  An expert whose logit or key is
+ * -inf or NaN is masked: it is never chosen (and adds nothing to a softmax).  Places that
+ * no expert is left for get id -1 and weight 0, which fp4w_moe skips; a row
+ * with every expert masked is all such places.  Logits of +inf share the
+ * softmax among themselves.
+ *
+ *   logits       logits_dtype[M, E]: FP4W_F16, FP4W_BF16 or FP4W_F32.
+ *   select_bias  float[E] or NULL.
+ *   ids          int32[M, topk] (written).   weights  float[M, topk] (written).
+ * E <= FP4W_MOE_MAX_EXPERTS and topk <= FP4W_MOE_MAX_TOPK (topk > E is
+ * legal).  M is not limited.  M == 0 or topk == 0: FP4W_OK, nothing launched.
+ * Errors: FP4W_ERR_NULL, FP4W_ERR_SHAPE, FP4W_ERR_DTYPE (an unknown type or
+ * score), FP4W_ERR_ALIAS, FP4W_ERR_LAUNCH.
+ */
+int fp4w_moe_route(const void* logits, int64_t M, int64_t E, int64_t topk, int score,
+                   const float* select_bias, int renormalize, float scale, int32_t* ids,
+                   float* weights, int logits_dtype, void* stream);
+
+/*
+ * Bytes of caller-owned workspace that fp4w_moe and fp8w_moe need for these
+ * sizes, or a negative fp4w_status for illegal ones.  Host-only.
+ */
+int64_t fp4w_moe_workspace(int64_t M, int64_t topk, int64_t K, int64_t I);
+
+/*
+ * fp4w_moe - a whole mixture-of-experts layer on FP4 weights, for a few
+ * tokens (decode, small batches).  With e = ids[m, j] and W1[e], W3[e] the
+ * first and last I rows of w13[e]:
+ *   h    = act(A[m] . W1[e]^T) * (A[m] . W3[e]^T)
+ *   Y[m] = sum_j weights[m, j] * (h . W2[e]^T)
+ *   act  = silu(g) = g / (1 + exp(-g)), or gelu in its tanh form
+ * Weights are those of fp4w_matmul: e2m1 * e4m3(block of block_size k) *
+ * scale_2 of the expert.  An id outside [0, E) contributes nothing (a masked
+ * or absent choice, an expert on another device); a token without any gets
+ * zeros.  A token may name an expert twice: both count.  Accumulation is
+ * FP32, h is kept to 16 significand bits at least, and Y is rounded once; the
+ * result for a token does not depend on the order in which the GPU works.
+ *
+ *   A            T[M, K]
+ *   ids          int32[M, topk]    weights  float[M, topk]
+ *   w13          uint8[E, 2 I, K/2]; gate rows, then up rows.
+ *   w13_scale    uint8[E, 2 I, ceil(K / block_size)]: E4M3 bytes.
+ *   w13_scale_2  float[E] (device)
+ *   w2           uint8[E, K, I/2]
+ *   w2_scale     uint8[E, K, ceil(I / block_size)]
+ *   w2_scale_2   float[E] (device)
+ *   workspace    at least fp4w_moe_workspace(M, topk, K, I) bytes, 4-byte
+ *                aligned; what it holds before does not matter.  Calls that
+ *                may run at once (two streams, two replayed graphs) need
+ *                one each.
+ *   Y            T[M, K] (written).
+ * K and I must be even, E <= FP4W_MOE_MAX_EXPERTS, topk <= FP4W_MOE_MAX_TOPK
+ * and M * topk <= FP4W_MOE_MAX_ASSIGNMENTS.  M == 0 or K == 0: FP4W_OK,
+ * nothing launched.  topk == 0, E == 0 or I == 0: Y = 0 (an empty sum).
+ * Errors: FP4W_ERR_NULL, FP4W_ERR_SHAPE (also a workspace that is too small
+ * or unaligned), FP4W_ERR_BLOCK, FP4W_ERR_DTYPE (also an unknown activation),
+ * FP4W_ERR_ALIAS (Y or the workspace overlaps an input or the other),
+ * FP4W_ERR_LAUNCH.
+ */
+int fp4w_moe(const void* A, int64_t M, int64_t K, const int32_t* ids, const float* weights,
+             int64_t topk, const uint8_t* w13, const uint8_t* w13_scale, const float* w13_scale_2,
+             const uint8_t* w2, const uint8_t* w2_scale, const float* w2_scale_2, int64_t E,
+             int64_t I, int64_t block_size, int activation, void* workspace,
+             int64_t workspace_bytes, void* Y, int dtype, void* stream);
+
+/* Path-forcing variant (FP4W_PATH_AUTO, _MOE_FP4_GENERIC). */
+int fp4w_moe_ex(const void* A, int64_t M, int64_t K, const int32_t* ids, const float* weights,
+                int64_t topk, const uint8_t* w13, const uint8_t* w13_scale,
+                const float* w13_scale_2, const uint8_t* w2, const uint8_t* w2_scale,
+                const float* w2_scale_2, int64_t E, int64_t I, int64_t block_size, int activation,
+                void* workspace, int64_t workspace_bytes, void* Y, int dtype, void* stream,
+                int path);
+
+/*
+ * fp8w_moe - the same layer on FP8 weights as fp8w_matmul takes them: E4M3
+ * bytes with FP32 scales per block_size k of a row.
+ *   w13  uint8[E, 2 I, K]    w13_scale  float[E, 2 I, ceil(K / block_size)]
+ *   w2   uint8[E, K, I]      w2_scale   float[E, K, ceil(I / block_size)]
+ * Other arguments, results and errors as fp4w_moe (K and I may be odd).
+ */
+int fp8w_moe(const void* A, int64_t M, int64_t K, const int32_t* ids, const float* weights,
+             int64_t topk, const uint8_t* w13, const float* w13_scale, const uint8_t* w2,
+             const float* w2_scale, int64_t E, int64_t I, int64_t block_size, int activation,
+             void* workspace, int64_t workspace_bytes, void* Y, int dtype, void* stream);
+
+/* Path-forcing variant (FP4W_PATH_AUTO, _MOE_FP8_GENERIC). */
+int fp8w_moe_ex(const void* A, int64_t M, int64_t K, const int32_t* ids, const float* weights,
+                int64_t topk, const uint8_t* w13, const float* w13_scale, const uint8_t* w2,
+                const float* w2_scale, int64_t E, int64_t I, int64_t block_size, int activation,
+                void* workspace, int64_t workspace_bytes, void* Y, int dtype, void* stream,
+                int path);
 
 /*
  * fp4w_select_path - the path FP4W_PATH_AUTO takes for these sizes, assuming

@@ -1,0 +1,273 @@
+"""fp4w_moe and fp8w_moe on the GPU against the oracle's float64 and its bound."""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_weight_only_fp4w_amd as fw
+from gpu_helpers import require_gpu
+from moe_cases import assert_within, make_moe, moe_call, moe_on, moe_want, rounded
+from oracle import moe as om
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = [False, True]
+GENERIC = {False: fw.PATH_MOE_FP4_GENERIC, True: fw.PATH_MOE_FP8_GENERIC}
+ids_of = lambda c: "x".join(map(str, c))  # noqa: E731
+
+# M, K, I, E, topk: sizes that fill tiles, end inside them, one token and
+# many, one expert, more choices than experts
+SIZES = [
+    (1, 128, 128, 4, 2), (1, 64, 64, 1, 1), (1, 2048, 768, 16, 8), (2, 192, 320, 3, 3), (3, 256, 64, 8, 2),
+    (5, 320, 192, 8, 6), (4, 1024, 512, 2, 1), (7, 128, 1408, 6, 4), (16, 512, 256, 4, 2), (17, 256, 448, 1, 1),
+    (33, 448, 128, 4, 3), (64, 256, 192, 16, 8), (100, 192, 128, 5, 2), (130, 128, 64, 3, 1), (9, 64, 128, 40, 20),
+]
+# sizes that only the generic kernels take
+ODD = [(1, 2, 2, 1, 1, 16), (3, 30, 22, 4, 2, 15), (2, 66, 34, 3, 2, 16), (5, 96, 40, 4, 3, 32), (2, 256, 128, 4, 2, 24)]
+
+
+def run(c, act="silu", **kw):
+    return moe_call(fw, c, moe_on(c), act, **kw)
+
+
+@pytest.mark.parametrize("path", ["auto", "generic"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+@pytest.mark.parametrize("size", SIZES, ids=ids_of)
+def test_against_oracle(size, fp8, dtype, path):
+    require_gpu()
+    M, K, I, E, topk = size  # noqa: E741
+    c = make_moe(fp8, M, K, I, E, topk, dtype, seed=M + K + I, masked=0.1 if M > 2 else 0.0)
+    act = "gelu" if (M + I) % 3 == 0 else "silu"
+    Y = run(c, act, path=GENERIC[fp8] if path == "generic" else fw.PATH_AUTO)
+    want, tol = moe_want(c, act)
+    assert_within(Y, want, tol, dtype, f"{size}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+@pytest.mark.parametrize("size", ODD, ids=ids_of)
+def test_odd_sizes_and_blocks(size, fp8, dtype):
+    require_gpu()
+    M, K, I, E, topk, bs = size  # noqa: E741
+    if fp8:
+        K, I = K + 1, I + 1  # noqa: E741
+    c = make_moe(fp8, M, K, I, E, topk, dtype, seed=K, block_size=bs)
+    want, tol = moe_want(c)
+    assert_within(run(c), want, tol, dtype, f"{size}")
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+def test_masked_rows_repeated_and_foreign_ids(fp8):
+    """Rows without any valid id give zeros; an expert named twice counts twice; ids past E and below 0 are skipped."""
+    require_gpu()
+    c = make_moe(fp8, 6, 256, 128, 5, 4, "bf16", 11)
+    c["ids"][:] = [[-1, -1, -1, -1], [2, 2, 2, 2], [5, 1000, -7, 2 ** 31 - 1], [0, 5, -2 ** 31, 0], [4, 3, 2, 1],
+                   [3, -1, 3, 9]]
+    want, tol = moe_want(c)
+    for path in (fw.PATH_AUTO, GENERIC[fp8]):
+        Y = run(c, path=path)
+        assert (Y[0] == 0).all() and (Y[2] == 0).all()
+        assert_within(Y, want, tol, "bf16")
+    c["ids"][:] = -1
+    assert (run(c) == 0).all()
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+def test_all_tokens_to_one_expert(fp8):
+    require_gpu()
+    for M in (16, 17, 40, 100):
+        c = make_moe(fp8, M, 256, 192, 6, 2, "fp16", 12 + M)
+        c["ids"][:, 0] = 4
+        c["ids"][:, 1] = -1
+        want, tol = moe_want(c)
+        assert_within(run(c), want, tol, "fp16", f"M {M}")
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+def test_empty(fp8):
+    require_gpu()
+    for M, K, I, E, topk in ((0, 128, 64, 4, 2), (3, 0, 64, 4, 2), (3, 128, 0, 4, 2), (3, 128, 64, 0, 2), (3, 128, 64, 4, 0)):  # noqa: E741
+        c = make_moe(fp8, M, K, I, E, topk, "bf16", 1)
+        out = torch.full((M, K), 5.0, dtype=torch.bfloat16, device="cuda")
+        run(c, out=out)
+        assert (out == 0).all()
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+def test_nan_and_infinity_stay_with_their_token_and_expert(fp8):
+    require_gpu()
+    c = make_moe(fp8, 5, 192, 192, 4, 1, "bf16", 13)
+    c["ids"][:, 0] = [0, 1, 1, 2, 3]
+    c["A"][2, 5] = float("nan")
+    c["A"][3, 100] = float("inf")
+    c["A64"] = c["A"].double().numpy()
+    if fp8:
+        c["w2"][3, 7, 11] = 0x7F      # one weight: one column of token 4
+        bad = [7]
+    else:
+        c["s2"][3, 7, -1] = 0x7F      # the row's last block
+        bad = [7]
+    with np.errstate(all="ignore"):
+        want, tol = moe_want(c)
+    Y = run(c).cpu()
+    assert Y[2].isnan().all() and not Y[3].isfinite().any()
+    assert [i for i in range(192) if Y[4, i].isnan()] == bad
+    keep = [0, 1]
+    assert_within(Y[keep], want[keep], tol[keep], "bf16")
+    cols = [i for i in range(192) if i not in bad]
+    assert_within(Y[4:5, cols], want[4:5, cols], tol[4:5, cols], "bf16")
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+def test_large_intermediates_do_not_overflow(fp8):
+    """gate * up past the range of FP16 is an intermediate only: the output is finite."""
+    require_gpu()
+    c = make_moe(fp8, 3, 256, 128, 2, 1, "fp16", 14, spread=300.0)
+    c["weights"][:] = 2.0 ** -12
+    want, tol = moe_want(c)
+    assert np.abs(want).max() < 60000
+    h = c["A64"][0] @ om.expert_matrix(c["w13"][c["ids"][0, 0]], c["s13"][c["ids"][0, 0]],
+                                       None if fp8 else c["g13"][c["ids"][0, 0]], c["block_size"], fp8).T
+    assert np.abs(h[:128] * h[128:]).max() > 65504
+    assert_within(run(c), want, tol, "fp16")
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+def test_unaligned_pointers(fp8):
+    """Weights, activations and scales that start anywhere, and nothing written outside Y."""
+    require_gpu()
+    c = make_moe(fp8, 3, 128, 128, 4, 2, "bf16", 15)
+    d = moe_on(c)
+
+    def shifted(t, by):
+        room = torch.empty(t.numel() + by + 8, dtype=t.dtype, device="cuda")
+        return room[by:by + t.numel()].view(t.shape).copy_(t)
+
+    want, tol = moe_want(c)
+    for name, by in (("A", 1), ("w13", 1), ("w2", 3), ("s13", 1), ("s2", 1), ("ids", 1), ("weights", 3)):
+        Y = moe_call(fw, c, dict(d, **{name: shifted(d[name], by)}))
+        assert_within(Y, want, tol, "bf16", name)
+    room = torch.full((5 * 128 + 1,), 9.0, dtype=torch.bfloat16, device="cuda")
+    moe_call(fw, c, d, out=room[1:1 + 3 * 128].view(3, 128))
+    assert_within(room[1:1 + 3 * 128].view(3, 128), want, tol, "bf16")
+    assert room[0] == 9 and (room[1 + 3 * 128:] == 9).all()
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+def test_same_bits_again_whatever_the_workspace_held(fp8):
+    require_gpu()
+    c = make_moe(fp8, 24, 512, 320, 12, 4, "bf16", 16)
+    d = moe_on(c)
+    need = fw.fp4w_moe_workspace(24, 4, 512, 320)
+    first = moe_call(fw, c, d)
+    for fill in (0, 0x7F, 0xFF):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        assert torch.equal(moe_call(fw, c, d, workspace=ws).view(torch.int16), first.view(torch.int16))
+    with pytest.raises(fw.FP4WError):
+        moe_call(fw, c, d, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+def test_two_streams_at_once(fp8):
+    require_gpu()
+    cs = [make_moe(fp8, M, 512, 256, 8, 4, "bf16", 17 + M) for M in (4, 30)]
+    ds = [moe_on(c) for c in cs]
+    alone = [moe_call(fw, c, d) for c, d in zip(cs, ds)]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(moe_call(fw, cs[i], ds[i]))
+    torch.cuda.synchronize()
+    for a, got in zip(alone, outs):
+        assert all(torch.equal(a, y) for y in got)
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+def test_captured_and_replayed_with_other_routings(fp8):
+    """A graph that was captured with one routing serves every other: nothing of the ids is kept on the host."""
+    require_gpu()
+    c = make_moe(fp8, 8, 256, 192, 16, 4, "bf16", 18)
+    d = moe_on(c)
+    ws = torch.empty(fw.fp4w_moe_workspace(8, 4, 256, 192), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(d["A"])
+    moe_call(fw, c, d, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moe_call(fw, c, d, out=out, workspace=ws)
+    rng = np.random.default_rng(19)
+    for k in range(5):
+        c["ids"] = rng.integers(-1, 16, (8, 4)).astype(np.int32) if k != 3 else np.full((8, 4), 5, np.int32)
+        d["ids"].copy_(torch.from_numpy(c["ids"]))
+        out.fill_(3.0)
+        g.replay()
+        torch.cuda.synchronize()
+        eager = moe_call(fw, c, d)
+        assert torch.equal(out.view(torch.int16), eager.view(torch.int16)), k
+        want, tol = moe_want(c)
+        assert_within(out, want, tol, "bf16", f"replay {k}")
+
+
+def test_float8_views_and_leading_dimensions():
+    require_gpu()
+    c = make_moe(True, 6, 128, 64, 4, 2, "bf16", 20)
+    d = moe_on(c)
+    Y = moe_call(fw, c, d)
+    e = dict(d, A=d["A"].view(2, 3, 128), ids=d["ids"].view(2, 3, 2), weights=d["weights"].view(2, 3, 2),
+             w13=d["w13"].view(torch.float8_e4m3fn), w2=d["w2"].view(torch.float8_e4m3fn))
+    assert torch.equal(moe_call(fw, c, e), Y.view(2, 3, 128))
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+def test_a_whole_block(fp8):
+    """Norm, router product, routing, layer and closing norm as a decode step chains them, eagerly and replayed."""
+    require_gpu()
+    M, K, E, topk = 5, 256, 12, 3
+    c = make_moe(fp8, M, K, 192, E, topk, "bf16", 21)
+    d = moe_on(c)
+    rng = np.random.default_rng(22)
+    x64, x = rounded(rng.standard_normal((M, K)), "bf16")
+    pre64, pre = rounded(1 + 0.1 * rng.standard_normal(K), "bf16")
+    post64, post = rounded(1 + 0.1 * rng.standard_normal(K), "bf16")
+    router = torch.from_numpy(rng.standard_normal((E, K)) / 16).float().cuda()
+    x, pre, post = x.cuda(), pre.cuda(), post.cuda()
+    ws = torch.empty(fw.fp4w_moe_workspace(M, topk, K, 192), dtype=torch.uint8, device="cuda")
+
+    def block(x):
+        _, a = fw.fp4w_block_norm(x, pre_weight=pre, write_residual=False)
+        logits = a.float() @ router.t()
+        ids, w = fw.fp4w_moe_route(logits, topk)
+        y = moe_call(fw, c, dict(d, A=a, ids=ids, weights=w), workspace=ws)
+        r, nxt = fw.fp4w_block_norm(y, residual=x, pre_weight=pre, post_weight=post, scale=0.5)
+        return a, logits, ids, w, y, r, nxt
+
+    a, logits, ids, w, y, r, nxt = block(x)
+    # each step against the oracle on the step's own inputs
+    _, want, _, tol = om.block_norm(x64, None, pre64)
+    assert_within(a, want, tol, "bf16", "norm")
+    want_ids, want_w, rel = om.route(logits.cpu().double().numpy(), topk)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    assert (np.abs(w.cpu().double().numpy() - want_w) <= rel * want_w).all()
+    c.update(A64=a.cpu().double().numpy(), ids=ids.cpu().numpy(), weights=w.cpu().numpy())
+    want, tol = moe_want(c)
+    assert_within(y, want, tol, "bf16", "layer")
+    wr, wy, tr, ty = om.block_norm(y.cpu().double().numpy(), x64, pre64, post64, None, 0.5)
+    assert_within(r, wr, tr, "bf16", "residual")
+    assert_within(nxt, wy, ty, "bf16", "next norm")
+
+    xs = x.clone()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        kept = block(xs)
+    for k in range(3):
+        xs.copy_(torch.roll(x, k, 0))
+        g.replay()
+        torch.cuda.synchronize()
+        again = block(xs)
+        for p, q in zip(kept, again):
+            assert torch.equal(p, q), k
