@@ -61,7 +61,7 @@ PATH_QDQ_VEC, PATH_QDQ_GENERIC = 10, 11
 PATH_FP4_SKINNY, PATH_FP8_SKINNY = 12, 13
 PATH_FP8_DEQUANT_VEC, PATH_FP8_DEQUANT_GENERIC = 14, 15
 PATH_NVFP4_VEC, PATH_NVFP4_GENERIC = 16, 17
-PATH_MOE_FP4_GENERIC, PATH_MOE_FP8_GENERIC = 19, 21
+PATH_MOE_FP4_STREAM, PATH_MOE_FP4_GENERIC, PATH_MOE_FP8_STREAM, PATH_MOE_FP8_GENERIC = 18, 19, 20, 21
 # operations (fp4w_op)
 OP_FP4_MATMUL, OP_FP8_MATMUL, OP_FP4_DEQUANT, OP_FP8_QDQ, OP_FP8_DEQUANT, OP_NVFP4_ACT = 0, 1, 2, 3, 4, 5
 # dtypes (fp4w_dtype)

@@ -559,7 +559,9 @@ const char* fp4w_path_name(int path) {
     case FP4W_PATH_FP8_DEQUANT_GENERIC: return "fp8_dequant_generic";
     case FP4W_PATH_NVFP4_VEC: return "nvfp4_vec";
     case FP4W_PATH_NVFP4_GENERIC: return "nvfp4_generic";
+    case FP4W_PATH_MOE_FP4_STREAM: return "moe_fp4_stream";
     case FP4W_PATH_MOE_FP4_GENERIC: return "moe_fp4_generic";
+    case FP4W_PATH_MOE_FP8_STREAM: return "moe_fp8_stream";
     case FP4W_PATH_MOE_FP8_GENERIC: return "moe_fp8_generic";
     default: return "unknown";
   }

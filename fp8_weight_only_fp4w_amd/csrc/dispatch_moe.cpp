@@ -40,23 +40,39 @@ int check_moe(bool fp8, int64_t M, int64_t K, int64_t topk, int64_t E, int64_t I
 
 int generic_path(bool fp8) { return fp8 ? FP4W_PATH_MOE_FP8_GENERIC : FP4W_PATH_MOE_FP4_GENERIC; }
 
-int64_t workspace_bytes(int64_t M, int64_t topk, int64_t I) { return align256(M * topk * I * 4); }
+int stream_path(bool fp8) { return fp8 ? FP4W_PATH_MOE_FP8_STREAM : FP4W_PATH_MOE_FP4_STREAM; }
+
+// The streaming kernels: whole 64-k halves of windows, FP4 blocks of 16, FP8
+// blocks of whole 128-k windows, and 32-bit offsets inside A, an expert's
+// matrices and the intermediate.
+bool stream_ok(bool fp8, const MoeArgs& a) {
+  const int64_t n = a.M * a.topk, limit = int64_t(1) << 31;
+  return a.K % 64 == 0 && a.I % 64 == 0 && (fp8 ? a.block_size % 128 == 0 : a.block_size == 16) &&
+         a.M * a.K * 2 < limit && n * a.I * 4 < limit && (2 * a.I + 16) * (a.K + 128) < limit && aligned(a.A, 16) &&
+         aligned(a.w13, 16) && aligned(a.w2, 16) && aligned(a.s13, 4) && aligned(a.s2, 4) && aligned(a.work, 16) &&
+         aligned(a.Y, 16);
+}
+
+// H (4 bytes a value), then the outputs of the single choices in FP32
+int64_t workspace_bytes(int64_t M, int64_t topk, int64_t K, int64_t I) {
+  return align256(M * topk * I * 4) + align256(M * topk * K * 4);
+}
 
 int run_moe(bool fp8, MoeArgs a, int64_t work_bytes, int path) {
   if (!dtype_ok(static_cast<int>(a.act))) return FP4W_ERR_DTYPE;
   if (a.activation != FP4W_ACT_SILU && a.activation != FP4W_ACT_GELU_TANH) return FP4W_ERR_DTYPE;
   const int st = check_moe(fp8, a.M, a.K, a.topk, a.E, a.I, a.block_size);
   if (st != FP4W_OK) return st;
-  if (path != FP4W_PATH_AUTO && path != generic_path(fp8)) return FP4W_ERR_PATH;
+  if (path != FP4W_PATH_AUTO && path != generic_path(fp8) && path != stream_path(fp8)) return FP4W_ERR_PATH;
   if (a.M == 0 || a.K == 0) return FP4W_OK;  // empty output
   // a block longer than either row is one block per row (and column counts cannot overflow)
-  a.block_size = std::min(a.block_size, std::max(a.K, a.I));
+  a.block_size = std::min(a.block_size, ceil_div(std::max(a.K, a.I), 128) * 128);
   if (a.Y == nullptr) return FP4W_ERR_NULL;
   const int64_t n = a.M * a.topk;
   const int64_t ybytes = a.M * a.K * 2, abytes = ybytes;
   if (n > 0 && (a.ids == nullptr || a.weights == nullptr)) return FP4W_ERR_NULL;
   const bool terms = n > 0 && a.E > 0 && a.I > 0;  // there is something to sum
-  const int64_t need = terms ? workspace_bytes(a.M, a.topk, a.I) : 0;
+  const int64_t need = terms ? workspace_bytes(a.M, a.topk, a.K, a.I) : 0;
   if (terms) {
     if (a.A == nullptr || a.w13 == nullptr || a.s13 == nullptr || a.w2 == nullptr || a.s2 == nullptr)
       return FP4W_ERR_NULL;
@@ -82,7 +98,12 @@ int run_moe(bool fp8, MoeArgs a, int64_t work_bytes, int path) {
   for (const auto& in : inputs)
     if (overlaps(a.Y, ybytes, in.p, in.bytes) || overlaps(a.work, need, in.p, in.bytes)) return FP4W_ERR_ALIAS;
   if (overlaps(a.Y, ybytes, a.work, need)) return FP4W_ERR_ALIAS;
-  const int rc = fp8 ? fp4w::launch_moe_fp8_generic(a) : fp4w::launch_moe_fp4_generic(a);
+  const bool fast = terms && stream_ok(fp8, a);
+  if (path == stream_path(fp8) && !fast) return FP4W_ERR_PATH;
+  int rc = 1;  // 1: the streaming kernels do not take the row length
+  if (fast && path != generic_path(fp8)) rc = fp8 ? fp4w::launch_moe_fp8(a) : fp4w::launch_moe_fp4(a);
+  if (rc == 1 && path == stream_path(fp8)) return FP4W_ERR_PATH;
+  if (rc == 1) rc = fp8 ? fp4w::launch_moe_fp8_generic(a) : fp4w::launch_moe_fp4_generic(a);
   return rc == 0 ? FP4W_OK : FP4W_ERR_LAUNCH;
 }
 
@@ -136,7 +157,7 @@ int fp4w_moe_route(const void* logits, int64_t M, int64_t E, int64_t topk, int s
 
 int64_t fp4w_moe_workspace(int64_t M, int64_t topk, int64_t K, int64_t I) {
   const int st = check_moe(true, M, K, topk, 1, I, 1);
-  return st != FP4W_OK ? st : workspace_bytes(M, topk, I);
+  return st != FP4W_OK ? st : workspace_bytes(M, topk, K, I);
 }
 
 int fp4w_moe_ex(const void* A, int64_t M, int64_t K, const int32_t* ids, const float* weights, int64_t topk,

@@ -207,6 +207,13 @@ int launch_block_norm(const BlockNormArgs& a, bool vec);
 // M, topk > 0, topk <= 64, E <= 1024.
 int launch_moe_route(const MoeRouteArgs& a);
 
+// n = M * topk in 1 .. 4096, E in 1 .. 1024, K % 64 == 0, I % 64 == 0 (both >
+// 0), block_size 16 (FP4) or a multiple of 128 (FP8); A, w13, w2, work and Y
+// 16-byte aligned, scales 4-byte; A, an expert's matrices and n x I x 4 below
+// 2^31 bytes.  Return 1, launching nothing, when a token's row does not fit in
+// LDS.
+int launch_moe_fp4(const MoeArgs& a);
+int launch_moe_fp8(const MoeArgs& a);
 // any validated arguments with M, K > 0 (E, topk and I may be 0)
 int launch_moe_fp4_generic(const MoeArgs& a);
 int launch_moe_fp8_generic(const MoeArgs& a);

@@ -1,0 +1,625 @@
+// Mixture-of-experts layer for a few tokens on FP4 or FP8 weights, on MFMA.
+//
+//   H[a, i] = act(A[m] . W1[e][i]) * (A[m] . W3[e][i])      a = m * topk + j, e = ids[a]
+//   Y[m, n] = RNE_T( sum_j weights[a] * (H[a] . W2[e][n]) )
+//
+// Memory-bound: every chosen expert is read once per pass of up to `rows`
+// tokens, in whole 128-byte lines, as the decode GEMV reads a single weight
+// matrix.  Three kernels: up (H from A), down (each choice's output from H)
+// and combine (their weighted sum over a token's choices in the order of j, so
+// the result does not depend on scheduling).
+//
+// Plan.  ids live on the device, so which experts are read is only known
+// there.  Every workgroup of up and down sorts the assignments by expert in
+// LDS (a count, a scan and a scatter over n <= 4096 ids) and cuts each
+// expert's tokens into passes of at most `rows`.  The work is the flat list of
+// (pass, group of column tiles); workgroup b of the persistent grid takes a
+// contiguous share, so it meets few experts.
+//
+// A pass's token rows are copied to LDS once (zero-padded to whole 128-k
+// windows) and shared by the 8 waves: KS waves split the sum of one column
+// tile, 8 / KS tiles run side by side.  A wave streams its weights through a
+// private LDS ring of direct loads, D units of 2 KiB ahead of the multiply
+// (unit: 128 bytes of 16 rows, loaded as two instructions of 8 rows x 128
+// bytes, chunks XOR-swizzled by row), across tiles and passes without a
+// break.  The up kernel's 16 rows are 8 gate rows and the 8 up rows that
+// belong to them, so both halves of a product meet in one tile.
+//
+// Operands (16x16x32 MFMA; lane li = l % 16 is token row for A and weight row
+// for B, lane group g = l / 16 selects 8 of a step's 32 k; the result lane
+// holds column li, token rows 4g .. 4g + 3).
+//  * FP4: E2M1 x E4M3 is exact in FP16 and BF16, so a weight is decoded with
+//    its block scale folded in; the expert's FP32 scale is applied to the sum.
+//  * FP8: E4M3 -> T is exact, a 128-k window (inside one scale block) is summed
+//    in a fresh accumulator and added times its FP32 scale.
+//
+// H is handed from up to down as two BF16 planes, high part and remainder (16
+// significand bits, FP32's exponent range): one BF16 or FP16 rounding of H
+// would double the output's error, and in FP16 gate * up may overflow.  The
+// down kernel runs both planes through the same decoded weights.
+
+#include <hip/hip_runtime.h>
+
+#include <mutex>
+
+#include "device.h"
+#include "launch.h"
+#include "moe_act.h"
+
+namespace fp4w {
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kThreads = 64 * kWaves;
+constexpr uint32_t kUnitBytes = 2048;  // 16 rows x 128 bytes
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __asm__ volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));  // vmcnt(N) only
+  __asm__ volatile("" ::: "memory");
+}
+
+// Barrier for data exchanged by ds_write / ds_read only: direct loads stay in
+// flight.
+__device__ __forceinline__ void lds_barrier() {
+  __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+struct MoeParams {
+  const void* x;        // up: A, T[M, L]; down: H planes, BF16 [2][n][L]
+  const uint8_t* w;     // [E, N, L] codes
+  const uint8_t* s;     // [E, N, cols] scales
+  const float* g;       // FP4: per expert
+  const int32_t* ids;   // [n]
+  void* out;            // up: H planes, BF16 [2][n][I]; down: FP32 [n][K]
+  FastDiv topk, win_per_block, chunks_per_row;  // chunks_per_row: 16-byte chunks of an LDS row
+  int n, E, L, N, cols;
+  int x_bytes;          // up: M * L * 2; down: 2 * n * L * 2
+  int rows;             // tokens per pass
+  int tiles, groups;    // column tiles of an expert, and groups of TPW of them
+  int units;            // per wave and tile
+  int act;
+  int list_max;         // passes at most
+};
+
+// LDS: unit rings, partial sums of the K split, then the plan and the token rows.
+constexpr uint32_t kRedBytes = kWaves * 1024;
+
+struct Plan {
+  const uint32_t* list;    // pass: expert | first sorted assignment << 10 | (tokens - 1) << 22
+  const uint16_t* sorted;  // assignments, by expert
+  int passes;
+};
+// list and multi [list_max], count [E], part [16], sorted and expert [n]
+constexpr uint32_t plan_bytes(int n, int E, int list_max) {
+  return (8u * list_max + 4u * E + 4u * 16u + 4u * n + 15u) & ~15u;
+}
+
+// All threads of the workgroup; `mem` holds plan_bytes().  Every workgroup
+// comes to the same list, and to the same tokens in each pass: an expert with
+// several passes has its assignments in rising order.
+__device__ __forceinline__ Plan make_plan(const MoeParams& p, unsigned char* mem) {
+  uint32_t* list = reinterpret_cast<uint32_t*>(mem);
+  uint32_t* multi = list + p.list_max;  // experts of several passes: expert | first sorted assignment << 10
+  uint32_t* count = multi + p.list_max;
+  uint32_t* part = count + p.E;
+  uint16_t* sorted = reinterpret_cast<uint16_t*>(part + 16);
+  uint16_t* expert = sorted + p.n;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int e = tid; e < p.E; e += kThreads) count[e] = 0;
+  if (tid == 0) part[8] = 0;
+  __syncthreads();
+  for (int a = tid; a < p.n; a += kThreads) {
+    const uint32_t e = static_cast<uint32_t>(p.ids[a]);
+    const bool valid = e < static_cast<uint32_t>(p.E);
+    expert[a] = static_cast<uint16_t>(valid ? e : 0xFFFFu);
+    if (valid) atomicAdd(&count[e], 1u);
+  }
+  __syncthreads();
+  // experts 2 tid and 2 tid + 1 (E <= 1024): tokens in the low half, passes in the high half
+  uint32_t c[2], v[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    c[i] = 2 * tid + i < p.E ? count[2 * tid + i] : 0u;
+    v[i] = c[i] | ((c[i] + p.rows - 1) / p.rows) << 16;
+  }
+  uint32_t sum = v[0] + v[1];
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = __shfl_up(sum, d, 64);
+    if (lane >= d) sum += o;
+  }
+  if (lane == 63) part[wave] = sum;
+  __syncthreads();
+  uint32_t before = sum - v[0] - v[1], total = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    const uint32_t t = part[i];
+    if (i < wave) before += t;
+    total += t;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t e = 2 * tid + i;
+    if (c[i]) {
+      uint32_t at = before & 0xFFFF, left = c[i], slot = before >> 16;
+      count[e] = at;
+      if (left > static_cast<uint32_t>(p.rows)) multi[atomicAdd(&part[8], 1u)] = e | at << 10;
+      for (; left; ++slot) {
+        const uint32_t t = left < static_cast<uint32_t>(p.rows) ? left : static_cast<uint32_t>(p.rows);
+        list[slot] = e | at << 10 | (t - 1) << 22;
+        at += t;
+        left -= t;
+      }
+    }
+    before += v[i];
+  }
+  __syncthreads();
+  for (int a = tid; a < p.n; a += kThreads) {
+    const uint32_t e = expert[a];
+    if (e != 0xFFFFu) sorted[atomicAdd(&count[e], 1u)] = static_cast<uint16_t>(a);
+  }
+  __syncthreads();
+  // Within an expert that order is the atomics'.  With one pass it only
+  // decides the MFMA row of a token; with several, which pass a token is in,
+  // and there every workgroup has to agree: a wave writes them again in order.
+  const int several = __builtin_amdgcn_readfirstlane(part[8]);
+  for (int i = wave; i < several; i += kWaves) {
+    const uint32_t e = multi[i] & 1023u;
+    uint32_t at = multi[i] >> 10;
+    for (int a0 = 0; a0 < p.n; a0 += 64) {
+      const bool mine = a0 + lane < p.n && expert[a0 + lane] == e;
+      const uint64_t m = __ballot(mine);
+      if (mine) sorted[at + __popcll(m & ((uint64_t(1) << lane) - 1))] = static_cast<uint16_t>(a0 + lane);
+      at += __popcll(m);
+    }
+  }
+  if (several) __syncthreads();
+  return Plan{list, sorted, static_cast<int>(total >> 16)};
+}
+
+struct Pass {
+  int expert, first, tokens;
+};
+__device__ __forceinline__ Pass read_pass(const uint32_t* list, int i) {
+  const uint32_t v = __builtin_amdgcn_readfirstlane(list[i]);
+  return Pass{static_cast<int>(v & 1023), static_cast<int>(v >> 10 & 4095), static_cast<int>(v >> 22) + 1};
+}
+
+// value of the lane 8 away in the row of 16
+__device__ __forceinline__ float swap8(float v) {
+  const int i = __builtin_bit_cast(int, v);
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, 0x128, 0xF, 0xF, false));  // row_ror:8
+}
+
+// UP: the first kernel (A of type T against w13), otherwise the second (H
+// planes against w2; its operands are BF16 whatever T is).
+template <typename T, bool FP8, bool UP, int KS, int D>
+__global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
+  typedef typename std::conditional<UP, T, __bf16>::type X;
+  typedef ActTraits<X> Tr;
+  typedef typename Tr::vec8 V;
+  typedef typename std::conditional<FP8, uint32_t, u32x4>::type Scale;
+  constexpr int TPW = kWaves / KS;
+  constexpr int S = D + 1;
+  constexpr int UW = FP8 ? 1 : 2;  // 128-k windows per unit
+  constexpr int PLANES = UP ? 1 : 2;
+  constexpr int LPU = 3;  // loads per unit: scales, then two direct weight loads
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int li = lane & 15, g = lane >> 4;  // fragment side: row li, chunk group g
+  const int lr = lane >> 3, lc = lane & 7;  // load side: row lr of an 8-row half, position lc
+  const int ks = wave % KS, tw = wave / KS;
+  unsigned char* ring = smem + static_cast<uint32_t>(wave) * (S * kUnitBytes);
+  unsigned char* red = smem + kWaves * S * kUnitBytes;
+  unsigned char* plan_mem = red + (KS > 1 ? kRedBytes : 0u);
+  unsigned char* rows_lds = plan_mem + plan_bytes(p.n, p.E, p.list_max);
+  const Plan plan = make_plan(p, plan_mem);
+
+  // this workgroup's share of the flat (pass, group) list
+  const uint64_t all = static_cast<uint64_t>(plan.passes) * static_cast<uint64_t>(p.groups);
+  const int64_t lo = static_cast<int64_t>(all * blockIdx.x / gridDim.x);
+  const int64_t hi = static_cast<int64_t>(all * (blockIdx.x + 1) / gridDim.x);
+  if (lo == hi) return;  // the whole workgroup
+  const int first_pass = static_cast<int>(lo / p.groups);
+  const int first_group = static_cast<int>(lo - static_cast<int64_t>(first_pass) * p.groups);
+  const int64_t total = (hi - lo) * p.units;
+
+  const int NW = (p.L + 127) >> 7;
+  const int NU = (NW + UW - 1) / UW;
+  const uint32_t row_bytes = FP8 ? static_cast<uint32_t>(p.L) : static_cast<uint32_t>(p.L >> 1);
+  const uint32_t srow_bytes = FP8 ? 4u * p.cols : static_cast<uint32_t>(p.cols);
+  const uint32_t half = UP ? static_cast<uint32_t>(p.N >> 1) : 8u;  // weight rows from a tile's first 8 to its last 8
+  const uint32_t tile_rows = UP ? 8u : 16u;
+  const uint32_t pitch = static_cast<uint32_t>(NW) * 256u + 16u;  // LDS bytes of a token row
+  const rsrc_t x_rsrc = make_rsrc(p.x, static_cast<uint32_t>(p.x_bytes));
+  const uint32_t wl = lr * row_bytes + 16u * (lc ^ lr);
+  const uint32_t wl8 = wl + half * row_bytes;
+  const uint32_t sl = (li < 8 ? li : li - 8 + half) * srow_bytes;
+  const int sw = li & 7;
+
+  // ---- load side
+  int l_pass = first_pass, l_group = first_group, l_unit = 0;
+  int l_expert = read_pass(plan.list, l_pass).expert;
+  int64_t l_left = hi - lo;  // groups still to load, the current one included
+  rsrc_t br, sr;
+  auto set_load_tile = [&]() {
+    const int t = l_group * TPW + tw;
+    const bool on = l_left > 0 && t < p.tiles;
+    const int64_t row = static_cast<int64_t>(l_expert) * p.N + static_cast<int64_t>(on ? t : 0) * tile_rows;
+    const uint32_t span = on ? half + 8u : 0u;  // past the last tile or the share: every load reads zeros
+    br = make_rsrc(p.w + row * row_bytes, span * row_bytes);
+    sr = make_rsrc(p.s + row * srow_bytes, span * srow_bytes);
+  };
+  set_load_tile();
+  auto load = [&](Scale& sc, unsigned char* slot) {
+    const int u = ks * p.units + l_unit;
+    const bool ok = u < NU;
+    if constexpr (FP8) {
+      const uint32_t col = min(fdiv(static_cast<uint32_t>(u), p.win_per_block), static_cast<uint32_t>(p.cols - 1));
+      sc = buf_load_b32(sr, ok ? sl + 4u * col : kOutOfRange);
+    } else {
+      sc = buf_load_b128(sr, ok ? sl + 16u * u : kOutOfRange);  // 16 blocks: two windows
+    }
+    const uint32_t ub = 128u * static_cast<uint32_t>(u);
+    buf_load_lds<16>(br, ok ? wl + ub : kOutOfRange, slot);
+    buf_load_lds<16>(br, ok ? wl8 + ub : kOutOfRange, slot + 1024);
+    if (++l_unit == p.units) {
+      l_unit = 0;
+      --l_left;
+      if (++l_group == p.groups) {
+        l_group = 0;
+        ++l_pass;
+        if (l_left > 0) l_expert = read_pass(plan.list, l_pass).expert;
+      }
+      set_load_tile();
+    }
+  };
+
+  // ---- token rows of a pass, by direct loads: LDS chunk q holds row q /
+  // chunks_per_row (down: the high parts of all tokens, then the remainders);
+  // rows' padding and the tail of the last instruction are out-of-range
+  // reads, which write zeros
+  auto fill = [&](const Pass& ps) {
+    const uint32_t cpr = p.chunks_per_row.d;
+    const uint32_t chunks = static_cast<uint32_t>(PLANES * ps.tokens) * cpr;
+    for (uint32_t q0 = 64u * static_cast<uint32_t>(wave); q0 < chunks; q0 += 64u * kWaves) {
+      const uint32_t q = q0 + static_cast<uint32_t>(lane);
+      const uint32_t row = fdiv(q, p.chunks_per_row), col = q - row * cpr;
+      uint32_t src = kOutOfRange;
+      if (q < chunks && col * 8u < static_cast<uint32_t>(p.L)) {
+        uint32_t r;
+        if constexpr (UP) {
+          r = fdiv(plan.sorted[ps.first + row], p.topk);
+        } else {
+          const bool rest = row >= static_cast<uint32_t>(ps.tokens);
+          r = plan.sorted[ps.first + (rest ? row - ps.tokens : row)] + (rest ? static_cast<uint32_t>(p.n) : 0u);
+        }
+        src = r * (2u * p.L) + 16u * col;
+      }
+      buf_load_lds<16>(x_rsrc, src, rows_lds + 16u * q0);
+    }
+  };
+
+  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+  Scale raw[S];
+  int c_pass = first_pass, c_group = first_group, c_unit = 0;
+  // FP4: the expert's FP32 scale (read here, not where a tile ends: a load
+  // there would wait for every weight load before it)
+  auto expert_scale = [&](const Pass& ps) {
+    return FP8 ? 1.0f : __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, p.g[ps.expert])));
+  };
+  Pass ps = read_pass(plan.list, c_pass);
+  float gs = expert_scale(ps);
+  fill(ps);
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(raw[d], ring + d * kUnitBytes);
+  wait_vm<D * LPU>();  // the fill is older
+  __builtin_amdgcn_s_barrier();
+  __asm__ volatile("" ::: "memory");
+
+  auto consume = [&](const Scale& sc, const unsigned char* slot) {
+    const int u = ks * p.units + c_unit;
+    wait_vm<D * LPU>();  // this unit's weights have landed
+    // rows past the pass's tokens repeat the last one; their results are dropped
+    const unsigned char* arow = rows_lds + static_cast<uint32_t>(min(li, ps.tokens - 1)) * pitch;
+    const uint32_t lo_plane = static_cast<uint32_t>(ps.tokens) * pitch;
+    if constexpr (FP8) {
+      if (u < NW) {
+        const unsigned char* q = arow + 256u * u + 32u * g;
+        u32x4 w0 = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * (g ^ sw));
+        u32x4 w1 = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * ((4 + g) ^ sw));
+        // a last window of 64 k: the bytes past the row are the next row's
+        if (128 * u + 64 >= p.L) w1 = u32x4{0u, 0u, 0u, 0u};
+        const V b0 = Tr::decode8_fp8(w0.x, w0.y), b1 = Tr::decode8_fp8(w0.z, w0.w);
+        const V b2 = Tr::decode8_fp8(w1.x, w1.y), b3 = Tr::decode8_fp8(w1.z, w1.w);
+        f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int pl = 0; pl < PLANES; ++pl) {
+          const unsigned char* qp = q + pl * lo_plane;
+          d = Tr::mfma(*reinterpret_cast<const V*>(qp), b0, d);
+          d = Tr::mfma(*reinterpret_cast<const V*>(qp + 16), b1, d);
+          d = Tr::mfma(*reinterpret_cast<const V*>(qp + 128), b2, d);
+          d = Tr::mfma(*reinterpret_cast<const V*>(qp + 144), b3, d);
+        }
+        const float s = __builtin_bit_cast(float, sc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(d[i], s, acc[i]);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int w = 2 * u + h;
+        if (w < NW) {
+          const unsigned char* q = arow + 256u * w + 64u * g;
+          const u32x4 wv = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * ((4 * h + g) ^ sw));
+          // E4M3 scales of the lane's blocks 2g and 2g + 1 of the window;
+          // blocks past the row (the next row's bytes) count as zero
+          const uint32_t s4 = (g & 2) ? sc[2 * h + 1] : sc[2 * h];
+          uint32_t s2 = s4 >> (16 * (g & 1));
+          if (128 * w + 64 >= p.L && g >= 2) s2 = 0;
+          const f32x2 sf = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s2), false);
+          const typename Tr::scale_t sa = Tr::make_scale(sf.x), sb = Tr::make_scale(sf.y);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const V b = Tr::decode8(wv[i], i < 2 ? sa : sb);
+#pragma unroll
+            for (int pl = 0; pl < PLANES; ++pl)
+              acc = Tr::mfma(*reinterpret_cast<const V*>(q + pl * lo_plane + 16 * i), b, acc);
+          }
+        }
+      }
+    }
+    if (++c_unit < p.units) return;
+    // end of a tile: join the K split, then the epilogue
+    c_unit = 0;
+    if (KS > 1) {
+      *reinterpret_cast<f32x4*>(red + wave * 1024 + 16 * lane) = acc;
+      lds_barrier();
+      if (ks == 0) {
+#pragma unroll
+        for (int v = 1; v < KS; ++v) acc += *reinterpret_cast<const f32x4*>(red + (wave + v) * 1024 + 16 * lane);
+      }
+      lds_barrier();
+    }
+    const int t = c_group * TPW + tw;
+    if (ks == 0 && t < p.tiles) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 4 * g + r;
+        if constexpr (UP) {
+          const float up = swap8(acc[r]);
+          if (row < ps.tokens && li < 8) {
+            const size_t at = static_cast<size_t>(plan.sorted[ps.first + row]) * (p.N >> 1) + 8 * t + li;
+            const float h = gated(p.act, acc[r] * gs, up * gs);
+            const __bf16 top = static_cast<__bf16>(h);
+            __bf16* out = static_cast<__bf16*>(p.out);
+            out[at] = top;
+            // the remainder is exact in FP32; where the high part is infinite or NaN it adds nothing
+            const float rest = h - static_cast<float>(top);
+            out[at + static_cast<size_t>(p.n) * (p.N >> 1)] = static_cast<__bf16>(__builtin_isfinite(rest) ? rest : 0.0f);
+          }
+        } else if (row < ps.tokens) {
+          static_cast<float*>(p.out)[static_cast<size_t>(plan.sorted[ps.first + row]) * p.N + 16 * t + li] = acc[r] * gs;
+        }
+      }
+    }
+    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (++c_group == p.groups) {
+      c_group = 0;
+      ++c_pass;
+    }
+  };
+
+  int64_t left = total;
+  for (int64_t f0 = 0; f0 < total; f0 += S) {
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+      load(raw[(u + D) % S], ring + ((u + D) % S) * kUnitBytes);
+      if (left > 0) {  // uniform across the workgroup
+        if (c_unit == 0 && c_group == 0 && c_pass != first_pass) {
+          // the next pass's tokens take the place of the last one's
+          ps = read_pass(plan.list, c_pass);
+          gs = expert_scale(ps);
+          lds_barrier();
+          fill(ps);
+          wait_vm<0>();
+          __builtin_amdgcn_s_barrier();
+          __asm__ volatile("" ::: "memory");
+        }
+        consume(raw[u], ring + u * kUnitBytes);
+        --left;
+      }
+    }
+  }
+  wait_vm<0>();  // loads past the end of the share write zeros to the ring
+}
+
+// Y[m, c .. c + 7] = sum over j of weights[m * topk + j] * P[m * topk + j, c ..], in the order of j
+template <typename T>
+__global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restrict__ P, const int32_t* __restrict__ ids,
+                                                          const float* __restrict__ weights, T* __restrict__ Y, int M, int K, int topk, int E) {
+  const int chunks = K >> 3;
+  const int64_t all = static_cast<int64_t>(M) * chunks;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all; i += 256 * static_cast<int64_t>(gridDim.x)) {
+    const int m = static_cast<int>(i / chunks), c = static_cast<int>(i - static_cast<int64_t>(m) * chunks);
+    float sum[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
+    for (int j = 0; j < topk; ++j) {
+      const int a = m * topk + j;
+      if (static_cast<uint32_t>(ids[a]) >= static_cast<uint32_t>(E)) continue;
+      const f32x4* q = reinterpret_cast<const f32x4*>(P + static_cast<size_t>(a) * K + 8 * c);
+      const f32x4 x = q[0], y = q[1];
+      const float w = weights[a];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sum[k] = fmaf(x[k], w, sum[k]);
+        sum[4 + k] = fmaf(y[k], w, sum[4 + k]);
+      }
+    }
+    typename ActTraits<T>::vec8 r;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = round_to<T>(sum[k]);
+    *reinterpret_cast<typename ActTraits<T>::vec8*>(Y + static_cast<size_t>(m) * K + 8 * c) = r;
+  }
+}
+
+// --------------------------------------------------------------------- launch
+
+constexpr size_t kMaxLds = 160 * 1024;
+
+template <typename T, bool FP8, bool UP, int KS, int D>
+void allow_lds() {
+  static std::once_flag once[kMaxDevices];
+  once_per_device(once, [] {
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&moe_kernel<T, FP8, UP, KS, D>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxLds));
+  });
+}
+
+struct Shape {
+  int rows, depth, ks, grid, units, groups, list_max;
+  size_t lds;
+};
+
+size_t fixed_lds(int depth, int n, int E, int list_max) {
+  return static_cast<size_t>(kWaves) * (depth + 1) * kUnitBytes + kRedBytes + plan_bytes(n, E, list_max);
+}
+
+// Token rows of `planes` planes, in whole direct-load instructions.
+size_t rows_lds_bytes(int rows, int planes, int NW) {
+  return (static_cast<size_t>(rows) * planes * (static_cast<size_t>(NW) * 256 + 16) + 1023) / 1024 * 1024;
+}
+
+// The launch of one kernel: rows per pass, ring depth and K split.  False
+// when not even one token row fits.
+bool plan_shape(const MoeArgs& a, bool fp8, bool up, Shape* out) {
+  const int64_t n = a.M * a.topk;
+  const int64_t L = up ? a.K : a.I;
+  const int NW = static_cast<int>((L + 127) / 128), NU = fp8 ? NW : (NW + 1) / 2;
+  const int planes = up ? 1 : 2;
+  // Tokens per pass: an expert's tokens beyond `rows` read its weights again.
+  // Twice the mean and a few more is rarely exceeded, and every row that is
+  // not reserved leaves LDS to the ring.
+  const int64_t mean = a.E > 0 ? (n + a.E - 1) / a.E : n;
+  int64_t want = 2 * mean + 4;
+  if (want > 16) want = 16;
+  if (want > n) want = n;
+  if (want < 1) want = 1;
+  for (int depth : {4, 2}) {
+    for (int64_t rows = want; rows >= 1; --rows) {
+      if (depth == 4 && rows < want) break;  // a shallower ring before fewer rows
+      const int64_t list_max = (n < a.E ? n : a.E) + n / rows;
+      const size_t lds = fixed_lds(depth, static_cast<int>(n), static_cast<int>(a.E), static_cast<int>(list_max)) +
+                         rows_lds_bytes(static_cast<int>(rows), planes, NW);
+      if (lds > kMaxLds) continue;
+      // K split: least work on the busiest wave, rounds of groups times units
+      // per wave (with what padding a split leaves) and one for a tile's end
+      const int64_t tiles = up ? a.I / 8 : a.K / 16;
+      const int64_t passes = n < a.E ? n : a.E;
+      const int64_t cus = device_cus();
+      int64_t best = -1;
+      for (int ks : {1, 2, 4, 8}) {
+        if (ks > 1 && NU < ks) break;
+        const int64_t groups = (tiles + kWaves / ks - 1) / (kWaves / ks);
+        const int64_t units = (NU + ks - 1) / ks;
+        const int64_t cost = (passes * groups + cus - 1) / cus * (units + 1);
+        if (best < 0 || cost < best) {
+          best = cost;
+          *out = Shape{static_cast<int>(rows), depth, ks, static_cast<int>(passes * groups < cus ? passes * groups : cus),
+                       static_cast<int>(units), static_cast<int>(groups), static_cast<int>(list_max), lds};
+        }
+      }
+      return true;
+    }
+  }
+  return false;
+}
+
+template <typename T, bool FP8, bool UP, int KS, int D>
+void launch_kernel(const MoeParams& p, const Shape& s, hipStream_t st) {
+  allow_lds<T, FP8, UP, KS, D>();
+  hipLaunchKernelGGL((moe_kernel<T, FP8, UP, KS, D>), dim3(s.grid), dim3(kThreads), s.lds, st, p);
+}
+
+template <typename T, bool FP8, bool UP>
+void launch_phase(MoeParams p, const Shape& s, hipStream_t st) {
+  p.rows = s.rows;
+  p.groups = s.groups;
+  p.units = s.units;
+  p.list_max = s.list_max;
+#define FP4W_MOE_KS(KS_) \
+  s.depth == 4 ? launch_kernel<T, FP8, UP, KS_, 4>(p, s, st) : launch_kernel<T, FP8, UP, KS_, 2>(p, s, st)
+  switch (s.ks) {
+    case 1: FP4W_MOE_KS(1); break;
+    case 2: FP4W_MOE_KS(2); break;
+    case 4: FP4W_MOE_KS(4); break;
+    default: FP4W_MOE_KS(8); break;
+  }
+#undef FP4W_MOE_KS
+}
+
+template <typename T, bool FP8>
+int launch_t(const MoeArgs& a) {
+  Shape up, down;
+  if (!plan_shape(a, FP8, true, &up) || !plan_shape(a, FP8, false, &down)) return 1;
+  hipStream_t st = static_cast<hipStream_t>(a.stream);
+  const int64_t n = a.M * a.topk;
+  __bf16* H = static_cast<__bf16*>(a.work);
+  float* P = reinterpret_cast<float*>(static_cast<unsigned char*>(a.work) + (n * a.I * 4 + 255) / 256 * 256);
+  MoeParams p{};
+  p.ids = a.ids;
+  p.topk = make_fastdiv(static_cast<uint32_t>(a.topk));
+  p.win_per_block = make_fastdiv(FP8 ? static_cast<uint32_t>(a.block_size / 128) : 1u);
+  p.n = static_cast<int>(n);
+  p.E = static_cast<int>(a.E);
+  p.act = a.activation;
+  // up
+  p.x = a.A;
+  p.w = a.w13;
+  p.s = static_cast<const uint8_t*>(a.s13);
+  p.g = a.g13;
+  p.out = H;
+  p.L = static_cast<int>(a.K);
+  p.N = static_cast<int>(2 * a.I);
+  p.cols = static_cast<int>((a.K + a.block_size - 1) / a.block_size);
+  p.x_bytes = static_cast<int>(a.M * a.K * 2);
+  p.tiles = static_cast<int>(a.I / 8);
+  p.chunks_per_row = make_fastdiv(static_cast<uint32_t>((a.K + 127) / 128 * 16 + 1));
+  launch_phase<T, FP8, true>(p, up, st);
+  // down
+  p.x = H;
+  p.w = a.w2;
+  p.s = static_cast<const uint8_t*>(a.s2);
+  p.g = a.g2;
+  p.out = P;
+  p.L = static_cast<int>(a.I);
+  p.N = static_cast<int>(a.K);
+  p.cols = static_cast<int>((a.I + a.block_size - 1) / a.block_size);
+  p.x_bytes = static_cast<int>(n * a.I * 4);
+  p.tiles = static_cast<int>(a.K / 16);
+  p.chunks_per_row = make_fastdiv(static_cast<uint32_t>((a.I + 127) / 128 * 16 + 1));
+  launch_phase<__bf16, FP8, false>(p, down, st);
+  // combine
+  const int64_t blocks = (a.M * (a.K / 8) + 255) / 256;
+  hipLaunchKernelGGL(moe_combine_kernel<T>, dim3(static_cast<int>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, P,
+                     a.ids, a.weights, static_cast<T*>(a.Y), static_cast<int>(a.M), static_cast<int>(a.K),
+                     static_cast<int>(a.topk), static_cast<int>(a.E));
+  return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+int launch_moe_fp4(const MoeArgs& a) {
+  return a.act == Act::BF16 ? launch_t<__bf16, false>(a) : launch_t<_Float16, false>(a);
+}
+int launch_moe_fp8(const MoeArgs& a) {
+  return a.act == Act::BF16 ? launch_t<__bf16, true>(a) : launch_t<_Float16, true>(a);
+}
+
+}  // namespace fp4w

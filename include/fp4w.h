@@ -79,7 +79,9 @@ typedef enum {
   FP4W_PATH_FP8_DEQUANT_GENERIC = 15, /* any legal FP8 dequant arguments */
   FP4W_PATH_NVFP4_VEC = 16,     /* NVFP4 activation quantize / QDQ, 16-byte loads (aligned pointers) */
   FP4W_PATH_NVFP4_GENERIC = 17, /* any legal NVFP4 activation arguments */
+  FP4W_PATH_MOE_FP4_STREAM = 18,  /* K % 64 == 0, I % 64 == 0, block_size 16 */
   FP4W_PATH_MOE_FP4_GENERIC = 19, /* any legal fp4w_moe arguments */
+  FP4W_PATH_MOE_FP8_STREAM = 20,  /* K % 64 == 0, I % 64 == 0, block_size % 128 == 0 */
   FP4W_PATH_MOE_FP8_GENERIC = 21  /* any legal fp8w_moe arguments */
 } fp4w_path;
 
@@ -433,7 +435,7 @@ int fp4w_moe(const void* A, int64_t M, int64_t K, const int32_t* ids, const floa
              int64_t I, int64_t block_size, int activation, void* workspace,
              int64_t workspace_bytes, void* Y, int dtype, void* stream);
 
-/* Path-forcing variant (FP4W_PATH_AUTO, _MOE_FP4_GENERIC). */
+/* Path-forcing variant (FP4W_PATH_AUTO, _MOE_FP4_STREAM, _MOE_FP4_GENERIC). */
 int fp4w_moe_ex(const void* A, int64_t M, int64_t K, const int32_t* ids, const float* weights,
                 int64_t topk, const uint8_t* w13, const uint8_t* w13_scale,
                 const float* w13_scale_2, const uint8_t* w2, const uint8_t* w2_scale,
@@ -453,7 +455,7 @@ int fp8w_moe(const void* A, int64_t M, int64_t K, const int32_t* ids, const floa
              const float* w2_scale, int64_t E, int64_t I, int64_t block_size, int activation,
              void* workspace, int64_t workspace_bytes, void* Y, int dtype, void* stream);
 
-/* Path-forcing variant (FP4W_PATH_AUTO, _MOE_FP8_GENERIC). */
+/* Path-forcing variant (FP4W_PATH_AUTO, _MOE_FP8_STREAM, _MOE_FP8_GENERIC). */
 int fp8w_moe_ex(const void* A, int64_t M, int64_t K, const int32_t* ids, const float* weights,
                 int64_t topk, const uint8_t* w13, const float* w13_scale, const uint8_t* w2,
                 const float* w2_scale, int64_t E, int64_t I, int64_t block_size, int activation,

@@ -21,6 +21,16 @@ int launch_moe_route(const MoeRouteArgs&) {
   g_last = "route";
   return 0;
 }
+// what the streaming kernels return: 0 (launched) or 1 (a row does not fit in LDS)
+static int g_stream_rc = 0;
+int launch_moe_fp4(const MoeArgs&) {
+  if (g_stream_rc == 0) g_last = "fp4_stream";
+  return g_stream_rc;
+}
+int launch_moe_fp8(const MoeArgs&) {
+  if (g_stream_rc == 0) g_last = "fp8_stream";
+  return g_stream_rc;
+}
 int launch_moe_fp4_generic(const MoeArgs&) {
   g_last = "fp4_generic";
   return 0;
@@ -93,6 +103,28 @@ int main() {
   LAUNCHED("fp4_generic");
   EXPECT(fp4(3, 64, 2, 0, 64, 16, FP4W_PATH_AUTO) == FP4W_OK);
   LAUNCHED("fp4_generic");
+  EXPECT(fp4(3, 64, 2, 4, 64, 16, FP4W_PATH_AUTO) == FP4W_OK);
+  LAUNCHED("fp4_stream");
+  EXPECT(fp4(3, 64, 2, 4, 64, 16, FP4W_PATH_MOE_FP4_GENERIC) == FP4W_OK);
+  LAUNCHED("fp4_generic");
+  EXPECT(fp4(3, 96, 2, 4, 64, 16, FP4W_PATH_MOE_FP4_STREAM) == FP4W_ERR_PATH);
+  EXPECT(fp4(3, 64, 2, 4, 64, 32, FP4W_PATH_MOE_FP4_STREAM) == FP4W_ERR_PATH);
+  EXPECT(fp4(3, 64, 2, 4, 64, 16, FP4W_PATH_MOE_FP8_STREAM) == FP4W_ERR_PATH);
+  EXPECT(fp8(3, 64, 2, 4, 64, 128, FP4W_PATH_MOE_FP8_STREAM) == FP4W_OK);
+  LAUNCHED("fp8_stream");
+  EXPECT(fp8(3, 64, 2, 4, 64, int64_t(1) << 40, FP4W_PATH_AUTO) == FP4W_OK);  // one block per row
+  LAUNCHED("fp8_stream");
+  EXPECT(fp8(3, 64, 2, 4, 64, 64, FP4W_PATH_AUTO) == FP4W_OK);
+  LAUNCHED("fp8_generic");
+  EXPECT(fp4(3, 1 << 16, 2, 4, 1 << 16, 16, FP4W_PATH_AUTO) == FP4W_OK);  // past 32-bit offsets
+  LAUNCHED("fp4_generic");
+  fp4w::g_stream_rc = 1;
+  EXPECT(fp4(3, 64, 2, 4, 64, 16, FP4W_PATH_AUTO) == FP4W_OK);
+  LAUNCHED("fp4_generic");
+  EXPECT(fp8(3, 64, 2, 4, 64, 128, FP4W_PATH_MOE_FP8_STREAM) == FP4W_ERR_PATH);
+  fp4w::g_stream_rc = -1;
+  EXPECT(fp8(3, 64, 2, 4, 64, 128, FP4W_PATH_AUTO) == FP4W_ERR_LAUNCH);
+  fp4w::g_stream_rc = 0;
   for (int64_t big : {INT64_MAX, INT64_MAX / 2 + 1, int64_t(1) << 41}) {
     EXPECT(fp4(big - big % 2, 64, 2, 4, 64, 16, 0) == FP4W_ERR_SHAPE);
     EXPECT(fp4(2, big - big % 2, 2, 4, 64, 16, 0) == FP4W_ERR_SHAPE);
