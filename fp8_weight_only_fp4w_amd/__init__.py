@@ -488,14 +488,22 @@ def fp4w_matmul_w4a4_noalloc(A: torch.Tensor, B: torch.Tensor, weight_scale: tor
 
 # ---------------------------------------------------------------- around a mixture-of-experts block
 
+# A call of these takes the GPU a few microseconds, so its marshalling is kept
+# short: the stream's handle comes straight from torch (a torch.cuda.Stream
+# object costs 1.8 us, the rest of a call about 4), and each tensor is checked
+# by one expression.
+
 def _call(device: torch.device, f, what: str, *args):
     """Call f(*args, stream) on the device's current stream, with that device current."""
-    stream = torch.cuda.current_stream(device)
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            status = f(*args, stream.cuda_stream)
+    index = device.index
+    if device.type != "cuda":
+        raise ValueError(f"{what} runs on the GPU, got tensors on {device}")
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            status = f(*args, stream)
     else:
-        status = f(*args, stream.cuda_stream)
+        status = f(*args, stream)
     if status != OK:
         raise FP4WError(status, what)
 
@@ -504,14 +512,10 @@ def _data(t):
     return None if t is None else t.data_ptr()
 
 
-def _like(t: torch.Tensor, name: str, A: torch.Tensor, shape):
-    """t is contiguous, on A's device, of A's type and of this shape."""
-    if t.shape != shape or t.dtype != A.dtype:
-        raise ValueError(f"{name} must be {tuple(shape)} with the type {A.dtype}, got {tuple(t.shape)} {t.dtype}")
-    _need(t, name, A.device)
-
-
 def _typed(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: torch.device):
+    """t has this type and shape, is contiguous and on the device."""
+    if t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+        return
     if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     _need(t, name, device)
@@ -531,39 +535,39 @@ def fp4w_block_norm(x: torch.Tensor, residual: torch.Tensor = None, pre_weight: 
     ``pre_weight``; with ``write_residual=False`` residual_out is neither
     written nor returned.  ``residual_out`` and ``out`` may be x or residual."""
     lib = load_library()
-    K = x.shape[-1] if x.dim() else 1
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    K = shape[-1] if shape else 1
     M = x.numel() // K if K else 0
-    code = _dtype_code(x.dtype)
-    _need(x, "x", x.device)
+    code = _dtype_code(dtype)
+    _need(x, "x", dev)
     if residual is not None:
-        _like(residual, "residual", x, x.shape)
-    for t, name in ((pre_weight, "pre_weight"), (post_weight, "post_weight")):
-        if t is not None:
-            _like(t, name, x, (K,))
+        _typed(residual, "residual", dtype, shape, dev)
+    if pre_weight is not None:
+        _typed(pre_weight, "pre_weight", dtype, (K,), dev)
+    if post_weight is not None:
+        _typed(post_weight, "post_weight", dtype, (K,), dev)
     gate_rows = 1
     if gate is not None:
-        if gate.shape == x.shape:
+        if gate.shape == shape:
             gate_rows = M
-            _like(gate, "gate", x, x.shape)
-        elif gate.dim() <= 2 and gate.numel() == K:
-            _like(gate, "gate", x, gate.shape)
-        else:
-            raise ValueError(f"gate must be [{K}] or {tuple(x.shape)}, got {tuple(gate.shape)}")
+        elif gate.dim() > 2 or gate.numel() != K:
+            raise ValueError(f"gate must be [{K}] or {tuple(shape)}, got {tuple(gate.shape)}")
+        _typed(gate, "gate", dtype, gate.shape, dev)
     if not write_residual:
         if residual_out is not None or pre_weight is None:
             raise ValueError("write_residual=False goes with a pre_weight and without a residual_out")
     elif residual_out is None:
         residual_out = torch.empty_like(x)
     else:
-        _like(residual_out, "residual_out", x, x.shape)
+        _typed(residual_out, "residual_out", dtype, shape, dev)
     if pre_weight is None:
         if out is not None:
             raise ValueError("out needs a pre_weight")
     elif out is None:
         out = torch.empty_like(x)
     else:
-        _like(out, "out", x, x.shape)
-    _call(x.device, lib.fp4w_block_norm, "fp4w_block_norm", x.data_ptr(), M, K, _data(post_weight), _data(gate),
+        _typed(out, "out", dtype, shape, dev)
+    _call(dev, lib.fp4w_block_norm, "fp4w_block_norm", x.data_ptr(), M, K, _data(post_weight), _data(gate),
           gate_rows, scale, _data(residual), _data(pre_weight), weight_offset, eps, _data(residual_out), _data(out),
           code)
     return residual_out, out
@@ -656,17 +660,19 @@ def _moe(fp8, A, ids, weights, w13, s13, g13, w2, s2, g2, block_size, activation
     if out is None:
         out = torch.empty_like(A)
     else:
-        _like(out, "out", A, A.shape)
-    args = [A.data_ptr(), M, K, ids.data_ptr(), weights.data_ptr(), topk, w13.data_ptr(), s13.data_ptr()]
+        _typed(out, "out", A.dtype, A.shape, dev)
+    head = (A.data_ptr(), M, K, ids.data_ptr(), weights.data_ptr(), topk, w13.data_ptr(), s13.data_ptr())
+    mid = (w2.data_ptr(), s2.data_ptr())
     if not fp8:
-        args.append(g13.data_ptr())
-    args += [w2.data_ptr(), s2.data_ptr()]
-    if not fp8:
-        args.append(g2.data_ptr())
-    args += [E, I, block_size, ACTIVATIONS[activation], workspace.data_ptr(),
-             workspace.numel() * workspace.element_size(), out.data_ptr(), code]
-    f = lib.fp8w_moe_ex if fp8 else lib.fp4w_moe_ex
-    _call(dev, lambda *a: f(*a, path), what, *args)
+        head, mid = head + (g13.data_ptr(),), mid + (g2.data_ptr(),)
+    tail = (E, I, block_size, ACTIVATIONS[activation], workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), out.data_ptr(), code)
+    if path == PATH_AUTO:
+        f = lib.fp8w_moe if fp8 else lib.fp4w_moe
+        _call(dev, f, what, *head, *mid, *tail)
+    else:
+        f = lib.fp8w_moe_ex if fp8 else lib.fp4w_moe_ex
+        _call(dev, lambda *a: f(*a, path), what, *head, *mid, *tail)
     return out
 
 

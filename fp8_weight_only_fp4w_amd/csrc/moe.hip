@@ -97,6 +97,57 @@ constexpr uint32_t plan_bytes(int n, int E, int list_max) {
   return (8u * list_max + 4u * E + 4u * 16u + 4u * n + 15u) & ~15u;
 }
 
+// Sum over this lane and those below it.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+#define FP4W_SCAN(CTRL, ROWS) \
+  v += static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xF, false))
+  FP4W_SCAN(0x111, 0xF);  // row_shr:1
+  FP4W_SCAN(0x112, 0xF);  // row_shr:2
+  FP4W_SCAN(0x114, 0xF);  // row_shr:4
+  FP4W_SCAN(0x118, 0xF);  // row_shr:8
+  FP4W_SCAN(0x142, 0xA);  // row_bcast:15 into rows 1 and 3
+  FP4W_SCAN(0x143, 0xC);  // row_bcast:31 into rows 2 and 3
+#undef FP4W_SCAN
+  return v;
+}
+
+// The passes of one expert whose assignments are sorted[at ..].
+__device__ __forceinline__ void write_passes(uint32_t* list, uint32_t slot, uint32_t e, uint32_t at, uint32_t tokens,
+                                             uint32_t rows) {
+  for (; tokens; ++slot) {
+    const uint32_t t = tokens < rows ? tokens : rows;
+    list[slot] = e | at << 10 | (t - 1) << 22;
+    at += t;
+    tokens -= t;
+  }
+}
+
+// n <= 64: every wave makes the whole plan by itself, one assignment a lane,
+// and writes it to LDS (all the same values), so no barrier is needed.
+// Experts come in the order of their first assignment.
+__device__ __forceinline__ Plan make_plan_wave(const MoeParams& p, unsigned char* mem) {
+  uint32_t* list = reinterpret_cast<uint32_t*>(mem);
+  uint16_t* sorted = reinterpret_cast<uint16_t*>(list + p.list_max);
+  const int lane = threadIdx.x & 63;
+  const int id = lane < p.n ? p.ids[lane] : -1;
+  int tokens = 0, rank = 0, first = lane;
+  for (int j = p.n - 1; j >= 0; --j) {
+    const bool same = __builtin_amdgcn_readlane(id, j) == id;
+    tokens += same;
+    rank += same && j < lane;
+    first = same ? j : first;
+  }
+  const bool valid = static_cast<uint32_t>(id) < static_cast<uint32_t>(p.E);
+  const bool leads = valid && first == lane;
+  const uint32_t rows = static_cast<uint32_t>(p.rows);
+  const uint32_t mine = leads ? static_cast<uint32_t>(tokens) | (tokens + rows - 1) / rows << 16 : 0u;
+  const uint32_t upto = wave_scan(mine), before = upto - mine;
+  if (leads) write_passes(list, before >> 16, static_cast<uint32_t>(id), before & 0xFFFF, tokens, rows);
+  const uint32_t at = __shfl(before, first, 64) & 0xFFFF;
+  if (valid) sorted[at + rank] = static_cast<uint16_t>(lane);
+  return Plan{list, sorted, static_cast<int>(static_cast<uint32_t>(__builtin_amdgcn_readlane(upto, 63)) >> 16)};
+}
+
 // All threads of the workgroup; `mem` holds plan_bytes().  Every workgroup
 // comes to the same list, and to the same tokens in each pass: an expert with
 // several passes has its assignments in rising order.
@@ -126,12 +177,7 @@ __device__ __forceinline__ Plan make_plan(const MoeParams& p, unsigned char* mem
     c[i] = 2 * tid + i < p.E ? count[2 * tid + i] : 0u;
     v[i] = c[i] | ((c[i] + p.rows - 1) / p.rows) << 16;
   }
-  uint32_t sum = v[0] + v[1];
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t o = __shfl_up(sum, d, 64);
-    if (lane >= d) sum += o;
-  }
+  const uint32_t sum = wave_scan(v[0] + v[1]);
   if (lane == 63) part[wave] = sum;
   __syncthreads();
   uint32_t before = sum - v[0] - v[1], total = 0;
@@ -145,15 +191,10 @@ __device__ __forceinline__ Plan make_plan(const MoeParams& p, unsigned char* mem
   for (int i = 0; i < 2; ++i) {
     const uint32_t e = 2 * tid + i;
     if (c[i]) {
-      uint32_t at = before & 0xFFFF, left = c[i], slot = before >> 16;
+      const uint32_t at = before & 0xFFFF;
       count[e] = at;
-      if (left > static_cast<uint32_t>(p.rows)) multi[atomicAdd(&part[8], 1u)] = e | at << 10;
-      for (; left; ++slot) {
-        const uint32_t t = left < static_cast<uint32_t>(p.rows) ? left : static_cast<uint32_t>(p.rows);
-        list[slot] = e | at << 10 | (t - 1) << 22;
-        at += t;
-        left -= t;
-      }
+      if (c[i] > static_cast<uint32_t>(p.rows)) multi[atomicAdd(&part[8], 1u)] = e | at << 10;
+      write_passes(list, before >> 16, e, at, c[i], static_cast<uint32_t>(p.rows));
     }
     before += v[i];
   }
@@ -218,7 +259,7 @@ __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
   unsigned char* red = smem + kWaves * S * kUnitBytes;
   unsigned char* plan_mem = red + (KS > 1 ? kRedBytes : 0u);
   unsigned char* rows_lds = plan_mem + plan_bytes(p.n, p.E, p.list_max);
-  const Plan plan = make_plan(p, plan_mem);
+  const Plan plan = p.n <= 64 ? make_plan_wave(p, plan_mem) : make_plan(p, plan_mem);
 
   // this workgroup's share of the flat (pass, group) list
   const uint64_t all = static_cast<uint64_t>(plan.passes) * static_cast<uint64_t>(p.groups);
@@ -308,17 +349,16 @@ __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
   f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
   Scale raw[S];
   int c_pass = first_pass, c_group = first_group, c_unit = 0;
-  // FP4: the expert's FP32 scale (read here, not where a tile ends: a load
-  // there would wait for every weight load before it)
-  auto expert_scale = [&](const Pass& ps) {
-    return FP8 ? 1.0f : __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, p.g[ps.expert])));
-  };
+  // FP4: the expert's FP32 scale, read ahead of the pass's rows and waited for
+  // with them (a load where a tile ends would wait for every weight load
+  // before it)
   Pass ps = read_pass(plan.list, c_pass);
-  float gs = expert_scale(ps);
+  float gs = FP8 ? 1.0f : p.g[ps.expert];
   fill(ps);
 #pragma unroll
   for (int d = 0; d < D; ++d) load(raw[d], ring + d * kUnitBytes);
   wait_vm<D * LPU>();  // the fill is older
+  __asm__ volatile("" : "+v"(gs));
   __builtin_amdgcn_s_barrier();
   __asm__ volatile("" ::: "memory");
 
@@ -424,10 +464,11 @@ __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
         if (c_unit == 0 && c_group == 0 && c_pass != first_pass) {
           // the next pass's tokens take the place of the last one's
           ps = read_pass(plan.list, c_pass);
-          gs = expert_scale(ps);
+          if (!FP8) gs = p.g[ps.expert];
           lds_barrier();
           fill(ps);
           wait_vm<0>();
+          __asm__ volatile("" : "+v"(gs));
           __builtin_amdgcn_s_barrier();
           __asm__ volatile("" ::: "memory");
         }
@@ -437,6 +478,229 @@ __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
     }
   }
   wait_vm<0>();  // loads past the end of the share write zeros to the ring
+}
+
+// ---------------------------------------------------------------- one token
+//
+// M = 1: assignment j is choice j of the only token, so no plan is made: a
+// pass is a choice, its token row is A for every choice (up) and row j of H
+// (down).  What counts is the chain of latencies (launch, ids, first weights,
+// join), so up shares out (choice, tile group) pairs to as many workgroups as
+// the chip holds, and down gives a workgroup whole column tiles, with the
+// choices spread over its waves, and adds them up itself: no third kernel.
+//
+// The token fills MFMA row 0, in down its H's remainder row 1, so both planes
+// take one MFMA; the other rows repeat them and are dropped.
+
+// up: grid-stride over (choice, group); down: over tiles.
+template <typename T, bool FP8, bool UP, int KS, int D>
+__global__ __launch_bounds__(kThreads) void moe_token_kernel(const MoeParams p, const float* __restrict__ weights) {
+  typedef typename std::conditional<UP, T, __bf16>::type X;
+  typedef ActTraits<X> Tr;
+  typedef typename Tr::vec8 V;
+  typedef typename std::conditional<FP8, uint32_t, u32x4>::type Scale;
+  constexpr int TPW = kWaves / KS;  // up: tiles side by side; down: choices side by side
+  constexpr int S = D + 1;
+  constexpr int UW = FP8 ? 1 : 2;
+  constexpr int LPU = 3;
+  extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int li = lane & 15, g = lane >> 4;
+  const int lr = lane >> 3, lc = lane & 7;
+  const int ks = wave % KS, tw = wave / KS;
+  unsigned char* ring = smem + static_cast<uint32_t>(wave) * (S * kUnitBytes);
+  unsigned char* red = smem + kWaves * S * kUnitBytes;
+  unsigned char* rows_lds = red + kRedBytes;
+  const int NW = (p.L + 127) >> 7;
+  const int NU = (NW + UW - 1) / UW;
+  const uint32_t row_bytes = FP8 ? static_cast<uint32_t>(p.L) : static_cast<uint32_t>(p.L >> 1);
+  const uint32_t srow_bytes = FP8 ? 4u * p.cols : static_cast<uint32_t>(p.cols);
+  const uint32_t half = UP ? static_cast<uint32_t>(p.N >> 1) : 8u;
+  const uint32_t tile_rows = UP ? 8u : 16u;
+  const uint32_t pitch = static_cast<uint32_t>(NW) * 256u + 16u;
+  const uint32_t wl = lr * row_bytes + 16u * (lc ^ lr);
+  const uint32_t wl8 = wl + half * row_bytes;
+  const uint32_t sl = (li < 8 ? li : li - 8 + half) * srow_bytes;
+  const int sw = li & 7;
+
+  // The wave's sequence.  up: items (choice, group) b, b + grid, ..; wave
+  // (tw, ks) takes tile group * TPW + tw.  down: tiles b, b + grid, .. and in
+  // each the choices tw, tw + TPW, ..
+  const int inner = UP ? 1 : (p.n + TPW - 1) / TPW;  // choices of a wave per tile
+  const int items = UP ? p.n * p.groups : p.tiles;
+  const int mine = items > static_cast<int>(blockIdx.x)
+                       ? (items - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x)
+                       : 0;
+  const int total = mine * inner * p.units;
+
+  int l_item = blockIdx.x, l_in = 0, l_unit = 0;
+  rsrc_t br, sr;
+  auto choice_of = [&](int item, int in) { return UP ? item / p.groups : tw + in * TPW; };
+  auto tile_of = [&](int item) { return UP ? item % p.groups * TPW + tw : item; };
+  // Lane j holds choice j (topk <= 64): its expert, -1 where there is none,
+  // the expert's FP32 scale and the choice's weight.  The last two are not
+  // waited for here.
+  int e_lane = lane < p.n ? p.ids[lane] : -1;
+  if (static_cast<uint32_t>(e_lane) >= static_cast<uint32_t>(p.E)) e_lane = -1;
+  float g_lane = !FP8 && e_lane >= 0 ? p.g[e_lane] : 1.0f;
+  float w_lane = !UP && lane < p.n ? weights[lane] : 0.0f;
+  auto expert_of = [&](int j) { return j < p.n ? __builtin_amdgcn_readlane(e_lane, j) : -1; };
+  auto value_of = [&](float v, int j) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), j));
+  };
+  auto set_load_tile = [&]() {
+    const int t = tile_of(l_item);
+    const int e = l_item < items ? expert_of(choice_of(l_item, l_in)) : -1;
+    const bool on = e >= 0 && t < p.tiles;
+    const int64_t row = static_cast<int64_t>(on ? e : 0) * p.N + static_cast<int64_t>(on ? t : 0) * tile_rows;
+    const uint32_t span = on ? half + 8u : 0u;
+    br = make_rsrc(p.w + row * row_bytes, span * row_bytes);
+    sr = make_rsrc(p.s + row * srow_bytes, span * srow_bytes);
+  };
+  set_load_tile();
+  auto load = [&](Scale& sc, unsigned char* slot) {
+    const int u = ks * p.units + l_unit;
+    const bool ok = u < NU;
+    if constexpr (FP8) {
+      const uint32_t col = min(fdiv(static_cast<uint32_t>(u), p.win_per_block), static_cast<uint32_t>(p.cols - 1));
+      sc = buf_load_b32(sr, ok ? sl + 4u * col : kOutOfRange);
+    } else {
+      sc = buf_load_b128(sr, ok ? sl + 16u * u : kOutOfRange);
+    }
+    const uint32_t ub = 128u * static_cast<uint32_t>(u);
+    buf_load_lds<16>(br, ok ? wl + ub : kOutOfRange, slot);
+    buf_load_lds<16>(br, ok ? wl8 + ub : kOutOfRange, slot + 1024);
+    if (++l_unit == p.units) {
+      l_unit = 0;
+      if (++l_in == inner) {
+        l_in = 0;
+        l_item += gridDim.x;
+      }
+      set_load_tile();
+    }
+  };
+
+  // up: the token's row; down: the high parts of all choices, then the
+  // remainders (rows of choices without an expert hold anything: their
+  // results are dropped)
+  {
+    const rsrc_t x_rsrc = make_rsrc(p.x, static_cast<uint32_t>(p.x_bytes));
+    const uint32_t cpr = p.chunks_per_row.d;
+    const uint32_t chunks = (UP ? 1u : 2u * p.n) * cpr;
+    for (uint32_t q0 = 64u * static_cast<uint32_t>(wave); q0 < chunks; q0 += 64u * kWaves) {
+      const uint32_t q = q0 + static_cast<uint32_t>(lane);
+      const uint32_t row = fdiv(q, p.chunks_per_row), col = q - row * cpr;
+      const bool in = q < chunks && col * 8u < static_cast<uint32_t>(p.L);
+      buf_load_lds<16>(x_rsrc, in ? row * (2u * p.L) + 16u * col : kOutOfRange, rows_lds + 16u * q0);
+    }
+  }
+  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+  float sum = 0.0f;  // down: the weighted choices of this wave, lanes g == 0
+  Scale raw[S];
+  int c_item = blockIdx.x, c_in = 0, c_unit = 0, turn = 0;
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(raw[d], ring + d * kUnitBytes);
+  wait_vm<D * LPU>();  // the rows, scales and weights are older
+  __asm__ volatile("" : "+v"(g_lane), "+v"(w_lane));
+  __builtin_amdgcn_s_barrier();
+  __asm__ volatile("" ::: "memory");
+
+  auto consume = [&](const Scale& sc, const unsigned char* slot) {
+    const int u = ks * p.units + c_unit;
+    const int j = choice_of(c_item, c_in);
+    wait_vm<D * LPU>();
+    const unsigned char* arow =
+        UP ? rows_lds : rows_lds + static_cast<uint32_t>((li & 1) * p.n + min(j, p.n - 1)) * pitch;
+    if constexpr (FP8) {
+      if (u < NW) {
+        const unsigned char* q = arow + 256u * u + 32u * g;
+        const u32x4 w0 = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * (g ^ sw));
+        u32x4 w1 = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * ((4 + g) ^ sw));
+        if (128 * u + 64 >= p.L) w1 = u32x4{0u, 0u, 0u, 0u};  // the next row's bytes
+        f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
+        d = Tr::mfma(*reinterpret_cast<const V*>(q), Tr::decode8_fp8(w0.x, w0.y), d);
+        d = Tr::mfma(*reinterpret_cast<const V*>(q + 16), Tr::decode8_fp8(w0.z, w0.w), d);
+        d = Tr::mfma(*reinterpret_cast<const V*>(q + 128), Tr::decode8_fp8(w1.x, w1.y), d);
+        d = Tr::mfma(*reinterpret_cast<const V*>(q + 144), Tr::decode8_fp8(w1.z, w1.w), d);
+        const float s = __builtin_bit_cast(float, sc);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) acc[i] = fmaf(d[i], s, acc[i]);
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int w = 2 * u + h;
+        if (w < NW) {
+          const unsigned char* q = arow + 256u * w + 64u * g;
+          const u32x4 wv = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * ((4 * h + g) ^ sw));
+          const uint32_t s4 = (g & 2) ? sc[2 * h + 1] : sc[2 * h];
+          uint32_t s2 = s4 >> (16 * (g & 1));
+          if (128 * w + 64 >= p.L && g >= 2) s2 = 0;
+          const f32x2 sf = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s2), false);
+          const typename Tr::scale_t sa = Tr::make_scale(sf.x), sb = Tr::make_scale(sf.y);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc = Tr::mfma(*reinterpret_cast<const V*>(q + 16 * i), Tr::decode8(wv[i], i < 2 ? sa : sb), acc);
+        }
+      }
+    }
+    if (++c_unit < p.units) return;
+    c_unit = 0;
+    const int e = expert_of(j);
+    // row 0 (and 1) of the result lie in lanes g == 0
+    float v = UP ? acc[0] : acc[0] + acc[1];
+    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (!UP) {
+      if (e >= 0) sum = fmaf(v * value_of(g_lane, j), value_of(w_lane, j), sum);
+      if (++c_in < inner) return;
+      c_in = 0;
+      v = sum;
+      sum = 0.0f;
+    }
+    // join: up the K split of a tile, down the waves' choices (and K splits),
+    // each in the order of the waves; the two halves of `red` are used in
+    // turn, so one barrier is enough
+    float* part = reinterpret_cast<float*>(red) + 128 * turn;
+    const int joined = UP ? KS : kWaves;
+    if (joined > 1) {
+      turn ^= 1;
+      if (g == 0) part[16 * wave + li] = v;
+      lds_barrier();
+    }
+    if ((UP ? ks : wave) == 0 && g == 0) {
+      if (joined > 1) {
+        v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < (UP ? KS : kWaves); ++i) v += part[16 * (wave + i) + li];
+      }
+      const int t = tile_of(c_item);
+      if (UP) {
+        const float up = swap8(v);
+        if (e >= 0 && t < p.tiles && li < 8) {
+          const float gs = value_of(g_lane, j);
+          const float hv = gated(p.act, v * gs, up * gs);
+          const __bf16 top = static_cast<__bf16>(hv);
+          const float rest = hv - static_cast<float>(top);
+          __bf16* out = static_cast<__bf16*>(p.out) + static_cast<size_t>(j) * (p.N >> 1) + 8 * t + li;
+          out[0] = top;
+          out[static_cast<size_t>(p.n) * (p.N >> 1)] = static_cast<__bf16>(__builtin_isfinite(rest) ? rest : 0.0f);
+        }
+      } else {
+        static_cast<T*>(p.out)[16 * t + li] = round_to<T>(v);
+      }
+    }
+    c_item += gridDim.x;
+  };
+
+  for (int f0 = 0; f0 < total; f0 += S) {
+#pragma unroll
+    for (int u = 0; u < S; ++u) {
+      load(raw[(u + D) % S], ring + ((u + D) % S) * kUnitBytes);
+      if (f0 + u < total) consume(raw[u], ring + u * kUnitBytes);
+    }
+  }
+  wait_vm<0>();
 }
 
 // Y[m, c .. c + 7] = sum over j of weights[m * topk + j] * P[m * topk + j, c ..], in the order of j
@@ -450,16 +714,28 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
     float sum[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
-    for (int j = 0; j < topk; ++j) {
-      const int a = m * topk + j;
-      if (static_cast<uint32_t>(ids[a]) >= static_cast<uint32_t>(E)) continue;
-      const f32x4* q = reinterpret_cast<const f32x4*>(P + static_cast<size_t>(a) * K + 8 * c);
-      const f32x4 x = q[0], y = q[1];
-      const float w = weights[a];
+    for (int j0 = 0; j0 < topk; j0 += 4) {
+      // four choices' loads at a time, none of them behind a branch; what a
+      // masked choice holds is not used
+      f32x4 x[4], y[4];
+      float w[4];
+      bool on[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        sum[k] = fmaf(x[k], w, sum[k]);
-        sum[4 + k] = fmaf(y[k], w, sum[4 + k]);
+      for (int j = 0; j < 4; ++j) {
+        const int a = m * topk + min(j0 + j, topk - 1);
+        const f32x4* q = reinterpret_cast<const f32x4*>(P + static_cast<size_t>(a) * K + 8 * c);
+        x[j] = q[0];
+        y[j] = q[1];
+        w[j] = weights[a];
+        on[j] = j0 + j < topk && static_cast<uint32_t>(ids[a]) < static_cast<uint32_t>(E);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          sum[k] = on[j] ? fmaf(x[j][k], w[j], sum[k]) : sum[k];
+          sum[4 + k] = on[j] ? fmaf(y[j][k], w[j], sum[4 + k]) : sum[4 + k];
+        }
       }
     }
     typename ActTraits<T>::vec8 r;
@@ -509,7 +785,7 @@ bool plan_shape(const MoeArgs& a, bool fp8, bool up, Shape* out) {
   const int64_t mean = a.E > 0 ? (n + a.E - 1) / a.E : n;
   int64_t want = 2 * mean + 4;
   if (want > 16) want = 16;
-  if (want > n) want = n;
+  if (want > a.M) want = a.M;  // (a token that names an expert twice may take a second pass)
   if (want < 1) want = 1;
   for (int depth : {4, 2}) {
     for (int64_t rows = want; rows >= 1; --rows) {
@@ -564,47 +840,103 @@ void launch_phase(MoeParams p, const Shape& s, hipStream_t st) {
 #undef FP4W_MOE_KS
 }
 
+template <typename T, bool FP8, bool UP, int KS>
+void launch_token_kernel(const MoeParams& p, const float* weights, int grid, size_t lds, hipStream_t st) {
+  static std::once_flag once[kMaxDevices];
+  once_per_device(once, [] {
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&moe_token_kernel<T, FP8, UP, KS, 4>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxLds));
+  });
+  hipLaunchKernelGGL((moe_token_kernel<T, FP8, UP, KS, 4>), dim3(grid), dim3(kThreads), lds, st, p, weights);
+}
+
+template <typename T, bool FP8, bool UP>
+void launch_token_ks(const MoeParams& p, const float* weights, int ks, int grid, size_t lds, hipStream_t st) {
+  switch (ks) {
+    case 1: launch_token_kernel<T, FP8, UP, 1>(p, weights, grid, lds, st); break;
+    case 2: launch_token_kernel<T, FP8, UP, 2>(p, weights, grid, lds, st); break;
+    case 4: launch_token_kernel<T, FP8, UP, 4>(p, weights, grid, lds, st); break;
+    default: launch_token_kernel<T, FP8, UP, 8>(p, weights, grid, lds, st); break;
+  }
+}
+
+// M = 1.  False where the rows do not fit in LDS beside the rings.
+template <typename T, bool FP8>
+bool launch_token(const MoeArgs& a, MoeParams up, MoeParams down, hipStream_t st) {
+  const size_t base = kWaves * 5 * kUnitBytes + kRedBytes;
+  const int cus = device_cus();
+  const int up_nw = static_cast<int>((a.K + 127) / 128), down_nw = static_cast<int>((a.I + 127) / 128);
+  const size_t up_lds = base + rows_lds_bytes(1, 1, up_nw);
+  const size_t down_lds = base + rows_lds_bytes(static_cast<int>(a.topk), 2, down_nw);
+  if (up_lds > kMaxLds || down_lds > kMaxLds) return false;
+  const int up_nu = FP8 ? up_nw : (up_nw + 1) / 2, down_nu = FP8 ? down_nw : (down_nw + 1) / 2;
+  // up: as for several tokens, the K split with the least work on a wave
+  int up_ks = 1, up_grid = 1;
+  int64_t best = -1;
+  for (int ks : {1, 2, 4, 8}) {
+    if (ks > 1 && up_nu < ks) break;
+    const int64_t groups = (up.tiles + kWaves / ks - 1) / (kWaves / ks), units = (up_nu + ks - 1) / ks;
+    const int64_t rounds = (a.topk * groups + cus - 1) / cus;
+    if (best < 0 || rounds * (units + 1) < best) {
+      best = rounds * (units + 1);
+      up_ks = ks;
+      up.groups = static_cast<int>(groups);
+      up.units = static_cast<int>(units);
+      up_grid = static_cast<int>((a.topk * groups + rounds - 1) / rounds);
+    }
+  }
+  // down: a wave per choice, the waves that this leaves split the sum
+  const int down_ks = a.topk > 4 ? 1 : a.topk > 2 ? 2 : a.topk > 1 ? 4 : 8;
+  down.units = (down_nu + down_ks - 1) / down_ks;
+  const int rounds = (down.tiles + cus - 1) / cus;
+  const int down_grid = (down.tiles + rounds - 1) / rounds;
+  down.out = a.Y;
+  launch_token_ks<T, FP8, true>(up, a.weights, up_ks, up_grid, up_lds, st);
+  launch_token_ks<T, FP8, false>(down, a.weights, down_ks, down_grid, down_lds, st);
+  return true;
+}
+
 template <typename T, bool FP8>
 int launch_t(const MoeArgs& a) {
-  Shape up, down;
-  if (!plan_shape(a, FP8, true, &up) || !plan_shape(a, FP8, false, &down)) return 1;
   hipStream_t st = static_cast<hipStream_t>(a.stream);
   const int64_t n = a.M * a.topk;
   __bf16* H = static_cast<__bf16*>(a.work);
   float* P = reinterpret_cast<float*>(static_cast<unsigned char*>(a.work) + (n * a.I * 4 + 255) / 256 * 256);
-  MoeParams p{};
-  p.ids = a.ids;
-  p.topk = make_fastdiv(static_cast<uint32_t>(a.topk));
-  p.win_per_block = make_fastdiv(FP8 ? static_cast<uint32_t>(a.block_size / 128) : 1u);
-  p.n = static_cast<int>(n);
-  p.E = static_cast<int>(a.E);
-  p.act = a.activation;
-  // up
-  p.x = a.A;
-  p.w = a.w13;
-  p.s = static_cast<const uint8_t*>(a.s13);
-  p.g = a.g13;
-  p.out = H;
-  p.L = static_cast<int>(a.K);
-  p.N = static_cast<int>(2 * a.I);
-  p.cols = static_cast<int>((a.K + a.block_size - 1) / a.block_size);
-  p.x_bytes = static_cast<int>(a.M * a.K * 2);
-  p.tiles = static_cast<int>(a.I / 8);
-  p.chunks_per_row = make_fastdiv(static_cast<uint32_t>((a.K + 127) / 128 * 16 + 1));
-  launch_phase<T, FP8, true>(p, up, st);
-  // down
-  p.x = H;
-  p.w = a.w2;
-  p.s = static_cast<const uint8_t*>(a.s2);
-  p.g = a.g2;
-  p.out = P;
-  p.L = static_cast<int>(a.I);
-  p.N = static_cast<int>(a.K);
-  p.cols = static_cast<int>((a.I + a.block_size - 1) / a.block_size);
-  p.x_bytes = static_cast<int>(n * a.I * 4);
-  p.tiles = static_cast<int>(a.K / 16);
-  p.chunks_per_row = make_fastdiv(static_cast<uint32_t>((a.I + 127) / 128 * 16 + 1));
-  launch_phase<__bf16, FP8, false>(p, down, st);
+  MoeParams up{};
+  up.ids = a.ids;
+  up.topk = make_fastdiv(static_cast<uint32_t>(a.topk));
+  up.win_per_block = make_fastdiv(FP8 ? static_cast<uint32_t>(a.block_size / 128) : 1u);
+  up.n = static_cast<int>(n);
+  up.E = static_cast<int>(a.E);
+  up.act = a.activation;
+  MoeParams down = up;
+  up.x = a.A;
+  up.w = a.w13;
+  up.s = static_cast<const uint8_t*>(a.s13);
+  up.g = a.g13;
+  up.out = H;
+  up.L = static_cast<int>(a.K);
+  up.N = static_cast<int>(2 * a.I);
+  up.cols = static_cast<int>((a.K + a.block_size - 1) / a.block_size);
+  up.x_bytes = static_cast<int>(a.M * a.K * 2);
+  up.tiles = static_cast<int>(a.I / 8);
+  up.chunks_per_row = make_fastdiv(static_cast<uint32_t>((a.K + 127) / 128 * 16 + 1));
+  down.x = H;
+  down.w = a.w2;
+  down.s = static_cast<const uint8_t*>(a.s2);
+  down.g = a.g2;
+  down.out = P;
+  down.L = static_cast<int>(a.I);
+  down.N = static_cast<int>(a.K);
+  down.cols = static_cast<int>((a.I + a.block_size - 1) / a.block_size);
+  down.x_bytes = static_cast<int>(n * a.I * 4);
+  down.tiles = static_cast<int>(a.K / 16);
+  down.chunks_per_row = make_fastdiv(static_cast<uint32_t>((a.I + 127) / 128 * 16 + 1));
+  if (a.M == 1 && launch_token<T, FP8>(a, up, down, st)) return hipGetLastError() == hipSuccess ? 0 : -1;
+  Shape up_shape, down_shape;
+  if (!plan_shape(a, FP8, true, &up_shape) || !plan_shape(a, FP8, false, &down_shape)) return 1;
+  launch_phase<T, FP8, true>(up, up_shape, st);
+  launch_phase<__bf16, FP8, false>(down, down_shape, st);
   // combine
   const int64_t blocks = (a.M * (a.K / 8) + 255) / 256;
   hipLaunchKernelGGL(moe_combine_kernel<T>, dim3(static_cast<int>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, P,
