@@ -85,7 +85,7 @@ struct MoeParams {
 };
 
 // LDS: unit rings, partial sums of the K split, then the plan and the token rows.
-constexpr uint32_t kRedBytes = kWaves * 1024;
+constexpr uint32_t kRedBytes = 2 * kWaves * 1024;
 
 struct Plan {
   const uint32_t* list;    // pass: expert | first sorted assignment << 10 | (tokens - 1) << 22
@@ -236,6 +236,121 @@ __device__ __forceinline__ float swap8(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(i, i, 0x128, 0xF, 0xF, false));  // row_ror:8
 }
 
+// H as two BF16 planes, `plane` values apart.  The remainder is exact in FP32;
+// where the high part is infinite or NaN it adds nothing.
+__device__ __forceinline__ void store_h(__bf16* out, size_t plane, float h) {
+  const __bf16 top = static_cast<__bf16>(h);
+  const float rest = h - static_cast<float>(top);
+  out[0] = top;
+  out[plane] = static_cast<__bf16>(__builtin_isfinite(rest) ? rest : 0.0f);
+}
+
+// ---- one unit of weights times the token rows
+//
+// a0: the lane's LDS address in window 0 of the high (or only) plane, `step`
+// bytes per window and lo_plane to the other plane (both 0 for a lane that
+// reads the zero block throughout); `zero`: the zero block, for windows past
+// the row.  Every LDS read of the unit is issued before its arithmetic.
+
+// FP4, dense: lane row li carries token li.  A weight is decoded with its
+// block scale (lane group g holds blocks 2g and 2g + 1 of a window): about 86
+// VALU instructions a window, for up to 16 tokens.
+// FP4, DIAG: the decode GEMV's block-diagonal operand, for up to 4 rows.  Row
+// 4 m + q carries row m in the k slots of lane group q only, so the lane (n,
+// g) gets row g's dots with single blocks, scaled by one FMA each: the
+// weights are decoded unscaled, which halves the VALU work.  The sum is
+// acc[0].
+template <typename Tr, int PLANES, bool DIAG>
+__device__ __forceinline__ void fp4_unit(f32x4& acc, const u32x4& sc, const unsigned char* slot, lds_cbytes a0,
+                                         uint32_t step, lds_cbytes zero, uint32_t lo_plane, int u, int NW, int L, int li,
+                                         int g) {
+  typedef typename Tr::vec8 V;
+  const int sw = li & 7;
+  u32x4 wv[2], av[2][PLANES][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int w = 2 * u + h;
+    wv[h] = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * ((4 * h + g) ^ sw));
+    const lds_cbytes q = w < NW ? a0 + step * static_cast<uint32_t>(w) : zero;
+    const uint32_t next = w < NW ? lo_plane : 0u;
+#pragma unroll
+    for (int pl = 0; pl < PLANES; ++pl)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) av[h][pl][i] = *reinterpret_cast<const lds_u32x4*>(q + pl * next + 16 * i);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int w = 2 * u + h;
+    // E4M3 scales of the window's 8 blocks; blocks past the row (the next
+    // row's bytes) count as zero
+    const uint32_t s_lo = w < NW ? sc[2 * h] : 0u, s_hi = 128 * w + 64 < L ? sc[2 * h + 1] : 0u;
+    if constexpr (DIAG) {
+      const f32x2 s01 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s_lo), false);
+      const f32x2 s23 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s_lo), true);
+      const f32x2 s45 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s_hi), false);
+      const f32x2 s67 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s_hi), true);
+      const float s8[8] = {s01.x, s01.y, s23.x, s23.y, s45.x, s45.y, s67.x, s67.y};
+      f32x4 d[2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const V b0 = Tr::decode8_fp4(wv[h][2 * s]), b1 = Tr::decode8_fp4(wv[h][2 * s + 1]);
+        d[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int pl = 0; pl < PLANES; ++pl) {
+          d[s] = Tr::mfma(__builtin_bit_cast(V, av[h][pl][2 * s]), b0, d[s]);
+          d[s] = Tr::mfma(__builtin_bit_cast(V, av[h][pl][2 * s + 1]), b1, d[s]);
+        }
+      }
+      // result row r of set s is block 2r + s
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) acc[0] = fmaf(d[s][r], s8[2 * r + s], acc[0]);
+    } else {
+      const uint32_t s2 = ((g & 2) ? s_hi : s_lo) >> (16 * (g & 1));
+      const f32x2 sf = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s2), false);
+      const typename Tr::scale_t sa = Tr::make_scale(sf.x), sb = Tr::make_scale(sf.y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const V b = Tr::decode8(wv[h][i], i < 2 ? sa : sb);
+#pragma unroll
+        for (int pl = 0; pl < PLANES; ++pl) acc = Tr::mfma(__builtin_bit_cast(V, av[h][pl][i]), b, acc);
+      }
+    }
+  }
+}
+
+// FP8: a window's sum in a fresh accumulator, added times its FP32 scale.
+// Lane group g takes chunks g and 4 + g (16 k each) of its row's 128 bytes.
+template <typename Tr, int PLANES>
+__device__ __forceinline__ void fp8_unit(f32x4& acc, uint32_t sc, const unsigned char* slot, lds_cbytes a0,
+                                         lds_cbytes zero, uint32_t lo_plane, int u, int NW, int L, int li, int g) {
+  typedef typename Tr::vec8 V;
+  const int sw = li & 7;
+  const u32x4 w0 = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * (g ^ sw));
+  u32x4 w1 = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * ((4 + g) ^ sw));
+  const lds_cbytes q = u < NW ? a0 + 256u * static_cast<uint32_t>(u) : zero;
+  const uint32_t next = u < NW ? lo_plane : 0u;
+  u32x4 av[PLANES][4];
+#pragma unroll
+  for (int pl = 0; pl < PLANES; ++pl)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      av[pl][i] = *reinterpret_cast<const lds_u32x4*>(q + pl * next + (i & 1) * 16 + (i >> 1) * 128);
+  // a last window of 64 k: the bytes past the row are the next row's
+  if (128 * u + 64 >= L) w1 = u32x4{0u, 0u, 0u, 0u};
+  const V b[4] = {Tr::decode8_fp8(w0.x, w0.y), Tr::decode8_fp8(w0.z, w0.w), Tr::decode8_fp8(w1.x, w1.y),
+                  Tr::decode8_fp8(w1.z, w1.w)};
+  f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int pl = 0; pl < PLANES; ++pl)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d = Tr::mfma(__builtin_bit_cast(V, av[pl][i]), b[i], d);
+  const float s = __builtin_bit_cast(float, sc);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = fmaf(d[i], s, acc[i]);
+}
+
 // UP: the first kernel (A of type T against w13), otherwise the second (H
 // planes against w2; its operands are BF16 whatever T is).
 template <typename T, bool FP8, bool UP, int KS, int D>
@@ -281,7 +396,6 @@ __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
   const uint32_t wl = lr * row_bytes + 16u * (lc ^ lr);
   const uint32_t wl8 = wl + half * row_bytes;
   const uint32_t sl = (li < 8 ? li : li - 8 + half) * srow_bytes;
-  const int sw = li & 7;
 
   // ---- load side
   int l_pass = first_pass, l_group = first_group, l_unit = 0;
@@ -322,17 +436,17 @@ __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
   };
 
   // ---- token rows of a pass, by direct loads: LDS chunk q holds row q /
-  // chunks_per_row (down: the high parts of all tokens, then the remainders);
-  // rows' padding and the tail of the last instruction are out-of-range
+  // chunks_per_row (down: the high parts of all tokens, then the remainders),
+  // then 256 bytes of zeros; the zeros, rows' padding and the tail of the last instruction are out-of-range
   // reads, which write zeros
   auto fill = [&](const Pass& ps) {
     const uint32_t cpr = p.chunks_per_row.d;
-    const uint32_t chunks = static_cast<uint32_t>(PLANES * ps.tokens) * cpr;
+    const uint32_t data = static_cast<uint32_t>(PLANES * ps.tokens) * cpr, chunks = data + 16u;
     for (uint32_t q0 = 64u * static_cast<uint32_t>(wave); q0 < chunks; q0 += 64u * kWaves) {
       const uint32_t q = q0 + static_cast<uint32_t>(lane);
       const uint32_t row = fdiv(q, p.chunks_per_row), col = q - row * cpr;
       uint32_t src = kOutOfRange;
-      if (q < chunks && col * 8u < static_cast<uint32_t>(p.L)) {
+      if (q < data && col * 8u < static_cast<uint32_t>(p.L)) {
         uint32_t r;
         if constexpr (UP) {
           r = fdiv(plan.sorted[ps.first + row], p.topk);
@@ -348,13 +462,30 @@ __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
 
   f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
   Scale raw[S];
-  int c_pass = first_pass, c_group = first_group, c_unit = 0;
+  int c_pass = first_pass, c_group = first_group, c_unit = 0, turn = 0;
   // FP4: the expert's FP32 scale, read ahead of the pass's rows and waited for
   // with them (a load where a tile ends would wait for every weight load
   // before it)
   Pass ps = read_pass(plan.list, c_pass);
   float gs = FP8 ? 1.0f : p.g[ps.expert];
   fill(ps);
+  // where the lane reads its token row: dense (and FP8) rows past the pass's
+  // tokens repeat the last one, and their results are dropped
+  bool diag;
+  lds_cbytes a_lane, zero;
+  uint32_t a_step, lo_plane;
+  auto place = [&]() {
+    const lds_cbytes base = (lds_cbytes)rows_lds;
+    lo_plane = static_cast<uint32_t>(ps.tokens) * pitch;  // from a token's high part to its remainder
+    zero = base + PLANES * lo_plane;
+    diag = !FP8 && ps.tokens <= 4;
+    const int m = diag ? li >> 2 : min(li, ps.tokens - 1);
+    const bool carries = !diag || ((li & 3) == g && m < ps.tokens);
+    a_lane = carries ? base + static_cast<uint32_t>(m) * pitch + (FP8 ? 32u : 64u) * g : zero;
+    a_step = carries ? 256u : 0u;
+    if (!carries) lo_plane = 0u;
+  };
+  place();
 #pragma unroll
   for (int d = 0; d < D; ++d) load(raw[d], ring + d * kUnitBytes);
   wait_vm<D * LPU>();  // the fill is older
@@ -365,87 +496,46 @@ __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
   auto consume = [&](const Scale& sc, const unsigned char* slot) {
     const int u = ks * p.units + c_unit;
     wait_vm<D * LPU>();  // this unit's weights have landed
-    // rows past the pass's tokens repeat the last one; their results are dropped
-    const unsigned char* arow = rows_lds + static_cast<uint32_t>(min(li, ps.tokens - 1)) * pitch;
-    const uint32_t lo_plane = static_cast<uint32_t>(ps.tokens) * pitch;
-    if constexpr (FP8) {
-      if (u < NW) {
-        const unsigned char* q = arow + 256u * u + 32u * g;
-        u32x4 w0 = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * (g ^ sw));
-        u32x4 w1 = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * ((4 + g) ^ sw));
-        // a last window of 64 k: the bytes past the row are the next row's
-        if (128 * u + 64 >= p.L) w1 = u32x4{0u, 0u, 0u, 0u};
-        const V b0 = Tr::decode8_fp8(w0.x, w0.y), b1 = Tr::decode8_fp8(w0.z, w0.w);
-        const V b2 = Tr::decode8_fp8(w1.x, w1.y), b3 = Tr::decode8_fp8(w1.z, w1.w);
-        f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int pl = 0; pl < PLANES; ++pl) {
-          const unsigned char* qp = q + pl * lo_plane;
-          d = Tr::mfma(*reinterpret_cast<const V*>(qp), b0, d);
-          d = Tr::mfma(*reinterpret_cast<const V*>(qp + 16), b1, d);
-          d = Tr::mfma(*reinterpret_cast<const V*>(qp + 128), b2, d);
-          d = Tr::mfma(*reinterpret_cast<const V*>(qp + 144), b3, d);
-        }
-        const float s = __builtin_bit_cast(float, sc);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = fmaf(d[i], s, acc[i]);
-      }
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int w = 2 * u + h;
-        if (w < NW) {
-          const unsigned char* q = arow + 256u * w + 64u * g;
-          const u32x4 wv = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * ((4 * h + g) ^ sw));
-          // E4M3 scales of the lane's blocks 2g and 2g + 1 of the window;
-          // blocks past the row (the next row's bytes) count as zero
-          const uint32_t s4 = (g & 2) ? sc[2 * h + 1] : sc[2 * h];
-          uint32_t s2 = s4 >> (16 * (g & 1));
-          if (128 * w + 64 >= p.L && g >= 2) s2 = 0;
-          const f32x2 sf = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s2), false);
-          const typename Tr::scale_t sa = Tr::make_scale(sf.x), sb = Tr::make_scale(sf.y);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const V b = Tr::decode8(wv[i], i < 2 ? sa : sb);
-#pragma unroll
-            for (int pl = 0; pl < PLANES; ++pl)
-              acc = Tr::mfma(*reinterpret_cast<const V*>(q + pl * lo_plane + 16 * i), b, acc);
-          }
-        }
-      }
-    }
+    if constexpr (FP8)
+      fp8_unit<Tr, PLANES>(acc, sc, slot, a_lane, zero, lo_plane, u, NW, p.L, li, g);
+    else if (diag)
+      fp4_unit<Tr, PLANES, true>(acc, sc, slot, a_lane, a_step, zero, lo_plane, u, NW, p.L, li, g);
+    else
+      fp4_unit<Tr, PLANES, false>(acc, sc, slot, a_lane, a_step, zero, lo_plane, u, NW, p.L, li, g);
     if (++c_unit < p.units) return;
     // end of a tile: join the K split, then the epilogue
     c_unit = 0;
     if (KS > 1) {
-      *reinterpret_cast<f32x4*>(red + wave * 1024 + 16 * lane) = acc;
+      // the two halves of `red` are used in turn, so one barrier is enough: a
+      // half is written again after a barrier that its readers reach later
+      unsigned char* part = red + turn * (kRedBytes / 2) + wave * 1024 + 16 * lane;
+      turn ^= 1;
+      *reinterpret_cast<f32x4*>(part) = acc;
       lds_barrier();
       if (ks == 0) {
 #pragma unroll
-        for (int v = 1; v < KS; ++v) acc += *reinterpret_cast<const f32x4*>(red + (wave + v) * 1024 + 16 * lane);
+        for (int v = 1; v < KS; ++v) acc += *reinterpret_cast<const f32x4*>(part + v * 1024);
       }
-      lds_barrier();
     }
     const int t = c_group * TPW + tw;
     if (ks == 0 && t < p.tiles) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 4 * g + r;
+      auto finish = [&](float v, int row) {
         if constexpr (UP) {
-          const float up = swap8(acc[r]);
+          const float up = swap8(v);
           if (row < ps.tokens && li < 8) {
             const size_t at = static_cast<size_t>(plan.sorted[ps.first + row]) * (p.N >> 1) + 8 * t + li;
-            const float h = gated(p.act, acc[r] * gs, up * gs);
-            const __bf16 top = static_cast<__bf16>(h);
-            __bf16* out = static_cast<__bf16*>(p.out);
-            out[at] = top;
-            // the remainder is exact in FP32; where the high part is infinite or NaN it adds nothing
-            const float rest = h - static_cast<float>(top);
-            out[at + static_cast<size_t>(p.n) * (p.N >> 1)] = static_cast<__bf16>(__builtin_isfinite(rest) ? rest : 0.0f);
+            store_h(static_cast<__bf16*>(p.out) + at, static_cast<size_t>(p.n) * (p.N >> 1),
+                    gated(p.act, v * gs, up * gs));
           }
         } else if (row < ps.tokens) {
-          static_cast<float*>(p.out)[static_cast<size_t>(plan.sorted[ps.first + row]) * p.N + 16 * t + li] = acc[r] * gs;
+          static_cast<float*>(p.out)[static_cast<size_t>(plan.sorted[ps.first + row]) * p.N + 16 * t + li] = v * gs;
         }
+      };
+      if (diag) {
+        finish(acc[0], g);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) finish(acc[r], 4 * g + r);
       }
     }
     acc = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -467,6 +557,7 @@ __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
           if (!FP8) gs = p.g[ps.expert];
           lds_barrier();
           fill(ps);
+          place();
           wait_vm<0>();
           __asm__ volatile("" : "+v"(gs));
           __builtin_amdgcn_s_barrier();
@@ -481,7 +572,9 @@ __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
 }
 
 // ---------------------------------------------------------------- one token
-//
+
+constexpr uint32_t kTokenRedBytes = 1024;  // 2 x 8 waves x 16 floats
+
 // M = 1: assignment j is choice j of the only token, so no plan is made: a
 // pass is a choice, its token row is A for every choice (up) and row j of H
 // (down).  What counts is the chain of latencies (launch, ids, first weights,
@@ -489,8 +582,7 @@ __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
 // the chip holds, and down gives a workgroup whole column tiles, with the
 // choices spread over its waves, and adds them up itself: no third kernel.
 //
-// The token fills MFMA row 0, in down its H's remainder row 1, so both planes
-// take one MFMA; the other rows repeat them and are dropped.
+// In down the two planes of H are two rows of one operand, not two MFMAs.
 
 // up: grid-stride over (choice, group); down: over tiles.
 template <typename T, bool FP8, bool UP, int KS, int D>
@@ -503,6 +595,7 @@ __global__ __launch_bounds__(kThreads) void moe_token_kernel(const MoeParams p, 
   constexpr int S = D + 1;
   constexpr int UW = FP8 ? 1 : 2;
   constexpr int LPU = 3;
+  constexpr int ROWS = UP ? 1 : 2;  // operand rows of a choice
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -511,18 +604,17 @@ __global__ __launch_bounds__(kThreads) void moe_token_kernel(const MoeParams p, 
   const int ks = wave % KS, tw = wave / KS;
   unsigned char* ring = smem + static_cast<uint32_t>(wave) * (S * kUnitBytes);
   unsigned char* red = smem + kWaves * S * kUnitBytes;
-  unsigned char* rows_lds = red + kRedBytes;
+  unsigned char* rows_lds = red + kTokenRedBytes;
   const int NW = (p.L + 127) >> 7;
   const int NU = (NW + UW - 1) / UW;
   const uint32_t row_bytes = FP8 ? static_cast<uint32_t>(p.L) : static_cast<uint32_t>(p.L >> 1);
   const uint32_t srow_bytes = FP8 ? 4u * p.cols : static_cast<uint32_t>(p.cols);
   const uint32_t half = UP ? static_cast<uint32_t>(p.N >> 1) : 8u;
   const uint32_t tile_rows = UP ? 8u : 16u;
-  const uint32_t pitch = static_cast<uint32_t>(NW) * 256u + 16u;
+  const uint32_t pitch = static_cast<uint32_t>(NW) * 256u + 16u;  // LDS bytes of a row
   const uint32_t wl = lr * row_bytes + 16u * (lc ^ lr);
   const uint32_t wl8 = wl + half * row_bytes;
   const uint32_t sl = (li < 8 ? li : li - 8 + half) * srow_bytes;
-  const int sw = li & 7;
 
   // The wave's sequence.  up: items (choice, group) b, b + grid, ..; wave
   // (tw, ks) takes tile group * TPW + tw.  down: tiles b, b + grid, .. and in
@@ -587,11 +679,11 @@ __global__ __launch_bounds__(kThreads) void moe_token_kernel(const MoeParams p, 
   {
     const rsrc_t x_rsrc = make_rsrc(p.x, static_cast<uint32_t>(p.x_bytes));
     const uint32_t cpr = p.chunks_per_row.d;
-    const uint32_t chunks = (UP ? 1u : 2u * p.n) * cpr;
+    const uint32_t data = (UP ? 1u : 2u * p.n) * cpr, chunks = data + 16u;  // and the zero block
     for (uint32_t q0 = 64u * static_cast<uint32_t>(wave); q0 < chunks; q0 += 64u * kWaves) {
       const uint32_t q = q0 + static_cast<uint32_t>(lane);
       const uint32_t row = fdiv(q, p.chunks_per_row), col = q - row * cpr;
-      const bool in = q < chunks && col * 8u < static_cast<uint32_t>(p.L);
+      const bool in = q < data && col * 8u < static_cast<uint32_t>(p.L);
       buf_load_lds<16>(x_rsrc, in ? row * (2u * p.L) + 16u * col : kOutOfRange, rows_lds + 16u * q0);
     }
   }
@@ -610,46 +702,24 @@ __global__ __launch_bounds__(kThreads) void moe_token_kernel(const MoeParams p, 
     const int u = ks * p.units + c_unit;
     const int j = choice_of(c_item, c_in);
     wait_vm<D * LPU>();
-    const unsigned char* arow =
-        UP ? rows_lds : rows_lds + static_cast<uint32_t>((li & 1) * p.n + min(j, p.n - 1)) * pitch;
-    if constexpr (FP8) {
-      if (u < NW) {
-        const unsigned char* q = arow + 256u * u + 32u * g;
-        const u32x4 w0 = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * (g ^ sw));
-        u32x4 w1 = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * ((4 + g) ^ sw));
-        if (128 * u + 64 >= p.L) w1 = u32x4{0u, 0u, 0u, 0u};  // the next row's bytes
-        f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
-        d = Tr::mfma(*reinterpret_cast<const V*>(q), Tr::decode8_fp8(w0.x, w0.y), d);
-        d = Tr::mfma(*reinterpret_cast<const V*>(q + 16), Tr::decode8_fp8(w0.z, w0.w), d);
-        d = Tr::mfma(*reinterpret_cast<const V*>(q + 128), Tr::decode8_fp8(w1.x, w1.y), d);
-        d = Tr::mfma(*reinterpret_cast<const V*>(q + 144), Tr::decode8_fp8(w1.z, w1.w), d);
-        const float s = __builtin_bit_cast(float, sc);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) acc[i] = fmaf(d[i], s, acc[i]);
-      }
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int w = 2 * u + h;
-        if (w < NW) {
-          const unsigned char* q = arow + 256u * w + 64u * g;
-          const u32x4 wv = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * ((4 * h + g) ^ sw));
-          const uint32_t s4 = (g & 2) ? sc[2 * h + 1] : sc[2 * h];
-          uint32_t s2 = s4 >> (16 * (g & 1));
-          if (128 * w + 64 >= p.L && g >= 2) s2 = 0;
-          const f32x2 sf = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s2), false);
-          const typename Tr::scale_t sa = Tr::make_scale(sf.x), sb = Tr::make_scale(sf.y);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc = Tr::mfma(*reinterpret_cast<const V*>(q + 16 * i), Tr::decode8(wv[i], i < 2 ? sa : sb), acc);
-        }
-      }
-    }
+    // row m of the operand: up 0: the token; down 0 and 1: the choice's two
+    // planes.  FP4: block-diagonal, so lane groups 0 and 1 end with the rows'
+    // sums in acc[0]; FP8: lane rows m, group 0 ends with them in acc[0 ..].
+    const int m = FP8 ? li & (ROWS - 1) : li >> 2;
+    const bool carries = FP8 || ((li & 3) == g && m < ROWS);
+    const lds_cbytes base = (lds_cbytes)rows_lds;
+    const lds_cbytes zero = base + static_cast<uint32_t>(UP ? 1 : 2 * p.n) * pitch;
+    const uint32_t row = UP ? 0u : static_cast<uint32_t>(m * p.n + min(j, p.n - 1));
+    const lds_cbytes a_lane = carries ? base + row * pitch + (FP8 ? 32u : 64u) * g : zero;
+    if constexpr (FP8)
+      fp8_unit<Tr, 1>(acc, sc, slot, a_lane, zero, 0u, u, NW, p.L, li, g);
+    else
+      fp4_unit<Tr, 1, true>(acc, sc, slot, a_lane, carries ? 256u : 0u, zero, 0u, u, NW, p.L, li, g);
     if (++c_unit < p.units) return;
     c_unit = 0;
     const int e = expert_of(j);
-    // row 0 (and 1) of the result lie in lanes g == 0
-    float v = UP ? acc[0] : acc[0] + acc[1];
+    float v = acc[0];  // lanes g == 0 hold the tile
+    if (!UP) v += FP8 ? acc[1] : __shfl_xor(acc[0], 16, 64);
     acc = f32x4{0.f, 0.f, 0.f, 0.f};
     if constexpr (!UP) {
       if (e >= 0) sum = fmaf(v * value_of(g_lane, j), value_of(w_lane, j), sum);
@@ -679,12 +749,8 @@ __global__ __launch_bounds__(kThreads) void moe_token_kernel(const MoeParams p, 
         const float up = swap8(v);
         if (e >= 0 && t < p.tiles && li < 8) {
           const float gs = value_of(g_lane, j);
-          const float hv = gated(p.act, v * gs, up * gs);
-          const __bf16 top = static_cast<__bf16>(hv);
-          const float rest = hv - static_cast<float>(top);
-          __bf16* out = static_cast<__bf16*>(p.out) + static_cast<size_t>(j) * (p.N >> 1) + 8 * t + li;
-          out[0] = top;
-          out[static_cast<size_t>(p.n) * (p.N >> 1)] = static_cast<__bf16>(__builtin_isfinite(rest) ? rest : 0.0f);
+          store_h(static_cast<__bf16*>(p.out) + static_cast<size_t>(j) * (p.N >> 1) + 8 * t + li,
+                  static_cast<size_t>(p.n) * (p.N >> 1), gated(p.act, v * gs, up * gs));
         }
       } else {
         static_cast<T*>(p.out)[16 * t + li] = round_to<T>(v);
@@ -767,9 +833,24 @@ size_t fixed_lds(int depth, int n, int E, int list_max) {
   return static_cast<size_t>(kWaves) * (depth + 1) * kUnitBytes + kRedBytes + plan_bytes(n, E, list_max);
 }
 
-// Token rows of `planes` planes, in whole direct-load instructions.
+// Token rows of `planes` planes and the zero block, in whole direct-load instructions.
 size_t rows_lds_bytes(int rows, int planes, int NW) {
-  return (static_cast<size_t>(rows) * planes * (static_cast<size_t>(NW) * 256 + 16) + 1023) / 1024 * 1024;
+  return (static_cast<size_t>(rows) * planes * (static_cast<size_t>(NW) * 256 + 16) + 256 + 1023) / 1024 * 1024;
+}
+
+// The K split of a tile over KS waves.  The larger it is, the smaller the
+// groups of tiles that are shared out and the better the shares' bytes match,
+// but every tile then ends with a join: measured (us of a layer; the split of
+// up) FP4 K = 7168, 28 units of a row: 152 at 1, 142 at 2, 139 at 4, 137 at 8;
+// FP4 K = 2048, 8 units: 73.6, 73.9, 80.9, 88.5; FP8 K = 4096, 32 units: 185,
+// 175, 173, 172; FP8 I = 1024 (down), 8 units: 171.7, 170.2, 173.0, 180.7.  So:
+// the largest split that leaves a wave four units of a tile, and beyond that
+// only as far as the workgroups would not fill the chip.
+int k_split(int NU, int64_t tiles, int64_t passes, int64_t cus) {
+  int ks = 1;
+  while (ks < kWaves && NU >= 8 * ks) ks *= 2;
+  while (ks < kWaves && NU >= 2 * ks && passes * ((tiles + kWaves / ks - 1) / (kWaves / ks)) < cus) ks *= 2;
+  return ks;
 }
 
 // The launch of one kernel: rows per pass, ring depth and K split.  False
@@ -794,23 +875,13 @@ bool plan_shape(const MoeArgs& a, bool fp8, bool up, Shape* out) {
       const size_t lds = fixed_lds(depth, static_cast<int>(n), static_cast<int>(a.E), static_cast<int>(list_max)) +
                          rows_lds_bytes(static_cast<int>(rows), planes, NW);
       if (lds > kMaxLds) continue;
-      // K split: least work on the busiest wave, rounds of groups times units
-      // per wave (with what padding a split leaves) and one for a tile's end
       const int64_t tiles = up ? a.I / 8 : a.K / 16;
       const int64_t passes = n < a.E ? n : a.E;
       const int64_t cus = device_cus();
-      int64_t best = -1;
-      for (int ks : {1, 2, 4, 8}) {
-        if (ks > 1 && NU < ks) break;
-        const int64_t groups = (tiles + kWaves / ks - 1) / (kWaves / ks);
-        const int64_t units = (NU + ks - 1) / ks;
-        const int64_t cost = (passes * groups + cus - 1) / cus * (units + 1);
-        if (best < 0 || cost < best) {
-          best = cost;
-          *out = Shape{static_cast<int>(rows), depth, ks, static_cast<int>(passes * groups < cus ? passes * groups : cus),
-                       static_cast<int>(units), static_cast<int>(groups), static_cast<int>(list_max), lds};
-        }
-      }
+      const int ks = k_split(NU, tiles, passes, cus);
+      const int64_t groups = (tiles + kWaves / ks - 1) / (kWaves / ks);
+      *out = Shape{static_cast<int>(rows), depth, ks, static_cast<int>(passes * groups < cus ? passes * groups : cus),
+                   (NU + ks - 1) / ks, static_cast<int>(groups), static_cast<int>(list_max), lds};
       return true;
     }
   }
@@ -863,28 +934,18 @@ void launch_token_ks(const MoeParams& p, const float* weights, int ks, int grid,
 // M = 1.  False where the rows do not fit in LDS beside the rings.
 template <typename T, bool FP8>
 bool launch_token(const MoeArgs& a, MoeParams up, MoeParams down, hipStream_t st) {
-  const size_t base = kWaves * 5 * kUnitBytes + kRedBytes;
+  const size_t base = kWaves * 5 * kUnitBytes + kTokenRedBytes;
   const int cus = device_cus();
   const int up_nw = static_cast<int>((a.K + 127) / 128), down_nw = static_cast<int>((a.I + 127) / 128);
   const size_t up_lds = base + rows_lds_bytes(1, 1, up_nw);
   const size_t down_lds = base + rows_lds_bytes(static_cast<int>(a.topk), 2, down_nw);
   if (up_lds > kMaxLds || down_lds > kMaxLds) return false;
   const int up_nu = FP8 ? up_nw : (up_nw + 1) / 2, down_nu = FP8 ? down_nw : (down_nw + 1) / 2;
-  // up: as for several tokens, the K split with the least work on a wave
-  int up_ks = 1, up_grid = 1;
-  int64_t best = -1;
-  for (int ks : {1, 2, 4, 8}) {
-    if (ks > 1 && up_nu < ks) break;
-    const int64_t groups = (up.tiles + kWaves / ks - 1) / (kWaves / ks), units = (up_nu + ks - 1) / ks;
-    const int64_t rounds = (a.topk * groups + cus - 1) / cus;
-    if (best < 0 || rounds * (units + 1) < best) {
-      best = rounds * (units + 1);
-      up_ks = ks;
-      up.groups = static_cast<int>(groups);
-      up.units = static_cast<int>(units);
-      up_grid = static_cast<int>((a.topk * groups + rounds - 1) / rounds);
-    }
-  }
+  const int up_ks = k_split(up_nu, up.tiles, a.topk, cus);
+  up.groups = (up.tiles + kWaves / up_ks - 1) / (kWaves / up_ks);
+  up.units = (up_nu + up_ks - 1) / up_ks;
+  const int up_items = static_cast<int>(a.topk) * up.groups, up_rounds = (up_items + cus - 1) / cus;
+  const int up_grid = (up_items + up_rounds - 1) / up_rounds;
   // down: a wave per choice, the waves that this leaves split the sum
   const int down_ks = a.topk > 4 ? 1 : a.topk > 2 ? 2 : a.topk > 1 ? 4 : 8;
   down.units = (down_nu + down_ks - 1) / down_ks;
