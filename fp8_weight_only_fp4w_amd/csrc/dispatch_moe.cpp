@@ -53,9 +53,10 @@ bool stream_ok(bool fp8, const MoeArgs& a) {
          aligned(a.Y, 16);
 }
 
-// H (4 bytes a value), then the outputs of the single choices in FP32
+// H (4 bytes a value), then the outputs of the single choices in FP32, once
+// for each part of the sum over I
 int64_t workspace_bytes(int64_t M, int64_t topk, int64_t K, int64_t I) {
-  return align256(M * topk * I * 4) + align256(M * topk * K * 4);
+  return align256(M * topk * I * 4) + fp4w::moe_down_splits(M, I) * align256(M * topk * K * 4);
 }
 
 int run_moe(bool fp8, MoeArgs a, int64_t work_bytes, int path) {

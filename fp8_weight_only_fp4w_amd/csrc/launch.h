@@ -207,6 +207,13 @@ int launch_block_norm(const BlockNormArgs& a, bool vec);
 // M, topk > 0, topk <= 64, E <= 1024.
 int launch_moe_route(const MoeRouteArgs& a);
 
+// Parts that the second product's sum over I may be cut into, at most, for M
+// tokens (each part has outputs of its own in the workspace): 32 (or M) token
+// rows of two BF16 planes have to fit in LDS.
+inline int64_t moe_down_splits(int64_t M, int64_t I) {
+  const int64_t rows = M < 32 ? M : 32, bytes = rows * 4 * I, parts = (bytes + (112 << 10) - 1) / (112 << 10);
+  return parts < 1 ? 1 : parts < 4 ? parts : 4;
+}
 // n = M * topk in 1 .. 4096, E in 1 .. 1024, K % 64 == 0, I % 64 == 0 (both >
 // 0), block_size 16 (FP4) or a multiple of 128 (FP8); A, w13, w2, work and Y
 // 16-byte aligned, scales 4-byte; A, an expert's matrices and n x I x 4 below

@@ -4,10 +4,17 @@
 //   Y[m, n] = RNE_T( sum_j weights[a] * (H[a] . W2[e][n]) )
 //
 // Memory-bound: every chosen expert is read once per pass of up to `rows`
-// tokens, in whole 128-byte lines, as the decode GEMV reads a single weight
-// matrix.  Three kernels: up (H from A), down (each choice's output from H)
+// tokens.  Three kernels: up (H from A), down (each choice's output from H)
 // and combine (their weighted sum over a token's choices in the order of j, so
-// the result does not depend on scheduling).
+// the result does not depend on scheduling); a single token takes two.
+//
+// Weights go straight to registers.  A wave owns a tile of 16 weight rows, and
+// a unit is 128 bytes of each: lane (li, g) loads chunks g and 4 + g (16 bytes
+// each) of row li, its MFMA operand as it stands.  Each of the two loads
+// touches half of every line, but back to back they make whole-line requests:
+// this pattern alone streams 5.9 TB/s (5.8 where rows start off a line), the
+// rate of whole-line loads, with four units in flight on 8 waves a CU, and it
+// leaves all of LDS to the token rows.
 //
 // Plan.  ids live on the device, so which experts are read is only known
 // there.  Every workgroup of up and down sorts the assignments by expert in
@@ -16,20 +23,23 @@
 // (pass, group of column tiles); workgroup b of the persistent grid takes a
 // contiguous share, so it meets few experts.
 //
-// A pass's token rows are copied to LDS once (zero-padded to whole 128-k
-// windows) and shared by the 8 waves: KS waves split the sum of one column
-// tile, 8 / KS tiles run side by side.  A wave streams its weights through a
-// private LDS ring of direct loads, D units of 2 KiB ahead of the multiply
-// (unit: 128 bytes of 16 rows, loaded as two instructions of 8 rows x 128
-// bytes, chunks XOR-swizzled by row), across tiles and passes without a
-// break.  The up kernel's 16 rows are 8 gate rows and the 8 up rows that
-// belong to them, so both halves of a product meet in one tile.
+// A pass's token rows are copied to LDS once (zero-padded to whole units) and
+// shared by the 8 waves: KS waves split the sum of one column tile, 8 / KS
+// tiles run side by side, and each wave's loads run Q units ahead across tiles
+// and passes.  Where LDS holds two passes' rows the next ones are fetched
+// while this pass is multiplied.  The up kernel's 16 rows are 8 gate rows and
+// the 8 up rows that belong to them, so both halves of a product meet in one
+// tile.  The down kernel may cut the sum over I into `splits` parts, each a
+// pass of its own with its own outputs: its token rows have two planes, and
+// rows that do not fit in LDS would mean passes that read the weights again.
 //
 // Operands (16x16x32 MFMA; lane li = l % 16 is token row for A and weight row
 // for B, lane group g = l / 16 selects 8 of a step's 32 k; the result lane
 // holds column li, token rows 4g .. 4g + 3).
-//  * FP4: E2M1 x E4M3 is exact in FP16 and BF16, so a weight is decoded with
-//    its block scale folded in; the expert's FP32 scale is applied to the sum.
+//  * FP4, more than 4 tokens: E2M1 x E4M3 is exact in FP16 and BF16, so a
+//    weight is decoded with its block scale folded in; the expert's FP32
+//    scale is applied to the sum.
+//  * FP4, up to 4 tokens: the decode GEMV's block-diagonal operand (below).
 //  * FP8: E4M3 -> T is exact, a 128-k window (inside one scale block) is summed
 //    in a fresh accumulator and added times its FP32 scale.
 //
@@ -40,7 +50,9 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "device.h"
 #include "launch.h"
@@ -51,7 +63,8 @@ namespace {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = 64 * kWaves;
-constexpr uint32_t kUnitBytes = 2048;  // 16 rows x 128 bytes
+constexpr int Q = 4;          // units a wave has in flight
+constexpr int kMaxRows = 32;  // tokens of a pass, at most: two MFMA row tiles
 
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -61,8 +74,7 @@ __device__ __forceinline__ void wait_vm() {
   __asm__ volatile("" ::: "memory");
 }
 
-// Barrier for data exchanged by ds_write / ds_read only: direct loads stay in
-// flight.
+// Barrier for data exchanged by ds_write / ds_read only: loads stay in flight.
 __device__ __forceinline__ void lds_barrier() {
   __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
@@ -73,28 +85,46 @@ struct MoeParams {
   const uint8_t* s;     // [E, N, cols] scales
   const float* g;       // FP4: per expert
   const int32_t* ids;   // [n]
-  void* out;            // up: H planes, BF16 [2][n][I]; down: FP32 [n][K]
+  void* out;            // up: H planes, BF16 [2][n][I]; down: FP32 [splits][n][K]
   FastDiv topk, win_per_block, chunks_per_row;  // chunks_per_row: 16-byte chunks of an LDS row
+  FastDiv by_rows, by_grid, by_groups, by_splits;
   int n, E, L, N, cols;
   int x_bytes;          // up: M * L * 2; down: 2 * n * L * 2
   int rows;             // tokens per pass
   int tiles, groups;    // column tiles of an expert, and groups of TPW of them
-  int units;            // per wave and tile
+  int splits;           // down: parts of the sum over I (up: 1)
+  int fp8;
+  int split_units;      // units of a row in a part
+  int units;            // of those, per wave and tile
+  int buffers;          // 2: LDS holds two passes' rows
   int act;
   int list_max;         // passes at most
 };
 
-// LDS: unit rings, partial sums of the K split, then the plan and the token rows.
-constexpr uint32_t kRedBytes = 2 * kWaves * 1024;
+// Partial sums of the K split, twice: 16 rows a wave, or (FP4, where no pass
+// has more than 4 tokens) the block-diagonal form's one value a lane.
+__host__ __device__ constexpr uint32_t red_stride_of(bool fp8, int rows) { return !fp8 && rows <= 4 ? 256u : 1024u; }
+
+// What a group of tiles costs in a pass of `tokens` tokens, in sixths of one
+// that only waits for memory: the dense forms are bound by their arithmetic
+// (measured per unit, 8 waves a CU: FP4 block-diagonal 0.75 us, dense 1.0,
+// with a second row tile 1.37).  Shares of equal cost end together, where
+// shares of equal bytes let the others wait a quarter of the kernel.
+__device__ __forceinline__ uint32_t pass_cost(int fp8, uint32_t tokens) {
+  return fp8 ? (tokens > 16 ? 7u : 6u) : tokens > 16 ? 11u : tokens > 4 ? 8u : 6u;
+}
+constexpr int64_t kMostCost = 11;
 
 struct Plan {
   const uint32_t* list;    // pass: expert | first sorted assignment << 10 | (tokens - 1) << 22
+  const uint32_t* before;  // cost of the passes before it
   const uint16_t* sorted;  // assignments, by expert
   int passes;
+  uint32_t cost;           // of all passes
 };
-// list and multi [list_max], count [E], part [16], sorted and expert [n]
+// list, before and multi [list_max], count [E], part [2 kWaves + 4], sorted and expert [n]
 constexpr uint32_t plan_bytes(int n, int E, int list_max) {
-  return (8u * list_max + 4u * E + 4u * 16u + 4u * n + 15u) & ~15u;
+  return (12u * list_max + 4u * E + 4u * (2u * kWaves + 4u) + 4u * n + 15u) & ~15u;
 }
 
 // Sum over this lane and those below it.
@@ -112,22 +142,32 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 }
 
 // The passes of one expert whose assignments are sorted[at ..].
-__device__ __forceinline__ void write_passes(uint32_t* list, uint32_t slot, uint32_t e, uint32_t at, uint32_t tokens,
-                                             uint32_t rows) {
+__device__ __forceinline__ void write_passes(const MoeParams& p, uint32_t* list, uint32_t* before, uint32_t slot,
+                                             uint32_t cost, uint32_t e, uint32_t at, uint32_t tokens) {
   for (; tokens; ++slot) {
-    const uint32_t t = tokens < rows ? tokens : rows;
+    const uint32_t t = min(tokens, static_cast<uint32_t>(p.rows));
     list[slot] = e | at << 10 | (t - 1) << 22;
+    before[slot] = cost;
+    cost += pass_cost(p.fp8, t);
     at += t;
     tokens -= t;
   }
 }
+__device__ __forceinline__ uint32_t passes_cost(const MoeParams& p, uint32_t tokens) {
+  const uint32_t rows = static_cast<uint32_t>(p.rows), full = fdiv(tokens, p.by_rows), rest = tokens - full * rows;
+  return full * pass_cost(p.fp8, rows) + (rest ? pass_cost(p.fp8, rest) : 0u);
+}
 
-// n <= 64: every wave makes the whole plan by itself, one assignment a lane,
-// and writes it to LDS (all the same values), so no barrier is needed.
-// Experts come in the order of their first assignment.
+// n <= kWavePlan: every wave makes the whole plan by itself, one assignment a
+// lane, and writes it to LDS (all the same values), so no barrier is needed.
+// Experts come in the order of their first assignment.  The loop over the
+// lanes takes about 55 ns an assignment, the other plan 1.0 us up to some
+// hundred: they meet at 16.
+constexpr int kWavePlan = 16;
 __device__ __forceinline__ Plan make_plan_wave(const MoeParams& p, unsigned char* mem) {
   uint32_t* list = reinterpret_cast<uint32_t*>(mem);
-  uint16_t* sorted = reinterpret_cast<uint16_t*>(list + p.list_max);
+  uint32_t* before = list + p.list_max;
+  uint16_t* sorted = reinterpret_cast<uint16_t*>(before + p.list_max);
   const int lane = threadIdx.x & 63;
   const int id = lane < p.n ? p.ids[lane] : -1;
   int tokens = 0, rank = 0, first = lane;
@@ -139,13 +179,14 @@ __device__ __forceinline__ Plan make_plan_wave(const MoeParams& p, unsigned char
   }
   const bool valid = static_cast<uint32_t>(id) < static_cast<uint32_t>(p.E);
   const bool leads = valid && first == lane;
-  const uint32_t rows = static_cast<uint32_t>(p.rows);
-  const uint32_t mine = leads ? static_cast<uint32_t>(tokens) | (tokens + rows - 1) / rows << 16 : 0u;
-  const uint32_t upto = wave_scan(mine), before = upto - mine;
-  if (leads) write_passes(list, before >> 16, static_cast<uint32_t>(id), before & 0xFFFF, tokens, rows);
-  const uint32_t at = __shfl(before, first, 64) & 0xFFFF;
-  if (valid) sorted[at + rank] = static_cast<uint16_t>(lane);
-  return Plan{list, sorted, static_cast<int>(static_cast<uint32_t>(__builtin_amdgcn_readlane(upto, 63)) >> 16)};
+  const uint32_t mine = leads ? static_cast<uint32_t>(tokens) | fdiv(tokens + p.rows - 1, p.by_rows) << 16 : 0u;
+  const uint32_t cost = leads ? passes_cost(p, tokens) : 0u;
+  const uint32_t upto = wave_scan(mine), cost_upto = wave_scan(cost), at = (upto - mine) & 0xFFFF;
+  if (leads) write_passes(p, list, before, (upto - mine) >> 16, cost_upto - cost, static_cast<uint32_t>(id), at, tokens);
+  const uint32_t first_at = __shfl(at, first, 64);
+  if (valid) sorted[first_at + rank] = static_cast<uint16_t>(lane);
+  return Plan{list, before, sorted, static_cast<int>(static_cast<uint32_t>(__builtin_amdgcn_readlane(upto, 63)) >> 16),
+              static_cast<uint32_t>(__builtin_amdgcn_readlane(cost_upto, 63))};
 }
 
 // All threads of the workgroup; `mem` holds plan_bytes().  Every workgroup
@@ -153,15 +194,16 @@ __device__ __forceinline__ Plan make_plan_wave(const MoeParams& p, unsigned char
 // several passes has its assignments in rising order.
 __device__ __forceinline__ Plan make_plan(const MoeParams& p, unsigned char* mem) {
   uint32_t* list = reinterpret_cast<uint32_t*>(mem);
-  uint32_t* multi = list + p.list_max;  // experts of several passes: expert | first sorted assignment << 10
+  uint32_t* before = list + p.list_max;
+  uint32_t* multi = before + p.list_max;  // experts of several passes: expert | first sorted assignment << 10
   uint32_t* count = multi + p.list_max;
   uint32_t* part = count + p.E;
-  uint16_t* sorted = reinterpret_cast<uint16_t*>(part + 16);
+  uint16_t* sorted = reinterpret_cast<uint16_t*>(part + 2 * kWaves + 4);
   uint16_t* expert = sorted + p.n;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   for (int e = tid; e < p.E; e += kThreads) count[e] = 0;
-  if (tid == 0) part[8] = 0;
+  if (tid == 0) part[2 * kWaves] = 0;
   __syncthreads();
   for (int a = tid; a < p.n; a += kThreads) {
     const uint32_t e = static_cast<uint32_t>(p.ids[a]);
@@ -171,32 +213,41 @@ __device__ __forceinline__ Plan make_plan(const MoeParams& p, unsigned char* mem
   }
   __syncthreads();
   // experts 2 tid and 2 tid + 1 (E <= 1024): tokens in the low half, passes in the high half
-  uint32_t c[2], v[2];
+  uint32_t c[2], v[2], w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     c[i] = 2 * tid + i < p.E ? count[2 * tid + i] : 0u;
-    v[i] = c[i] | ((c[i] + p.rows - 1) / p.rows) << 16;
+    v[i] = c[i] | fdiv(c[i] + p.rows - 1, p.by_rows) << 16;
+    w[i] = passes_cost(p, c[i]);
   }
-  const uint32_t sum = wave_scan(v[0] + v[1]);
-  if (lane == 63) part[wave] = sum;
+  const uint32_t sum = wave_scan(v[0] + v[1]), wsum = wave_scan(w[0] + w[1]);
+  if (lane == 63) {
+    part[wave] = sum;
+    part[kWaves + wave] = wsum;
+  }
   __syncthreads();
-  uint32_t before = sum - v[0] - v[1], total = 0;
+  uint32_t ahead = sum - v[0] - v[1], cost = wsum - w[0] - w[1], total = 0, total_cost = 0;
 #pragma unroll
   for (int i = 0; i < kWaves; ++i) {
-    const uint32_t t = part[i];
-    if (i < wave) before += t;
+    const uint32_t t = part[i], tc = part[kWaves + i];
+    if (i < wave) {
+      ahead += t;
+      cost += tc;
+    }
     total += t;
+    total_cost += tc;
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t e = 2 * tid + i;
     if (c[i]) {
-      const uint32_t at = before & 0xFFFF;
+      const uint32_t at = ahead & 0xFFFF;
       count[e] = at;
-      if (c[i] > static_cast<uint32_t>(p.rows)) multi[atomicAdd(&part[8], 1u)] = e | at << 10;
-      write_passes(list, before >> 16, e, at, c[i], static_cast<uint32_t>(p.rows));
+      if (c[i] > static_cast<uint32_t>(p.rows)) multi[atomicAdd(&part[2 * kWaves], 1u)] = e | at << 10;
+      write_passes(p, list, before, ahead >> 16, cost, e, at, c[i]);
     }
-    before += v[i];
+    ahead += v[i];
+    cost += w[i];
   }
   __syncthreads();
   for (int a = tid; a < p.n; a += kThreads) {
@@ -207,7 +258,7 @@ __device__ __forceinline__ Plan make_plan(const MoeParams& p, unsigned char* mem
   // Within an expert that order is the atomics'.  With one pass it only
   // decides the MFMA row of a token; with several, which pass a token is in,
   // and there every workgroup has to agree: a wave writes them again in order.
-  const int several = __builtin_amdgcn_readfirstlane(part[8]);
+  const int several = __builtin_amdgcn_readfirstlane(part[2 * kWaves]);
   for (int i = wave; i < several; i += kWaves) {
     const uint32_t e = multi[i] & 1023u;
     uint32_t at = multi[i] >> 10;
@@ -219,7 +270,32 @@ __device__ __forceinline__ Plan make_plan(const MoeParams& p, unsigned char* mem
     }
   }
   if (several) __syncthreads();
-  return Plan{list, sorted, static_cast<int>(total >> 16)};
+  return Plan{list, before, sorted, static_cast<int>(static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(total)) >> 16),
+              static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(total_cost))};
+}
+
+// Where share b of the work begins: items (pass, split, group) in order, cut
+// at equal cost.
+struct Place {
+  int pass, item;  // item of the pass
+};
+__device__ __forceinline__ Place share_begin(const MoeParams& p, const Plan& plan, uint32_t b) {
+  const uint32_t per_pass = static_cast<uint32_t>(p.splits * p.groups);
+  const uint32_t all = plan.cost * per_pass, each = fdiv(all, p.by_grid), rest = all - each * p.by_grid.d;
+  const uint32_t x = b * each + min(b, rest);  // < 2^32: the host sees to it
+  if (x >= all) return Place{plan.passes, 0};
+  // the last pass whose cost begins at or before x
+  const int lane = threadIdx.x & 63;
+  int pass = -1;
+  for (int i0 = 0; i0 < plan.passes; i0 += 64) {
+    const bool at = i0 + lane < plan.passes && plan.before[i0 + lane] * per_pass <= x;
+    const int found = __popcll(__ballot(at));
+    pass += found;
+    if (found < 64) break;
+  }
+  const uint32_t begin = __builtin_amdgcn_readfirstlane(plan.before[pass]);
+  const uint32_t end = pass + 1 < plan.passes ? __builtin_amdgcn_readfirstlane(plan.before[pass + 1]) : plan.cost;
+  return Place{pass, static_cast<int>((x - begin * per_pass) / (end - begin))};
 }
 
 struct Pass {
@@ -246,33 +322,143 @@ __device__ __forceinline__ void store_h(__bf16* out, size_t plane, float h) {
 }
 
 // ---- one unit of weights times the token rows
-//
-// a0: the lane's LDS address in window 0 of the high (or only) plane, `step`
-// bytes per window and lo_plane to the other plane (both 0 for a lane that
-// reads the zero block throughout); `zero`: the zero block, for windows past
-// the row.  Every LDS read of the unit is issued before its arithmetic.
 
-// FP4, dense: lane row li carries token li.  A weight is decoded with its
-// block scale (lane group g holds blocks 2g and 2g + 1 of a window): about 86
-// VALU instructions a window, for up to 16 tokens.
-// FP4, DIAG: the decode GEMV's block-diagonal operand, for up to 4 rows.  Row
-// 4 m + q carries row m in the k slots of lane group q only, so the lane (n,
-// g) gets row g's dots with single blocks, scaled by one FMA each: the
-// weights are decoded unscaled, which halves the VALU work.  The sum is
-// acc[0].
-template <typename Tr, int PLANES, bool DIAG>
-__device__ __forceinline__ void fp4_unit(f32x4& acc, const u32x4& sc, const unsigned char* slot, lds_cbytes a0,
-                                         uint32_t step, lds_cbytes zero, uint32_t lo_plane, int u, int NW, int L, int li,
-                                         int g) {
-  typedef typename Tr::vec8 V;
+// A unit's scales: FP4 16 E4M3 bytes, FP8 one FP32 value.
+template <bool FP8>
+using Scale = typename std::conditional<FP8, uint32_t, u32x4>::type;
+
+// A lane's part of one unit: chunks g and 4 + g of its row.  The first of each
+// four units of a tile also brings the scales of all four, lane group g those
+// of unit g: a load per unit would fetch 16 bytes (FP8: 4) of 16 lines each
+// time, and cost as much as half the weights (FP4, K = 2880: 40 of 192 us).
+template <bool FP8>
+struct Unit {
+  u32x4 w[2];
+  Scale<FP8> sc;
+};
+// Loads of any Q = 4 units in a row, at least: two each, and the scales of one
+// (they come with every fourth unit of a tile, and with its first).
+constexpr int kAheadLoads = 2 * Q + 1;
+
+// RING: the weights travel through a private LDS ring instead, Q + 1 slots of a
+// unit, by direct loads of 8 rows x 128 bytes, whose requests are whole lines:
+// that streams 6.4 TB/s against 5.9 straight into registers (FP8, 128 experts
+// of 4096 x 1024: 169 against 181 us), where the token rows leave it 64 KiB
+// of LDS.  A row's chunks are loaded in the order chunk ^ (row & 7), so the
+// reads are free of bank conflicts.
+constexpr uint32_t kSlotBytes = 2048;
+constexpr uint32_t kRingBytes = kWaves * (Q + 1) * kSlotBytes;
+
+template <bool RING>
+struct Lane {
+  uint32_t at, at8;  // offsets in the tile: REG the lane's first chunk; RING its chunks of rows lr and 8 + lr
+};
+template <bool RING>
+__device__ __forceinline__ Lane<RING> lane_offsets(int lane, uint32_t row_bytes, uint32_t half) {
+  if constexpr (RING) {
+    const uint32_t lr = lane >> 3, lc = lane & 7, at = lr * row_bytes + 16u * (lc ^ lr);
+    return Lane<RING>{at, at + half * row_bytes};
+  } else {
+    const uint32_t li = lane & 15, row = li < 8 ? li : li - 8 + half;
+    return Lane<RING>{row * row_bytes + 16u * (lane >> 4), 0u};
+  }
+}
+// asks for unit u of the tile (zeros without `ok`)
+template <bool FP8, bool RING>
+__device__ __forceinline__ void load_weights(Unit<FP8>& un, rsrc_t r, const Lane<RING>& l, int u, bool ok,
+                                             unsigned char* slot) {
+  const uint32_t ub = 128u * static_cast<uint32_t>(u);
+  if constexpr (RING) {
+    buf_load_lds<16>(r, ok ? l.at + ub : kOutOfRange, slot);
+    buf_load_lds<16>(r, ok ? l.at8 + ub : kOutOfRange, slot + 1024);
+  } else {
+    un.w[0] = buf_load_b128(r, ok ? l.at + ub : kOutOfRange);
+    un.w[1] = buf_load_b128(r, ok ? l.at + ub + 64u : kOutOfRange);
+  }
+}
+// RING: the oldest unit's weights to registers, with Q units behind it in
+// flight; its slot is asked for again a step later
+template <bool FP8>
+__device__ __forceinline__ void fetch(Unit<FP8>& un, const unsigned char* slot, int li, int g) {
   const int sw = li & 7;
-  u32x4 wv[2], av[2][PLANES][4];
+  wait_vm<kAheadLoads>();
+  un.w[0] = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * (g ^ sw));
+  un.w[1] = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * ((4 + g) ^ sw));
+}
+
+// The scales change lanes through LDS: a wave's slice has the four units'
+// scales of 16 rows, the rows kSlicePitch apart.
+template <bool FP8>
+constexpr uint32_t kSlicePitch = FP8 ? 20 : 80;
+template <bool FP8>
+constexpr uint32_t kSliceBytes = 16 * kSlicePitch<FP8>;
+template <bool FP8>
+__device__ __forceinline__ Scale<FP8> unit_scales(const Unit<FP8>& un, unsigned char* slice, int unit, int li, int g) {
+  typedef Scale<FP8> S;
+  if ((unit & 3) == 0) *reinterpret_cast<S*>(slice + kSlicePitch<FP8> * li + sizeof(S) * g) = un.sc;
+  return *reinterpret_cast<const S*>(slice + kSlicePitch<FP8> * li + sizeof(S) * (unit & 3));
+}
+
+// Where a lane reads its token rows: window 0 of its row of the first and of
+// the second row tile (high plane), the step per window, the way to the other
+// plane (both 0 for a lane that reads the zero block throughout), and the zero
+// block, for windows past the row.
+struct Rows {
+  lds_cbytes a[2];
+  lds_cbytes zero;
+  uint32_t step, plane;
+};
+
+// FP4, dense: lane row li carries token li (and 16 + li in the second row
+// tile).  Lane group g holds blocks 2g and 2g + 1 of a window; a weight is
+// decoded with its block scale: 67 VALU instructions a window for up to 32
+// tokens, where the block-diagonal form below takes 33 for 4.
+template <typename Tr, int PLANES, int MT>
+__device__ __forceinline__ void fp4_dense(f32x4 (&acc)[2], const Unit<false>& un, const u32x4& sc, const Rows& r, int u,
+                                          int NW, int len, int g) {
+  typedef typename Tr::vec8 V;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int w = 2 * u + h;
-    wv[h] = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * ((4 * h + g) ^ sw));
-    const lds_cbytes q = w < NW ? a0 + step * static_cast<uint32_t>(w) : zero;
-    const uint32_t next = w < NW ? lo_plane : 0u;
+    // E4M3 scales of the window's 8 blocks; blocks past the row (the next
+    // row's bytes) count as zero
+    const uint32_t s_lo = w < NW ? sc[2 * h] : 0u, s_hi = 128 * w + 64 < len ? sc[2 * h + 1] : 0u;
+    const uint32_t s2 = ((g & 2) ? s_hi : s_lo) >> (16 * (g & 1));
+    const f32x2 sf = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s2), false);
+    const typename Tr::scale_t sa = Tr::make_scale(sf.x), sb = Tr::make_scale(sf.y);
+    V b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = Tr::decode8(un.w[h][i], i < 2 ? sa : sb);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const lds_cbytes q = w < NW ? r.a[mt] + r.step * static_cast<uint32_t>(w) : r.zero;
+      const uint32_t next = w < NW ? r.plane : 0u;
+#pragma unroll
+      for (int pl = 0; pl < PLANES; ++pl) {
+        u32x4 av[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) av[i] = *reinterpret_cast<const lds_u32x4*>(q + pl * next + 16 * i);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[mt] = Tr::mfma(__builtin_bit_cast(V, av[i]), b[i], acc[mt]);
+      }
+    }
+  }
+}
+
+// FP4, block-diagonal, for up to 4 operand rows: row 4 m + q carries row m in
+// the k slots of lane group q only, so the lane (n, g) gets row g's dots with
+// single blocks, scaled by one FMA each, and the weights are decoded unscaled.
+// The sum is acc[0][0].
+template <typename Tr, int PLANES>
+__device__ __forceinline__ void fp4_diag(f32x4 (&acc)[2], const Unit<false>& un, const u32x4& sc, const Rows& r, int u,
+                                         int NW, int len) {
+  typedef typename Tr::vec8 V;
+  u32x4 av[2][PLANES][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int w = 2 * u + h;
+    const lds_cbytes q = w < NW ? r.a[0] + r.step * static_cast<uint32_t>(w) : r.zero;
+    const uint32_t next = w < NW ? r.plane : 0u;
 #pragma unroll
     for (int pl = 0; pl < PLANES; ++pl)
 #pragma unroll
@@ -281,172 +467,164 @@ __device__ __forceinline__ void fp4_unit(f32x4& acc, const u32x4& sc, const unsi
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int w = 2 * u + h;
-    // E4M3 scales of the window's 8 blocks; blocks past the row (the next
-    // row's bytes) count as zero
-    const uint32_t s_lo = w < NW ? sc[2 * h] : 0u, s_hi = 128 * w + 64 < L ? sc[2 * h + 1] : 0u;
-    if constexpr (DIAG) {
-      const f32x2 s01 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s_lo), false);
-      const f32x2 s23 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s_lo), true);
-      const f32x2 s45 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s_hi), false);
-      const f32x2 s67 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s_hi), true);
-      const float s8[8] = {s01.x, s01.y, s23.x, s23.y, s45.x, s45.y, s67.x, s67.y};
-      f32x4 d[2];
+    const uint32_t s_lo = w < NW ? sc[2 * h] : 0u, s_hi = 128 * w + 64 < len ? sc[2 * h + 1] : 0u;
+    const f32x2 s01 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s_lo), false);
+    const f32x2 s23 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s_lo), true);
+    const f32x2 s45 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s_hi), false);
+    const f32x2 s67 = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s_hi), true);
+    const float s8[8] = {s01.x, s01.y, s23.x, s23.y, s45.x, s45.y, s67.x, s67.y};
+    f32x4 d[2];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const V b0 = Tr::decode8_fp4(wv[h][2 * s]), b1 = Tr::decode8_fp4(wv[h][2 * s + 1]);
-        d[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < 2; ++s) {
+      const V b0 = Tr::decode8_fp4(un.w[h][2 * s]), b1 = Tr::decode8_fp4(un.w[h][2 * s + 1]);
+      d[s] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int pl = 0; pl < PLANES; ++pl) {
-          d[s] = Tr::mfma(__builtin_bit_cast(V, av[h][pl][2 * s]), b0, d[s]);
-          d[s] = Tr::mfma(__builtin_bit_cast(V, av[h][pl][2 * s + 1]), b1, d[s]);
-        }
-      }
-      // result row r of set s is block 2r + s
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) acc[0] = fmaf(d[s][r], s8[2 * r + s], acc[0]);
-    } else {
-      const uint32_t s2 = ((g & 2) ? s_hi : s_lo) >> (16 * (g & 1));
-      const f32x2 sf = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(s2), false);
-      const typename Tr::scale_t sa = Tr::make_scale(sf.x), sb = Tr::make_scale(sf.y);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const V b = Tr::decode8(wv[h][i], i < 2 ? sa : sb);
-#pragma unroll
-        for (int pl = 0; pl < PLANES; ++pl) acc = Tr::mfma(__builtin_bit_cast(V, av[h][pl][i]), b, acc);
+      for (int pl = 0; pl < PLANES; ++pl) {
+        d[s] = Tr::mfma(__builtin_bit_cast(V, av[h][pl][2 * s]), b0, d[s]);
+        d[s] = Tr::mfma(__builtin_bit_cast(V, av[h][pl][2 * s + 1]), b1, d[s]);
       }
     }
+    // result row q of set s is block 2q + s
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) acc[0][0] = fmaf(d[s][q], s8[2 * q + s], acc[0][0]);
   }
 }
 
 // FP8: a window's sum in a fresh accumulator, added times its FP32 scale.
-// Lane group g takes chunks g and 4 + g (16 k each) of its row's 128 bytes.
-template <typename Tr, int PLANES>
-__device__ __forceinline__ void fp8_unit(f32x4& acc, uint32_t sc, const unsigned char* slot, lds_cbytes a0,
-                                         lds_cbytes zero, uint32_t lo_plane, int u, int NW, int L, int li, int g) {
+template <typename Tr, int PLANES, int MT>
+__device__ __forceinline__ void fp8_window(f32x4 (&acc)[2], const Unit<true>& un, uint32_t sc, const Rows& r, int u,
+                                           int NW, int len) {
   typedef typename Tr::vec8 V;
-  const int sw = li & 7;
-  const u32x4 w0 = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * (g ^ sw));
-  u32x4 w1 = *reinterpret_cast<const u32x4*>(slot + 128 * li + 16 * ((4 + g) ^ sw));
-  const lds_cbytes q = u < NW ? a0 + 256u * static_cast<uint32_t>(u) : zero;
-  const uint32_t next = u < NW ? lo_plane : 0u;
-  u32x4 av[PLANES][4];
-#pragma unroll
-  for (int pl = 0; pl < PLANES; ++pl)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      av[pl][i] = *reinterpret_cast<const lds_u32x4*>(q + pl * next + (i & 1) * 16 + (i >> 1) * 128);
   // a last window of 64 k: the bytes past the row are the next row's
-  if (128 * u + 64 >= L) w1 = u32x4{0u, 0u, 0u, 0u};
-  const V b[4] = {Tr::decode8_fp8(w0.x, w0.y), Tr::decode8_fp8(w0.z, w0.w), Tr::decode8_fp8(w1.x, w1.y),
-                  Tr::decode8_fp8(w1.z, w1.w)};
-  f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
+  const u32x4 w1 = 128 * u + 64 < len ? un.w[1] : u32x4{0u, 0u, 0u, 0u};
+  const V b[4] = {Tr::decode8_fp8(un.w[0].x, un.w[0].y), Tr::decode8_fp8(un.w[0].z, un.w[0].w),
+                  Tr::decode8_fp8(w1.x, w1.y), Tr::decode8_fp8(w1.z, w1.w)};
+  const float s = u < NW ? __builtin_bit_cast(float, sc) : 0.0f;
 #pragma unroll
-  for (int pl = 0; pl < PLANES; ++pl)
+  for (int mt = 0; mt < MT; ++mt) {
+    const lds_cbytes q = u < NW ? r.a[mt] + r.step * static_cast<uint32_t>(u) : r.zero;
+    const uint32_t next = u < NW ? r.plane : 0u;
+    f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d = Tr::mfma(__builtin_bit_cast(V, av[pl][i]), b[i], d);
-  const float s = __builtin_bit_cast(float, sc);
+    for (int pl = 0; pl < PLANES; ++pl) {
+      u32x4 av[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = fmaf(d[i], s, acc[i]);
+      for (int i = 0; i < 4; ++i)
+        av[i] = *reinterpret_cast<const lds_u32x4*>(q + pl * next + (i & 1) * 16 + (i >> 1) * 128);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d = Tr::mfma(__builtin_bit_cast(V, av[i]), b[i], d);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[mt][i] = fmaf(d[i], s, acc[mt][i]);
+  }
 }
+
+// ---------------------------------------------------------------- several tokens
 
 // UP: the first kernel (A of type T against w13), otherwise the second (H
 // planes against w2; its operands are BF16 whatever T is).
-template <typename T, bool FP8, bool UP, int KS, int D>
+template <typename T, bool FP8, bool UP, int KS, bool RING>
 __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
   typedef typename std::conditional<UP, T, __bf16>::type X;
   typedef ActTraits<X> Tr;
-  typedef typename Tr::vec8 V;
-  typedef typename std::conditional<FP8, uint32_t, u32x4>::type Scale;
   constexpr int TPW = kWaves / KS;
-  constexpr int S = D + 1;
-  constexpr int UW = FP8 ? 1 : 2;  // 128-k windows per unit
+  constexpr int UK = FP8 ? 128 : 256;  // k of a unit
   constexpr int PLANES = UP ? 1 : 2;
-  constexpr int LPU = 3;  // loads per unit: scales, then two direct weight loads
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int li = lane & 15, g = lane >> 4;  // fragment side: row li, chunk group g
-  const int lr = lane >> 3, lc = lane & 7;  // load side: row lr of an 8-row half, position lc
+  const int li = lane & 15, g = lane >> 4;  // row li, chunk group g
   const int ks = wave % KS, tw = wave / KS;
-  unsigned char* ring = smem + static_cast<uint32_t>(wave) * (S * kUnitBytes);
-  unsigned char* red = smem + kWaves * S * kUnitBytes;
-  unsigned char* plan_mem = red + (KS > 1 ? kRedBytes : 0u);
+  unsigned char* slice = smem + static_cast<uint32_t>(wave) * kSliceBytes<FP8>;
+  unsigned char* slots = smem + kWaves * kSliceBytes<FP8> + static_cast<uint32_t>(wave) * ((Q + 1) * kSlotBytes);
+  unsigned char* red = smem + kWaves * kSliceBytes<FP8> + (RING ? kRingBytes : 0u);
+  const uint32_t red_stride = red_stride_of(FP8, p.rows);
+  unsigned char* plan_mem = red + (KS > 1 ? 2u * kWaves * red_stride : 0u);
   unsigned char* rows_lds = plan_mem + plan_bytes(p.n, p.E, p.list_max);
-  const Plan plan = p.n <= 64 ? make_plan_wave(p, plan_mem) : make_plan(p, plan_mem);
+  const Plan plan = p.n <= kWavePlan ? make_plan_wave(p, plan_mem) : make_plan(p, plan_mem);
 
-  // this workgroup's share of the flat (pass, group) list
-  const uint64_t all = static_cast<uint64_t>(plan.passes) * static_cast<uint64_t>(p.groups);
-  const int64_t lo = static_cast<int64_t>(all * blockIdx.x / gridDim.x);
-  const int64_t hi = static_cast<int64_t>(all * (blockIdx.x + 1) / gridDim.x);
-  if (lo == hi) return;  // the whole workgroup
-  const int first_pass = static_cast<int>(lo / p.groups);
-  const int first_group = static_cast<int>(lo - static_cast<int64_t>(first_pass) * p.groups);
-  const int64_t total = (hi - lo) * p.units;
+  // This workgroup's share.  (pass, split) pairs are counted through: part v is
+  // split v % splits of pass v / splits.
+  const Place from = share_begin(p, plan, blockIdx.x), to = share_begin(p, plan, blockIdx.x + 1);
+  const int per_pass = p.splits * p.groups;
+  const int items = (to.pass - from.pass) * per_pass + to.item - from.item;
+  if (items == 0) return;  // the whole workgroup
+  const int first_split = static_cast<int>(fdiv(static_cast<uint32_t>(from.item), p.by_groups));
+  const int first_part = from.pass * p.splits + first_split, first_group = from.item - first_split * p.groups;
+  const int last_part = first_part + static_cast<int>(fdiv(static_cast<uint32_t>(first_group + items - 1), p.by_groups));
+  const int total = items * p.units;
 
-  const int NW = (p.L + 127) >> 7;
-  const int NU = (NW + UW - 1) / UW;
+  const int split_k = p.split_units * UK;
   const uint32_t row_bytes = FP8 ? static_cast<uint32_t>(p.L) : static_cast<uint32_t>(p.L >> 1);
   const uint32_t srow_bytes = FP8 ? 4u * p.cols : static_cast<uint32_t>(p.cols);
   const uint32_t half = UP ? static_cast<uint32_t>(p.N >> 1) : 8u;  // weight rows from a tile's first 8 to its last 8
   const uint32_t tile_rows = UP ? 8u : 16u;
-  const uint32_t pitch = static_cast<uint32_t>(NW) * 256u + 16u;  // LDS bytes of a token row
+  const uint32_t pitch = 16u * p.chunks_per_row.d;  // LDS bytes of a token row: whole units and 16
+  const uint32_t buffer_bytes = (static_cast<uint32_t>(PLANES * p.rows) * pitch + 256u + 1023u) & ~1023u;
   const rsrc_t x_rsrc = make_rsrc(p.x, static_cast<uint32_t>(p.x_bytes));
-  const uint32_t wl = lr * row_bytes + 16u * (lc ^ lr);
-  const uint32_t wl8 = wl + half * row_bytes;
+  const Lane<RING> lane_at = lane_offsets<RING>(lane, row_bytes, half);
   const uint32_t sl = (li < 8 ? li : li - 8 + half) * srow_bytes;
 
   // ---- load side
-  int l_pass = first_pass, l_group = first_group, l_unit = 0;
-  int l_expert = read_pass(plan.list, l_pass).expert;
-  int64_t l_left = hi - lo;  // groups still to load, the current one included
+  int l_part = first_part, l_group = first_group, l_unit = 0;
+  int l_left = items;  // groups still to load, the current one included
+  int l_expert = 0, l_split = 0;
+  auto set_part = [&]() {
+    const int pass = static_cast<int>(fdiv(static_cast<uint32_t>(l_part), p.by_splits));
+    l_expert = read_pass(plan.list, pass).expert;
+    l_split = l_part - pass * p.splits;
+  };
+  set_part();
   rsrc_t br, sr;
   auto set_load_tile = [&]() {
     const int t = l_group * TPW + tw;
-    const bool on = l_left > 0 && t < p.tiles;
+    const bool on = l_left > 0 && t < p.tiles;  // past the last tile or the share: every load reads zeros
     const int64_t row = static_cast<int64_t>(l_expert) * p.N + static_cast<int64_t>(on ? t : 0) * tile_rows;
-    const uint32_t span = on ? half + 8u : 0u;  // past the last tile or the share: every load reads zeros
-    br = make_rsrc(p.w + row * row_bytes, span * row_bytes);
+    const uint32_t span = on ? half + 8u : 0u, skip = on ? 128u * p.split_units * l_split : 0u;
+    br = make_rsrc(p.w + row * row_bytes + skip, span * row_bytes - skip);
     sr = make_rsrc(p.s + row * srow_bytes, span * srow_bytes);
   };
   set_load_tile();
-  auto load = [&](Scale& sc, unsigned char* slot) {
-    const int u = ks * p.units + l_unit;
-    const bool ok = u < NU;
-    if constexpr (FP8) {
-      const uint32_t col = min(fdiv(static_cast<uint32_t>(u), p.win_per_block), static_cast<uint32_t>(p.cols - 1));
-      sc = buf_load_b32(sr, ok ? sl + 4u * col : kOutOfRange);
-    } else {
-      sc = buf_load_b128(sr, ok ? sl + 16u * u : kOutOfRange);  // 16 blocks: two windows
+  auto load = [&](Unit<FP8>& un, unsigned char* slot) {
+    const int u = ks * p.units + l_unit, v = u + l_split * p.split_units;  // unit of the part, and of the row
+    const bool ok = u < p.split_units && v * UK < p.L;
+    if ((l_unit & 3) == 0) {
+      // (units past the row: bytes of the next row, or zeros; not used)
+      if constexpr (FP8) {
+        const uint32_t col = min(fdiv(static_cast<uint32_t>(v + g), p.win_per_block), static_cast<uint32_t>(p.cols - 1));
+        un.sc = buf_load_b32(sr, sl + 4u * col);
+      } else {
+        un.sc = buf_load_b128(sr, sl + 16u * static_cast<uint32_t>(v + g));
+      }
     }
-    const uint32_t ub = 128u * static_cast<uint32_t>(u);
-    buf_load_lds<16>(br, ok ? wl + ub : kOutOfRange, slot);
-    buf_load_lds<16>(br, ok ? wl8 + ub : kOutOfRange, slot + 1024);
+    load_weights<FP8, RING>(un, br, lane_at, u, ok, slot);
     if (++l_unit == p.units) {
       l_unit = 0;
       --l_left;
       if (++l_group == p.groups) {
         l_group = 0;
-        ++l_pass;
-        if (l_left > 0) l_expert = read_pass(plan.list, l_pass).expert;
+        ++l_part;
+        if (l_left > 0) set_part();
       }
       set_load_tile();
     }
   };
 
-  // ---- token rows of a pass, by direct loads: LDS chunk q holds row q /
+  // ---- token rows of a part, by direct loads: LDS chunk q holds row q /
   // chunks_per_row (down: the high parts of all tokens, then the remainders),
-  // then 256 bytes of zeros; the zeros, rows' padding and the tail of the last instruction are out-of-range
-  // reads, which write zeros
-  auto fill = [&](const Pass& ps) {
+  // then 256 bytes of zeros; the zeros, rows' padding and the tail of the last
+  // instruction are out-of-range reads, which write zeros
+  auto fill = [&](const Pass& ps, int split, int buf) {
     const uint32_t cpr = p.chunks_per_row.d;
     const uint32_t data = static_cast<uint32_t>(PLANES * ps.tokens) * cpr, chunks = data + 16u;
+    const uint32_t k0 = static_cast<uint32_t>(split * split_k);
     for (uint32_t q0 = 64u * static_cast<uint32_t>(wave); q0 < chunks; q0 += 64u * kWaves) {
       const uint32_t q = q0 + static_cast<uint32_t>(lane);
       const uint32_t row = fdiv(q, p.chunks_per_row), col = q - row * cpr;
       uint32_t src = kOutOfRange;
-      if (q < data && col * 8u < static_cast<uint32_t>(p.L)) {
+      if (q < data && col + 1u < cpr && k0 + col * 8u < static_cast<uint32_t>(p.L)) {
         uint32_t r;
         if constexpr (UP) {
           r = fdiv(plan.sorted[ps.first + row], p.topk);
@@ -454,72 +632,117 @@ __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
           const bool rest = row >= static_cast<uint32_t>(ps.tokens);
           r = plan.sorted[ps.first + (rest ? row - ps.tokens : row)] + (rest ? static_cast<uint32_t>(p.n) : 0u);
         }
-        src = r * (2u * p.L) + 16u * col;
+        src = 2u * (r * static_cast<uint32_t>(p.L) + k0) + 16u * col;
       }
-      buf_load_lds<16>(x_rsrc, src, rows_lds + 16u * q0);
+      buf_load_lds<16>(x_rsrc, src, rows_lds + buf * buffer_bytes + 16u * q0);
     }
   };
 
-  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-  Scale raw[S];
-  int c_pass = first_pass, c_group = first_group, c_unit = 0, turn = 0;
-  // FP4: the expert's FP32 scale, read ahead of the pass's rows and waited for
-  // with them (a load where a tile ends would wait for every weight load
-  // before it)
-  Pass ps = read_pass(plan.list, c_pass);
-  float gs = FP8 ? 1.0f : p.g[ps.expert];
-  fill(ps);
-  // where the lane reads its token row: dense (and FP8) rows past the pass's
-  // tokens repeat the last one, and their results are dropped
+  // ---- the part being multiplied
+  f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+  int c_part = first_part, c_group = first_group, c_unit = 0;
+  uint32_t turn = 0;
+  Pass ps;
+  int c_split, len, NW;  // k of the row in this part, and its windows
+  int buf = 0, since = 0;
   bool diag;
-  lds_cbytes a_lane, zero;
-  uint32_t a_step, lo_plane;
-  auto place = [&]() {
-    const lds_cbytes base = (lds_cbytes)rows_lds;
-    lo_plane = static_cast<uint32_t>(ps.tokens) * pitch;  // from a token's high part to its remainder
-    zero = base + PLANES * lo_plane;
+  Rows rows;
+  float gs = 1.0f;  // FP4: the expert's FP32 scale
+  auto set_current = [&]() {
+    const int pass = static_cast<int>(fdiv(static_cast<uint32_t>(c_part), p.by_splits));
+    ps = read_pass(plan.list, pass);
+    c_split = c_part - pass * p.splits;
+    len = min(split_k, p.L - c_split * split_k);
+    NW = (len + 127) >> 7;
+    // dense (and FP8) rows past the part's tokens repeat the last one, and
+    // their results are dropped
+    const lds_cbytes base = (lds_cbytes)(rows_lds + buf * buffer_bytes);
+    const uint32_t plane = static_cast<uint32_t>(ps.tokens) * pitch;
+    rows.zero = base + PLANES * plane;
     diag = !FP8 && ps.tokens <= 4;
+    const bool carries = !diag || ((li & 3) == g && (li >> 2) < ps.tokens);
+    const uint32_t off = (FP8 ? 32u : 64u) * g;
     const int m = diag ? li >> 2 : min(li, ps.tokens - 1);
-    const bool carries = !diag || ((li & 3) == g && m < ps.tokens);
-    a_lane = carries ? base + static_cast<uint32_t>(m) * pitch + (FP8 ? 32u : 64u) * g : zero;
-    a_step = carries ? 256u : 0u;
-    if (!carries) lo_plane = 0u;
+    rows.a[0] = carries ? base + static_cast<uint32_t>(m) * pitch + off : rows.zero;
+    rows.a[1] = base + static_cast<uint32_t>(min(16 + li, ps.tokens - 1)) * pitch + off;
+    rows.step = carries ? 256u : 0u;
+    rows.plane = carries ? plane : 0u;
+    // a scalar load: a vector load would wait for the weight loads before it
+    if constexpr (!FP8)
+      gs = reinterpret_cast<const __attribute__((address_space(4))) float*>(reinterpret_cast<uintptr_t>(p.g))[ps.expert];
   };
-  place();
+  // the rows of the part after this one, into the other buffer
+  auto prefetch = [&]() {
+    since = 0;
+    if (p.buffers == 2 && c_part < last_part) {
+      const int pass = static_cast<int>(fdiv(static_cast<uint32_t>(c_part + 1), p.by_splits));
+      // the fences keep the unit loads on their side of it: `since` counts those after it
+      __asm__ volatile("" ::: "memory");
+      fill(read_pass(plan.list, pass), c_part + 1 - pass * p.splits, buf ^ 1);
+      __asm__ volatile("" ::: "memory");
+    }
+  };
+  Unit<FP8> ring[Q];
+  set_current();
+  fill(ps, c_split, 0);
 #pragma unroll
-  for (int d = 0; d < D; ++d) load(raw[d], ring + d * kUnitBytes);
-  wait_vm<D * LPU>();  // the fill is older
-  __asm__ volatile("" : "+v"(gs));
+  for (int q = 0; q < Q; ++q) load(ring[q], slots + q * kSlotBytes);
+  wait_vm<kAheadLoads>();  // the rows are older
   __builtin_amdgcn_s_barrier();
   __asm__ volatile("" ::: "memory");
+  prefetch();
 
-  auto consume = [&](const Scale& sc, const unsigned char* slot) {
+  auto multiply = [&](const Unit<FP8>& un, const Scale<FP8>& sc) {
     const int u = ks * p.units + c_unit;
-    wait_vm<D * LPU>();  // this unit's weights have landed
-    if constexpr (FP8)
-      fp8_unit<Tr, PLANES>(acc, sc, slot, a_lane, zero, lo_plane, u, NW, p.L, li, g);
-    else if (diag)
-      fp4_unit<Tr, PLANES, true>(acc, sc, slot, a_lane, a_step, zero, lo_plane, u, NW, p.L, li, g);
-    else
-      fp4_unit<Tr, PLANES, false>(acc, sc, slot, a_lane, a_step, zero, lo_plane, u, NW, p.L, li, g);
-    if (++c_unit < p.units) return;
-    // end of a tile: join the K split, then the epilogue
-    c_unit = 0;
+    if constexpr (FP8) {
+      if (ps.tokens > 16)
+        fp8_window<Tr, PLANES, 2>(acc, un, sc, rows, u, NW, len);
+      else
+        fp8_window<Tr, PLANES, 1>(acc, un, sc, rows, u, NW, len);
+    } else {
+      if (diag)
+        fp4_diag<Tr, PLANES>(acc, un, sc, rows, u, NW, len);
+      else if (ps.tokens > 16)
+        fp4_dense<Tr, PLANES, 2>(acc, un, sc, rows, u, NW, len, g);
+      else
+        fp4_dense<Tr, PLANES, 1>(acc, un, sc, rows, u, NW, len, g);
+    }
+  };
+
+  // join the K split of a tile and write it
+  auto finish = [&]() {
     if (KS > 1) {
-      // the two halves of `red` are used in turn, so one barrier is enough: a
-      // half is written again after a barrier that its readers reach later
-      unsigned char* part = red + turn * (kRedBytes / 2) + wave * 1024 + 16 * lane;
+      // The two halves of `red` are used in turn, so one barrier is enough: a
+      // half is written again after a barrier that its readers reach later.
+      // Two row tiles take both halves, between barriers.
+      const bool two = ps.tokens > 16;
+      unsigned char* part = red + (two ? 0u : turn) * (kWaves * red_stride) + wave * red_stride;
       turn ^= 1;
-      *reinterpret_cast<f32x4*>(part) = acc;
+      if (two) lds_barrier();
+      if (diag) {
+        reinterpret_cast<float*>(part)[lane] = acc[0][0];
+      } else {
+        reinterpret_cast<f32x4*>(part)[lane] = acc[0];
+        if (two) reinterpret_cast<f32x4*>(part + kWaves * red_stride)[lane] = acc[1];
+      }
       lds_barrier();
       if (ks == 0) {
 #pragma unroll
-        for (int v = 1; v < KS; ++v) acc += *reinterpret_cast<const f32x4*>(part + v * 1024);
+        for (int v = 1; v < KS; ++v) {
+          const unsigned char* q = part + v * red_stride;
+          if (diag) {
+            acc[0][0] += reinterpret_cast<const float*>(q)[lane];
+          } else {
+            acc[0] += reinterpret_cast<const f32x4*>(q)[lane];
+            if (two) acc[1] += reinterpret_cast<const f32x4*>(q + kWaves * red_stride)[lane];
+          }
+        }
       }
+      if (two) lds_barrier();
     }
     const int t = c_group * TPW + tw;
     if (ks == 0 && t < p.tiles) {
-      auto finish = [&](float v, int row) {
+      auto write = [&](float v, int row) {
         if constexpr (UP) {
           const float up = swap8(v);
           if (row < ps.tokens && li < 8) {
@@ -528,47 +751,82 @@ __global__ __launch_bounds__(kThreads) void moe_kernel(const MoeParams p) {
                     gated(p.act, v * gs, up * gs));
           }
         } else if (row < ps.tokens) {
-          static_cast<float*>(p.out)[static_cast<size_t>(plan.sorted[ps.first + row]) * p.N + 16 * t + li] = v * gs;
+          const size_t at = static_cast<size_t>(c_split) * p.n + plan.sorted[ps.first + row];
+          static_cast<float*>(p.out)[at * p.N + 16 * t + li] = v * gs;
         }
       };
       if (diag) {
-        finish(acc[0], g);
+        write(acc[0][0], g);
       } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) finish(acc[r], 4 * g + r);
+        for (int r = 0; r < 4; ++r) write(acc[0][r], 4 * g + r);
+        if (ps.tokens > 16) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) write(acc[1][r], 16 + 4 * g + r);
+        }
       }
     }
-    acc = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (++c_group == p.groups) {
-      c_group = 0;
-      ++c_pass;
+    acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    acc[1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  };
+
+  // the next part's rows take over
+  auto next_part = [&]() {
+    if (p.buffers == 2) {
+      // asked for when this part began; newer are the unit loads since
+      if (since >= Q)
+        wait_vm<kAheadLoads>();
+      else
+        wait_vm<0>();
+      buf ^= 1;
+      set_current();
+      lds_barrier();  // every wave's rows have landed, and the other buffer is free
+      prefetch();
+    } else {
+      set_current();
+      lds_barrier();  // the last part's rows are read
+      fill(ps, c_split, 0);
+      wait_vm<0>();
+      __builtin_amdgcn_s_barrier();
+      __asm__ volatile("" ::: "memory");
     }
   };
 
-  int64_t left = total;
-  for (int64_t f0 = 0; f0 < total; f0 += S) {
+  // Units past the end of the share are out-of-range loads, and not
+  // multiplied.  No way leaves the loop body before its end: it would merge
+  // with the others at the loop head and make every wait there a full one.
+  int l_slot = Q, c_slot = 0;  // RING: the slot to ask for next, and the oldest
+  for (int f0 = 0; f0 < total; f0 += Q) {
 #pragma unroll
-    for (int u = 0; u < S; ++u) {
-      load(raw[(u + D) % S], ring + ((u + D) % S) * kUnitBytes);
-      if (left > 0) {  // uniform across the workgroup
-        if (c_unit == 0 && c_group == 0 && c_pass != first_pass) {
-          // the next pass's tokens take the place of the last one's
-          ps = read_pass(plan.list, c_pass);
-          if (!FP8) gs = p.g[ps.expert];
-          lds_barrier();
-          fill(ps);
-          place();
-          wait_vm<0>();
-          __asm__ volatile("" : "+v"(gs));
-          __builtin_amdgcn_s_barrier();
-          __asm__ volatile("" ::: "memory");
+    for (int q = 0; q < Q; ++q) {
+      const bool on = f0 + q < total;  // uniform across the workgroup
+      const Scale<FP8> sc = unit_scales<FP8>(ring[q], slice, c_unit, li, g);
+      if constexpr (RING) {
+        // the slot that is asked for was read a step ago, and those reads are
+        // done: their values have been multiplied
+        load(ring[q], slots + l_slot * kSlotBytes);
+        Unit<FP8> now;
+        fetch<FP8>(now, slots + c_slot * kSlotBytes, li, g);
+        l_slot = l_slot == Q ? 0 : l_slot + 1;
+        c_slot = c_slot == Q ? 0 : c_slot + 1;
+        if (on) multiply(now, sc);
+      } else {
+        if (on) multiply(ring[q], sc);
+        load(ring[q], slots);
+      }
+      if (on) {
+        ++since;
+        if (++c_unit == p.units) {
+          c_unit = 0;
+          finish();
+          if (++c_group == p.groups) {
+            c_group = 0;
+            if (++c_part <= last_part) next_part();
+          }
         }
-        consume(raw[u], ring + u * kUnitBytes);
-        --left;
       }
     }
   }
-  wait_vm<0>();  // loads past the end of the share write zeros to the ring
 }
 
 // ---------------------------------------------------------------- one token
@@ -585,25 +843,21 @@ constexpr uint32_t kTokenRedBytes = 1024;  // 2 x 8 waves x 16 floats
 // In down the two planes of H are two rows of one operand, not two MFMAs.
 
 // up: grid-stride over (choice, group); down: over tiles.
-template <typename T, bool FP8, bool UP, int KS, int D>
+template <typename T, bool FP8, bool UP, int KS, bool RING>
 __global__ __launch_bounds__(kThreads) void moe_token_kernel(const MoeParams p, const float* __restrict__ weights) {
   typedef typename std::conditional<UP, T, __bf16>::type X;
   typedef ActTraits<X> Tr;
-  typedef typename Tr::vec8 V;
-  typedef typename std::conditional<FP8, uint32_t, u32x4>::type Scale;
   constexpr int TPW = kWaves / KS;  // up: tiles side by side; down: choices side by side
-  constexpr int S = D + 1;
-  constexpr int UW = FP8 ? 1 : 2;
-  constexpr int LPU = 3;
+  constexpr int UW = FP8 ? 1 : 2;  // windows of a unit
   constexpr int ROWS = UP ? 1 : 2;  // operand rows of a choice
   extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15, g = lane >> 4;
-  const int lr = lane >> 3, lc = lane & 7;
   const int ks = wave % KS, tw = wave / KS;
-  unsigned char* ring = smem + static_cast<uint32_t>(wave) * (S * kUnitBytes);
-  unsigned char* red = smem + kWaves * S * kUnitBytes;
+  unsigned char* slice = smem + static_cast<uint32_t>(wave) * kSliceBytes<FP8>;
+  unsigned char* slots = smem + kWaves * kSliceBytes<FP8> + static_cast<uint32_t>(wave) * ((Q + 1) * kSlotBytes);
+  unsigned char* red = smem + kWaves * kSliceBytes<FP8> + (RING ? kRingBytes : 0u);
   unsigned char* rows_lds = red + kTokenRedBytes;
   const int NW = (p.L + 127) >> 7;
   const int NU = (NW + UW - 1) / UW;
@@ -612,8 +866,7 @@ __global__ __launch_bounds__(kThreads) void moe_token_kernel(const MoeParams p, 
   const uint32_t half = UP ? static_cast<uint32_t>(p.N >> 1) : 8u;
   const uint32_t tile_rows = UP ? 8u : 16u;
   const uint32_t pitch = static_cast<uint32_t>(NW) * 256u + 16u;  // LDS bytes of a row
-  const uint32_t wl = lr * row_bytes + 16u * (lc ^ lr);
-  const uint32_t wl8 = wl + half * row_bytes;
+  const Lane<RING> lane_at = lane_offsets<RING>(lane, row_bytes, half);
   const uint32_t sl = (li < 8 ? li : li - 8 + half) * srow_bytes;
 
   // The wave's sequence.  up: items (choice, group) b, b + grid, ..; wave
@@ -651,18 +904,18 @@ __global__ __launch_bounds__(kThreads) void moe_token_kernel(const MoeParams p, 
     sr = make_rsrc(p.s + row * srow_bytes, span * srow_bytes);
   };
   set_load_tile();
-  auto load = [&](Scale& sc, unsigned char* slot) {
+  auto load = [&](Unit<FP8>& un, unsigned char* slot) {
     const int u = ks * p.units + l_unit;
     const bool ok = u < NU;
-    if constexpr (FP8) {
-      const uint32_t col = min(fdiv(static_cast<uint32_t>(u), p.win_per_block), static_cast<uint32_t>(p.cols - 1));
-      sc = buf_load_b32(sr, ok ? sl + 4u * col : kOutOfRange);
-    } else {
-      sc = buf_load_b128(sr, ok ? sl + 16u * u : kOutOfRange);
+    if ((l_unit & 3) == 0) {
+      if constexpr (FP8) {
+        const uint32_t col = min(fdiv(static_cast<uint32_t>(u + g), p.win_per_block), static_cast<uint32_t>(p.cols - 1));
+        un.sc = buf_load_b32(sr, sl + 4u * col);
+      } else {
+        un.sc = buf_load_b128(sr, sl + 16u * static_cast<uint32_t>(u + g));
+      }
     }
-    const uint32_t ub = 128u * static_cast<uint32_t>(u);
-    buf_load_lds<16>(br, ok ? wl + ub : kOutOfRange, slot);
-    buf_load_lds<16>(br, ok ? wl8 + ub : kOutOfRange, slot + 1024);
+    load_weights<FP8, RING>(un, br, lane_at, u, ok, slot);
     if (++l_unit == p.units) {
       l_unit = 0;
       if (++l_in == inner) {
@@ -673,6 +926,10 @@ __global__ __launch_bounds__(kThreads) void moe_token_kernel(const MoeParams p, 
     }
   };
 
+  f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+  float sum = 0.0f;  // down: the weighted choices of this wave, lanes g == 0
+  Unit<FP8> ring[Q];
+  int c_item = blockIdx.x, c_in = 0, c_unit = 0, turn = 0;
   // up: the token's row; down: the high parts of all choices, then the
   // remainders (rows of choices without an expert hold anything: their
   // results are dropped)
@@ -687,40 +944,38 @@ __global__ __launch_bounds__(kThreads) void moe_token_kernel(const MoeParams p, 
       buf_load_lds<16>(x_rsrc, in ? row * (2u * p.L) + 16u * col : kOutOfRange, rows_lds + 16u * q0);
     }
   }
-  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
-  float sum = 0.0f;  // down: the weighted choices of this wave, lanes g == 0
-  Scale raw[S];
-  int c_item = blockIdx.x, c_in = 0, c_unit = 0, turn = 0;
 #pragma unroll
-  for (int d = 0; d < D; ++d) load(raw[d], ring + d * kUnitBytes);
-  wait_vm<D * LPU>();  // the rows, scales and weights are older
+  for (int q = 0; q < Q; ++q) load(ring[q], slots + q * kSlotBytes);
+  wait_vm<kAheadLoads>();  // the rows, scales and weights are older
   __asm__ volatile("" : "+v"(g_lane), "+v"(w_lane));
   __builtin_amdgcn_s_barrier();
   __asm__ volatile("" ::: "memory");
 
-  auto consume = [&](const Scale& sc, const unsigned char* slot) {
+  auto consume = [&](const Unit<FP8>& un, const Scale<FP8>& sc) {
     const int u = ks * p.units + c_unit;
     const int j = choice_of(c_item, c_in);
-    wait_vm<D * LPU>();
     // row m of the operand: up 0: the token; down 0 and 1: the choice's two
     // planes.  FP4: block-diagonal, so lane groups 0 and 1 end with the rows'
     // sums in acc[0]; FP8: lane rows m, group 0 ends with them in acc[0 ..].
     const int m = FP8 ? li & (ROWS - 1) : li >> 2;
     const bool carries = FP8 || ((li & 3) == g && m < ROWS);
     const lds_cbytes base = (lds_cbytes)rows_lds;
-    const lds_cbytes zero = base + static_cast<uint32_t>(UP ? 1 : 2 * p.n) * pitch;
     const uint32_t row = UP ? 0u : static_cast<uint32_t>(m * p.n + min(j, p.n - 1));
-    const lds_cbytes a_lane = carries ? base + row * pitch + (FP8 ? 32u : 64u) * g : zero;
+    Rows rows;
+    rows.zero = base + static_cast<uint32_t>(UP ? 1 : 2 * p.n) * pitch;
+    rows.a[0] = carries ? base + row * pitch + (FP8 ? 32u : 64u) * g : rows.zero;
+    rows.step = carries ? 256u : 0u;
+    rows.plane = 0u;
     if constexpr (FP8)
-      fp8_unit<Tr, 1>(acc, sc, slot, a_lane, zero, 0u, u, NW, p.L, li, g);
+      fp8_window<Tr, 1, 1>(acc, un, sc, rows, u, NW, p.L);
     else
-      fp4_unit<Tr, 1, true>(acc, sc, slot, a_lane, carries ? 256u : 0u, zero, 0u, u, NW, p.L, li, g);
+      fp4_diag<Tr, 1>(acc, un, sc, rows, u, NW, p.L);
     if (++c_unit < p.units) return;
     c_unit = 0;
     const int e = expert_of(j);
-    float v = acc[0];  // lanes g == 0 hold the tile
-    if (!UP) v += FP8 ? acc[1] : __shfl_xor(acc[0], 16, 64);
-    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    float v = acc[0][0];  // lanes g == 0 hold the tile
+    if (!UP) v += FP8 ? acc[0][1] : __shfl_xor(acc[0][0], 16, 64);
+    acc[0] = f32x4{0.f, 0.f, 0.f, 0.f};
     if constexpr (!UP) {
       if (e >= 0) sum = fmaf(v * value_of(g_lane, j), value_of(w_lane, j), sum);
       if (++c_in < inner) return;
@@ -759,55 +1014,71 @@ __global__ __launch_bounds__(kThreads) void moe_token_kernel(const MoeParams p, 
     c_item += gridDim.x;
   };
 
-  for (int f0 = 0; f0 < total; f0 += S) {
+  int l_slot = Q, c_slot = 0;  // RING: the slot to ask for next, and the oldest
+  for (int f0 = 0; f0 < total; f0 += Q) {
 #pragma unroll
-    for (int u = 0; u < S; ++u) {
-      load(raw[(u + D) % S], ring + ((u + D) % S) * kUnitBytes);
-      if (f0 + u < total) consume(raw[u], ring + u * kUnitBytes);
+    for (int q = 0; q < Q; ++q) {
+      const bool on = f0 + q < total;  // uniform across the workgroup
+      const Scale<FP8> sc = unit_scales<FP8>(ring[q], slice, c_unit, li, g);
+      if constexpr (RING) {
+        // the slot that is asked for was read a step ago, and those reads are
+        // done: their values have been multiplied
+        load(ring[q], slots + l_slot * kSlotBytes);
+        Unit<FP8> now;
+        fetch<FP8>(now, slots + c_slot * kSlotBytes, li, g);
+        l_slot = l_slot == Q ? 0 : l_slot + 1;
+        c_slot = c_slot == Q ? 0 : c_slot + 1;
+        if (on) consume(now, sc);
+      } else {
+        if (on) consume(ring[q], sc);
+        load(ring[q], slots);
+      }
     }
   }
-  wait_vm<0>();
 }
 
-// Y[m, c .. c + 7] = sum over j of weights[m * topk + j] * P[m * topk + j, c ..], in the order of j
+// ---------------------------------------------------------------- combine
+
+// Y[m, c .. c + 3] = sum over j of weights[a] * (sum over s of P[s][a, c ..]), a = m * topk + j, in order.
+// A few microseconds of latency at these sizes: eight choices' loads at a
+// time, none of them behind a branch (what a masked choice holds is not used).
 template <typename T>
 __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restrict__ P, const int32_t* __restrict__ ids,
-                                                          const float* __restrict__ weights, T* __restrict__ Y, int M, int K, int topk, int E) {
-  const int chunks = K >> 3;
-  const int64_t all = static_cast<int64_t>(M) * chunks;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < all; i += 256 * static_cast<int64_t>(gridDim.x)) {
-    const int m = static_cast<int>(i / chunks), c = static_cast<int>(i - static_cast<int64_t>(m) * chunks);
-    float sum[8];
+                                                          const float* __restrict__ weights, T* __restrict__ Y, int M,
+                                                          int K, int topk, int E, int splits, FastDiv chunks) {
+  typedef typename ActTraits<T>::vec8 V;
+  const uint32_t all = static_cast<uint32_t>(M) * chunks.d;  // chunks of 4 columns
+  const size_t part = static_cast<size_t>(M) * topk * K;     // of one split
+  for (uint32_t i = blockIdx.x * 256u + threadIdx.x; i < all; i += 256u * gridDim.x) {
+    const uint32_t m = fdiv(i, chunks), c = i - m * chunks.d;
+    const float* q = P + static_cast<size_t>(m) * topk * K + 4 * c;
+    f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < topk; j0 += 8) {
+      f32x4 x[8];
+      float w[8];
+      bool on[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
-    for (int j0 = 0; j0 < topk; j0 += 4) {
-      // four choices' loads at a time, none of them behind a branch; what a
-      // masked choice holds is not used
-      f32x4 x[4], y[4];
-      float w[4];
-      bool on[4];
+      for (int j = 0; j < 8; ++j) {
+        const int k = min(j0 + j, topk - 1);
+        x[j] = *reinterpret_cast<const f32x4*>(q + static_cast<size_t>(k) * K);
+        w[j] = weights[m * topk + k];
+        on[j] = j0 + j < topk && static_cast<uint32_t>(ids[m * topk + k]) < static_cast<uint32_t>(E);
+      }
+      for (int s = 1; s < splits; ++s) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int a = m * topk + min(j0 + j, topk - 1);
-        const f32x4* q = reinterpret_cast<const f32x4*>(P + static_cast<size_t>(a) * K + 8 * c);
-        x[j] = q[0];
-        y[j] = q[1];
-        w[j] = weights[a];
-        on[j] = j0 + j < topk && static_cast<uint32_t>(ids[a]) < static_cast<uint32_t>(E);
+        for (int j = 0; j < 8; ++j)
+          x[j] += *reinterpret_cast<const f32x4*>(q + s * part + static_cast<size_t>(min(j0 + j, topk - 1)) * K);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          sum[k] = on[j] ? fmaf(x[j][k], w[j], sum[k]) : sum[k];
-          sum[4 + k] = on[j] ? fmaf(y[j][k], w[j], sum[4 + k]) : sum[4 + k];
-        }
-      }
+        for (int k = 0; k < 4; ++k) sum[k] = on[j] ? fmaf(x[j][k], w[j], sum[k]) : sum[k];
     }
-    typename ActTraits<T>::vec8 r;
+    V r;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = round_to<T>(sum[k]);
-    *reinterpret_cast<typename ActTraits<T>::vec8*>(Y + static_cast<size_t>(m) * K + 8 * c) = r;
+    for (int k = 0; k < 4; ++k) r[k] = round_to<T>(sum[k]);
+    const u32x4 bits = __builtin_bit_cast(u32x4, r);
+    *reinterpret_cast<u32x2*>(Y + static_cast<size_t>(m) * K + 4 * c) = u32x2{bits.x, bits.y};
   }
 }
 
@@ -815,27 +1086,26 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
 
 constexpr size_t kMaxLds = 160 * 1024;
 
-template <typename T, bool FP8, bool UP, int KS, int D>
+// Dynamic LDS above 64 KiB must be allowed per kernel, once per device.
+template <auto KERNEL>
 void allow_lds() {
   static std::once_flag once[kMaxDevices];
   once_per_device(once, [] {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&moe_kernel<T, FP8, UP, KS, D>),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxLds));
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kMaxLds));
   });
 }
 
 struct Shape {
-  int rows, depth, ks, grid, units, groups, list_max;
+  int rows, buffers, splits, split_units, ks, grid, units, groups, list_max;
+  bool ring;
   size_t lds;
 };
 
-size_t fixed_lds(int depth, int n, int E, int list_max) {
-  return static_cast<size_t>(kWaves) * (depth + 1) * kUnitBytes + kRedBytes + plan_bytes(n, E, list_max);
-}
-
-// Token rows of `planes` planes and the zero block, in whole direct-load instructions.
-size_t rows_lds_bytes(int rows, int planes, int NW) {
-  return (static_cast<size_t>(rows) * planes * (static_cast<size_t>(NW) * 256 + 16) + 256 + 1023) / 1024 * 1024;
+// Token rows of `planes` planes and the zero block, in whole direct-load
+// instructions (the kernel's buffer_bytes).
+size_t rows_lds_bytes(int64_t rows, int planes, int windows) {
+  return (static_cast<size_t>(rows) * planes * (static_cast<size_t>(windows) * 256 + 16) + 256 + 1023) / 1024 * 1024;
 }
 
 // The K split of a tile over KS waves.  The larger it is, the smaller the
@@ -853,72 +1123,89 @@ int k_split(int NU, int64_t tiles, int64_t passes, int64_t cus) {
   return ks;
 }
 
-// The launch of one kernel: rows per pass, ring depth and K split.  False
-// when not even one token row fits.
+// The launch of one kernel for several tokens.  False when not even one token
+// row fits.
 bool plan_shape(const MoeArgs& a, bool fp8, bool up, Shape* out) {
-  const int64_t n = a.M * a.topk;
-  const int64_t L = up ? a.K : a.I;
-  const int NW = static_cast<int>((L + 127) / 128), NU = fp8 ? NW : (NW + 1) / 2;
-  const int planes = up ? 1 : 2;
-  // Tokens per pass: an expert's tokens beyond `rows` read its weights again.
-  // Twice the mean and a few more is rarely exceeded, and every row that is
-  // not reserved leaves LDS to the ring.
+  const int64_t n = a.M * a.topk, L = up ? a.K : a.I;
+  const int uk = fp8 ? 128 : 256, NU = static_cast<int>((L + uk - 1) / uk), planes = up ? 1 : 2;
+  // Tokens per pass: an expert's tokens beyond `rows` read its weights again;
+  // twice the mean and a few more is rarely exceeded.
   const int64_t mean = a.E > 0 ? (n + a.E - 1) / a.E : n;
-  int64_t want = 2 * mean + 4;
-  if (want > 16) want = 16;
-  if (want > a.M) want = a.M;  // (a token that names an expert twice may take a second pass)
-  if (want < 1) want = 1;
-  for (int depth : {4, 2}) {
-    for (int64_t rows = want; rows >= 1; --rows) {
-      if (depth == 4 && rows < want) break;  // a shallower ring before fewer rows
-      const int64_t list_max = (n < a.E ? n : a.E) + n / rows;
-      const size_t lds = fixed_lds(depth, static_cast<int>(n), static_cast<int>(a.E), static_cast<int>(list_max)) +
-                         rows_lds_bytes(static_cast<int>(rows), planes, NW);
-      if (lds > kMaxLds) continue;
-      const int64_t tiles = up ? a.I / 8 : a.K / 16;
-      const int64_t passes = n < a.E ? n : a.E;
-      const int64_t cus = device_cus();
-      const int ks = k_split(NU, tiles, passes, cus);
-      const int64_t groups = (tiles + kWaves / ks - 1) / (kWaves / ks);
-      *out = Shape{static_cast<int>(rows), depth, ks, static_cast<int>(passes * groups < cus ? passes * groups : cus),
-                   (NU + ks - 1) / ks, static_cast<int>(groups), static_cast<int>(list_max), lds};
-      return true;
-    }
-  }
-  return false;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>({2 * mean + 4, kMaxRows, a.M}));
+  // Rows that fit: first with two buffers, then with one, then (down) with the
+  // sum in parts, then fewer rows.
+  const int max_splits = up ? 1 : static_cast<int>(moe_down_splits(a.M, a.I));
+  const int64_t passes = std::min<int64_t>(n, a.E);
+  const size_t slices = kWaves * (fp8 ? kSliceBytes<true> : kSliceBytes<false>);
+  auto fits = [&](int64_t rows, int buffers, int splits, bool ring) {
+    const int units = (NU + splits - 1) / splits;
+    const int64_t list_max = passes + n / rows;
+    const size_t lds = slices + (ring ? kRingBytes : 0u) + 2 * kWaves * red_stride_of(fp8, static_cast<int>(rows)) +
+                       plan_bytes(static_cast<int>(n), static_cast<int>(a.E), static_cast<int>(list_max)) +
+                       buffers * rows_lds_bytes(rows, planes, units * (uk / 128));
+    if (lds > kMaxLds) return false;
+    *out = Shape{static_cast<int>(rows), buffers, (NU + units - 1) / units, units, 1, 1, 1, 1, static_cast<int>(list_max), ring, lds};
+    return true;
+  };
+  bool ok = fits(want, 2, 1, true) || fits(want, 1, 1, true) || fits(want, 2, 1, false);
+  for (int s = 1; !ok && s <= max_splits; ++s) ok = fits(want, 1, s, false);
+  for (int64_t rows = want - 1; !ok && rows >= 1; --rows) ok = fits(rows, 1, max_splits, false);
+  if (!ok) return false;
+  const int64_t tiles = up ? a.I / 8 : a.K / 16, cus = device_cus();
+  out->ks = k_split(out->split_units, tiles, passes * out->splits, cus);
+  const int64_t groups = (tiles + kWaves / out->ks - 1) / (kWaves / out->ks);
+  // the shares are counted in 32 bits
+  if (out->list_max * out->splits * groups * kMostCost >= (int64_t(1) << 31)) return false;
+  out->groups = static_cast<int>(groups);
+  out->units = (out->split_units + out->ks - 1) / out->ks;
+  out->grid = static_cast<int>(std::min(passes * out->splits * groups, cus));
+  return true;
 }
 
-template <typename T, bool FP8, bool UP, int KS, int D>
+template <typename T, bool FP8, bool UP, int KS, bool RING>
+void launch_ring(const MoeParams& p, const Shape& s, hipStream_t st) {
+  allow_lds<&moe_kernel<T, FP8, UP, KS, RING>>();
+  hipLaunchKernelGGL((moe_kernel<T, FP8, UP, KS, RING>), dim3(s.grid), dim3(kThreads), s.lds, st, p);
+}
+template <typename T, bool FP8, bool UP, int KS>
 void launch_kernel(const MoeParams& p, const Shape& s, hipStream_t st) {
-  allow_lds<T, FP8, UP, KS, D>();
-  hipLaunchKernelGGL((moe_kernel<T, FP8, UP, KS, D>), dim3(s.grid), dim3(kThreads), s.lds, st, p);
+  s.ring ? launch_ring<T, FP8, UP, KS, true>(p, s, st) : launch_ring<T, FP8, UP, KS, false>(p, s, st);
 }
 
 template <typename T, bool FP8, bool UP>
 void launch_phase(MoeParams p, const Shape& s, hipStream_t st) {
   p.rows = s.rows;
+  p.buffers = s.buffers;
+  p.splits = s.splits;
+  p.split_units = s.split_units;
   p.groups = s.groups;
   p.units = s.units;
   p.list_max = s.list_max;
-#define FP4W_MOE_KS(KS_) \
-  s.depth == 4 ? launch_kernel<T, FP8, UP, KS_, 4>(p, s, st) : launch_kernel<T, FP8, UP, KS_, 2>(p, s, st)
+  p.fp8 = FP8;
+  p.by_rows = make_fastdiv(static_cast<uint32_t>(s.rows));
+  p.by_grid = make_fastdiv(static_cast<uint32_t>(s.grid));
+  p.by_groups = make_fastdiv(static_cast<uint32_t>(s.groups));
+  p.by_splits = make_fastdiv(static_cast<uint32_t>(s.splits));
+  p.chunks_per_row = make_fastdiv(static_cast<uint32_t>(s.split_units * (FP8 ? 16 : 32) + 1));
   switch (s.ks) {
-    case 1: FP4W_MOE_KS(1); break;
-    case 2: FP4W_MOE_KS(2); break;
-    case 4: FP4W_MOE_KS(4); break;
-    default: FP4W_MOE_KS(8); break;
+    case 1: launch_kernel<T, FP8, UP, 1>(p, s, st); break;
+    case 2: launch_kernel<T, FP8, UP, 2>(p, s, st); break;
+    case 4: launch_kernel<T, FP8, UP, 4>(p, s, st); break;
+    default: launch_kernel<T, FP8, UP, 8>(p, s, st); break;
   }
-#undef FP4W_MOE_KS
 }
 
+template <typename T, bool FP8, bool UP, int KS, bool RING>
+void launch_token_ring(const MoeParams& p, const float* weights, int grid, size_t lds, hipStream_t st) {
+  allow_lds<&moe_token_kernel<T, FP8, UP, KS, RING>>();
+  hipLaunchKernelGGL((moe_token_kernel<T, FP8, UP, KS, RING>), dim3(grid), dim3(kThreads), lds, st, p, weights);
+}
 template <typename T, bool FP8, bool UP, int KS>
 void launch_token_kernel(const MoeParams& p, const float* weights, int grid, size_t lds, hipStream_t st) {
-  static std::once_flag once[kMaxDevices];
-  once_per_device(once, [] {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(&moe_token_kernel<T, FP8, UP, KS, 4>),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMaxLds));
-  });
-  hipLaunchKernelGGL((moe_token_kernel<T, FP8, UP, KS, 4>), dim3(grid), dim3(kThreads), lds, st, p, weights);
+  if (lds + kRingBytes <= kMaxLds)
+    launch_token_ring<T, FP8, UP, KS, true>(p, weights, grid, lds + kRingBytes, st);
+  else
+    launch_token_ring<T, FP8, UP, KS, false>(p, weights, grid, lds, st);
 }
 
 template <typename T, bool FP8, bool UP>
@@ -931,12 +1218,12 @@ void launch_token_ks(const MoeParams& p, const float* weights, int ks, int grid,
   }
 }
 
-// M = 1.  False where the rows do not fit in LDS beside the rings.
+// M = 1.  False where the rows do not fit in LDS.
 template <typename T, bool FP8>
 bool launch_token(const MoeArgs& a, MoeParams up, MoeParams down, hipStream_t st) {
-  const size_t base = kWaves * 5 * kUnitBytes + kTokenRedBytes;
   const int cus = device_cus();
   const int up_nw = static_cast<int>((a.K + 127) / 128), down_nw = static_cast<int>((a.I + 127) / 128);
+  const size_t base = kWaves * kSliceBytes<FP8> + kTokenRedBytes;
   const size_t up_lds = base + rows_lds_bytes(1, 1, up_nw);
   const size_t down_lds = base + rows_lds_bytes(static_cast<int>(a.topk), 2, down_nw);
   if (up_lds > kMaxLds || down_lds > kMaxLds) return false;
@@ -999,10 +1286,11 @@ int launch_t(const MoeArgs& a) {
   launch_phase<T, FP8, true>(up, up_shape, st);
   launch_phase<__bf16, FP8, false>(down, down_shape, st);
   // combine
-  const int64_t blocks = (a.M * (a.K / 8) + 255) / 256;
-  hipLaunchKernelGGL(moe_combine_kernel<T>, dim3(static_cast<int>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, P,
+  const int64_t blocks = (a.M * (a.K / 4) + 255) / 256;
+  hipLaunchKernelGGL(moe_combine_kernel<T>, dim3(static_cast<int>(std::min<int64_t>(blocks, 8192))), dim3(256), 0, st, P,
                      a.ids, a.weights, static_cast<T*>(a.Y), static_cast<int>(a.M), static_cast<int>(a.K),
-                     static_cast<int>(a.topk), static_cast<int>(a.E));
+                     static_cast<int>(a.topk), static_cast<int>(a.E), down_shape.splits,
+                     make_fastdiv(static_cast<uint32_t>(a.K / 4)));
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -13,6 +13,7 @@ pytestmark = pytest.mark.gpu
 
 FORMATS = [False, True]
 GENERIC = {False: fw.PATH_MOE_FP4_GENERIC, True: fw.PATH_MOE_FP8_GENERIC}
+STREAM = {False: fw.PATH_MOE_FP4_STREAM, True: fw.PATH_MOE_FP8_STREAM}
 ids_of = lambda c: "x".join(map(str, c))  # noqa: E731
 
 # M, K, I, E, topk: sizes that fill tiles, end inside them, one token and
@@ -42,6 +43,49 @@ def test_against_oracle(size, fp8, dtype, path):
     Y = run(c, act, path=GENERIC[fp8] if path == "generic" else fw.PATH_AUTO)
     want, tol = moe_want(c, act)
     assert_within(Y, want, tol, dtype, f"{size}")
+
+
+# sizes that bring the streaming kernels to the other layouts of LDS: one
+# buffer of token rows, weights straight to registers, the second product's sum
+# in parts, fewer rows than tokens, and as many assignments and experts as a
+# call may have
+LAYOUTS = [(6, 4096, 256, 8, 2), (4, 7168, 128, 4, 2), (20, 2880, 192, 2, 1), (40, 128, 2048, 2, 1),
+           (70, 192, 2880, 3, 1), (40, 8192, 128, 2, 1), (33, 128, 4160, 2, 1), (2, 16384, 64, 3, 2),
+           (512, 64, 64, 1024, 8), (64, 64, 64, 70, 64)]
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+@pytest.mark.parametrize("size", LAYOUTS, ids=ids_of)
+def test_layouts_of_the_streaming_kernels(size, fp8):
+    require_gpu()
+    M, K, I, E, topk = size  # noqa: E741
+    c = make_moe(fp8, M, K, I, E, topk, "bf16", seed=K + I, masked=0.05)
+    want, tol = moe_want(c)
+    assert_within(run(c, path=STREAM[fp8]), want, tol, "bf16", f"{size}")
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+@pytest.mark.parametrize("M", [1, 3])
+def test_rows_that_no_lds_holds_take_the_generic_kernels(fp8, M):
+    require_gpu()
+    c = make_moe(fp8, M, 98304, 64, 2, 2, "bf16", seed=M)
+    want, tol = moe_want(c)
+    assert_within(run(c), want, tol, "bf16")
+    with pytest.raises(fw.FP4WError) as e:
+        run(c, path=STREAM[fp8])
+    assert e.value.status == fw.ERR_PATH
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+def test_one_token_with_many_choices(fp8):
+    """A single token: topk up to 64, masked and repeated choices, rows that do and do not fit beside the ring."""
+    require_gpu()
+    for K, I, E, topk in ((128, 64, 70, 64), (512, 320, 9, 9), (192, 2048, 12, 8), (256, 1024, 20, 16), (64, 128, 3, 5)):  # noqa: E741
+        c = make_moe(fp8, 1, K, I, E, topk, "bf16", seed=K + topk)
+        c["ids"][0, topk // 2] = -1
+        c["ids"][0, -1] = c["ids"][0, 0]
+        want, tol = moe_want(c)
+        assert_within(run(c, path=STREAM[fp8]), want, tol, "bf16", f"{(K, I, E, topk)}")
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
