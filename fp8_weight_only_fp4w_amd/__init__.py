@@ -171,9 +171,9 @@ def fp4w_select_path(op: int, M: int, N: int, K: int, block_size: int, scale_col
 # ---------------------------------------------------------------- marshalling
 
 def _dtype_code(t: torch.dtype) -> int:
-    if t == torch.bfloat16:
+    if t is torch.bfloat16:
         return BF16
-    if t == torch.float16:
+    if t is torch.float16:
         return F16
     raise TypeError(f"activation dtype must be float16 or bfloat16, got {t}")
 
@@ -490,21 +490,20 @@ def fp4w_matmul_w4a4_noalloc(A: torch.Tensor, B: torch.Tensor, weight_scale: tor
 
 # A call of these takes the GPU a few microseconds, so its marshalling is kept
 # short: the stream's handle comes straight from torch (a torch.cuda.Stream
-# object costs 1.8 us, the rest of a call about 4), and each tensor is checked
-# by one expression.
+# object costs 1.8 us, the launch itself about 3), and each tensor is checked by
+# one expression; what does not fit is looked at again for the message.
 
 def _call(device: torch.device, f, what: str, *args):
     """Call f(*args, stream) on the device's current stream, with that device current."""
     index = device.index
     if device.type != "cuda":
         raise ValueError(f"{what} runs on the GPU, got tensors on {device}")
-    stream = torch._C._cuda_getCurrentRawStream(index)
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(index):
-            status = f(*args, stream)
+    if index == torch._C._cuda_getDevice():
+        status = f(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        status = f(*args, stream)
-    if status != OK:
+        with torch.cuda.device(index):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status:
         raise FP4WError(status, what)
 
 
@@ -514,9 +513,9 @@ def _data(t):
 
 def _typed(t: torch.Tensor, name: str, dtype: torch.dtype, shape, device: torch.device):
     """t has this type and shape, is contiguous and on the device."""
-    if t.dtype == dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
         return
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
     _need(t, name, device)
 
@@ -627,52 +626,57 @@ def _moe(fp8, A, ids, weights, w13, s13, g13, w2, s2, g2, block_size, activation
     code = _dtype_code(A.dtype)
     if block_size < 1:
         raise FP4WError(ERR_BLOCK, what)
-    if w13.dtype != torch.uint8 or w2.dtype != torch.uint8:
+    u8, f32 = torch.uint8, torch.float32
+    if w13.dtype is not u8 or w2.dtype is not u8:
         w13, w2 = _bytes(w13), _bytes(w2)
-    K = A.shape[-1]
-    lead = A.shape[:-1]
-    M = lead.numel()
-    topk = ids.shape[-1]
-    if w13.dim() != 3 or w2.dim() != 3:
+    shape, chosen, size2 = A.shape, ids.shape, w2.shape
+    K, topk = shape[-1], chosen[-1]
+    M = A.numel() // K if K else shape[:-1].numel()
+    if w13.dim() != 3 or len(size2) != 3:
         raise ValueError("w13 must be [E, 2 I, K] and w2 [E, K, I] (FP4: two codes per byte)")
-    E, half = w2.shape[0], 1 if fp8 else 2
-    I = w2.shape[2] * half  # noqa: E741
-    if K % half or w13.shape != (E, 2 * I, K // half) or w2.shape[1] != K:
-        raise ValueError(f"w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not fit A's K = {K}")
+    E, half = size2[0], 1 if fp8 else 2
+    I = size2[2] * half  # noqa: E741
+    if K % half or w13.shape != (E, 2 * I, K // half) or size2[1] != K:
+        raise ValueError(f"w13 {tuple(w13.shape)} and w2 {tuple(size2)} do not fit A's K = {K}")
+    if chosen[:-1] != shape[:-1]:
+        raise ValueError(f"ids must be [..., topk] with A's leading dimensions, got {tuple(chosen)}")
     _need(A, "A", dev)
-    _typed(ids, "ids", torch.int32, (*lead, topk), dev)
-    _typed(weights, "weights", torch.float32, (*lead, topk), dev)
+    _typed(ids, "ids", torch.int32, chosen, dev)
+    _typed(weights, "weights", f32, chosen, dev)
     _need(w13, "w13", dev)
     _need(w2, "w2", dev)
-    scale_type = torch.float32 if fp8 else torch.uint8
-    if not fp8 and (s13.dtype != torch.uint8 or s2.dtype != torch.uint8):
-        s13, s2 = _bytes(s13), _bytes(s2)
+    scale_type = f32 if fp8 else u8
+    if not fp8:
+        if s13.dtype is not u8 or s2.dtype is not u8:
+            s13, s2 = _bytes(s13), _bytes(s2)
+        _typed(g13, "w13_scale_2", f32, (E,), dev)
+        _typed(g2, "w2_scale_2", f32, (E,), dev)
     _typed(s13, "w13_scale", scale_type, (E, 2 * I, -(-K // block_size)), dev)
     _typed(s2, "w2_scale", scale_type, (E, K, -(-I // block_size)), dev)
-    if not fp8:
-        _typed(g13, "w13_scale_2", torch.float32, (E,), dev)
-        _typed(g2, "w2_scale_2", torch.float32, (E,), dev)
     if workspace is None:
-        need = fp4w_moe_workspace(M, topk, K, I)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        held = lib.fp4w_moe_workspace(M, topk, K, I)
+        if held < 0:
+            raise FP4WError(held, what)
+        workspace = torch.empty(held, dtype=u8, device=dev)
     else:
         _need(workspace, "workspace", dev)
+        held = workspace.numel() * workspace.element_size()
     if out is None:
         out = torch.empty_like(A)
     else:
         _typed(out, "out", A.dtype, A.shape, dev)
-    head = (A.data_ptr(), M, K, ids.data_ptr(), weights.data_ptr(), topk, w13.data_ptr(), s13.data_ptr())
-    mid = (w2.data_ptr(), s2.data_ptr())
-    if not fp8:
-        head, mid = head + (g13.data_ptr(),), mid + (g2.data_ptr(),)
-    tail = (E, I, block_size, ACTIVATIONS[activation], workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), out.data_ptr(), code)
+    tail = (E, I, block_size, ACTIVATIONS[activation], workspace.data_ptr(), held, out.data_ptr(), code)
+    if fp8:
+        args = (A.data_ptr(), M, K, ids.data_ptr(), weights.data_ptr(), topk, w13.data_ptr(), s13.data_ptr(),
+                w2.data_ptr(), s2.data_ptr(), *tail)
+    else:
+        args = (A.data_ptr(), M, K, ids.data_ptr(), weights.data_ptr(), topk, w13.data_ptr(), s13.data_ptr(),
+                g13.data_ptr(), w2.data_ptr(), s2.data_ptr(), g2.data_ptr(), *tail)
     if path == PATH_AUTO:
-        f = lib.fp8w_moe if fp8 else lib.fp4w_moe
-        _call(dev, f, what, *head, *mid, *tail)
+        _call(dev, lib.fp8w_moe if fp8 else lib.fp4w_moe, what, *args)
     else:
         f = lib.fp8w_moe_ex if fp8 else lib.fp4w_moe_ex
-        _call(dev, lambda *a: f(*a, path), what, *head, *mid, *tail)
+        _call(dev, lambda *a: f(*a, path), what, *args)
     return out
 
 
