@@ -69,7 +69,7 @@ F16, BF16, F32 = 0, 1, 2
 # scores (fp4w_score) and activations (fp4w_activation) by name
 SCORES = {"softmax": 0, "sigmoid": 1}
 ACTIVATIONS = {"silu": 0, "gelu": 1}
-MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_MAX_ASSIGNMENTS = 1024, 64, 4096
+MOE_MAX_EXPERTS, MOE_MAX_TOPK = 1024, 64
 
 EXPORTED = (
     "fp4w_matmul", "fp4w_matmul_ex", "fp8w_matmul", "fp8w_matmul_ex", "fp4w_dequant",

@@ -24,6 +24,18 @@ using fp4w::overlaps;
 
 bool dtype_ok(int dtype) { return dtype == FP4W_F16 || dtype == FP4W_BF16; }
 
+// M and M * topk of a call stay below it.
+constexpr int64_t kMaxTokens = int64_t(1) << 31;
+
+// A call works through its tokens in parts of equal size with at most this
+// many choices: the kernels sort a part's choices in LDS, and the workspace
+// does not grow beyond a part's.
+constexpr int64_t kPartChoices = 4096;
+int64_t part_tokens(int64_t M, int64_t topk) {
+  const int64_t most = topk > 0 ? kPartChoices / topk : M;
+  return M <= most ? M : ceil_div(M, ceil_div(M, most));
+}
+
 int64_t align256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 // Sizes of one layer.  Returns FP4W_OK or an error status.
@@ -32,9 +44,9 @@ int check_moe(bool fp8, int64_t M, int64_t K, int64_t topk, int64_t E, int64_t I
   if (bs < 1) return FP4W_ERR_BLOCK;
   if (!fp8 && (K % 2 != 0 || I % 2 != 0)) return FP4W_ERR_SHAPE;  // two E2M1 codes per byte
   if (E > FP4W_MOE_MAX_EXPERTS || topk > FP4W_MOE_MAX_TOPK) return FP4W_ERR_SHAPE;
-  if (M > FP4W_MOE_MAX_ASSIGNMENTS || M * topk > FP4W_MOE_MAX_ASSIGNMENTS) return FP4W_ERR_SHAPE;
+  if (M >= kMaxTokens || M * topk >= kMaxTokens) return FP4W_ERR_SHAPE;
   // byte counts of the weights, the intermediate and the outputs below 2^63
-  if (!mul_ok(K, I) || !mul_ok(2 * E, K * I) || K > (int64_t(1) << 40) || I > (int64_t(1) << 40)) return FP4W_ERR_SHAPE;
+  if (!mul_ok(4 * M, K) || !mul_ok(K, I) || !mul_ok(2 * E, K * I) || K > (int64_t(1) << 40) || I > (int64_t(1) << 40)) return FP4W_ERR_SHAPE;
   return FP4W_OK;
 }
 
@@ -55,8 +67,20 @@ bool stream_ok(bool fp8, const MoeArgs& a) {
 
 // H (4 bytes a value), then the outputs of the single choices in FP32, once
 // for each part of the sum over I
-int64_t workspace_bytes(int64_t M, int64_t topk, int64_t K, int64_t I) {
+int64_t workspace_bytes(int64_t tokens, int64_t topk, int64_t K, int64_t I) {
+  const int64_t M = part_tokens(tokens, topk);
   return align256(M * topk * I * 4) + fp4w::moe_down_splits(M, I) * align256(M * topk * K * 4);
+}
+
+// The call's arguments for the tokens behind a's.
+void next_part(MoeArgs& a) {
+  const int64_t row = a.M * a.K * 2, n = a.M * a.topk;
+  a.Y = static_cast<unsigned char*>(a.Y) + row;
+  if (a.A != nullptr) a.A = static_cast<const unsigned char*>(a.A) + row;
+  if (n > 0) {
+    a.ids += n;
+    a.weights += n;
+  }
 }
 
 int run_moe(bool fp8, MoeArgs a, int64_t work_bytes, int path) {
@@ -99,13 +123,20 @@ int run_moe(bool fp8, MoeArgs a, int64_t work_bytes, int path) {
   for (const auto& in : inputs)
     if (overlaps(a.Y, ybytes, in.p, in.bytes) || overlaps(a.work, need, in.p, in.bytes)) return FP4W_ERR_ALIAS;
   if (overlaps(a.Y, ybytes, a.work, need)) return FP4W_ERR_ALIAS;
+  const int64_t M = a.M, step = part_tokens(M, a.topk);
+  a.M = step;  // the first part is a largest one
   const bool fast = terms && stream_ok(fp8, a);
   if (path == stream_path(fp8) && !fast) return FP4W_ERR_PATH;
-  int rc = 1;  // 1: the streaming kernels do not take the row length
-  if (fast && path != generic_path(fp8)) rc = fp8 ? fp4w::launch_moe_fp8(a) : fp4w::launch_moe_fp4(a);
-  if (rc == 1 && path == stream_path(fp8)) return FP4W_ERR_PATH;
-  if (rc == 1) rc = fp8 ? fp4w::launch_moe_fp8_generic(a) : fp4w::launch_moe_fp4_generic(a);
-  return rc == 0 ? FP4W_OK : FP4W_ERR_LAUNCH;
+  for (int64_t m = 0; m < M; m += step) {
+    a.M = std::min(step, M - m);
+    int rc = 1;  // 1: the streaming kernels do not take the row length
+    if (fast && path != generic_path(fp8)) rc = fp8 ? fp4w::launch_moe_fp8(a) : fp4w::launch_moe_fp4(a);
+    if (rc == 1 && path == stream_path(fp8)) return FP4W_ERR_PATH;
+    if (rc == 1) rc = fp8 ? fp4w::launch_moe_fp8_generic(a) : fp4w::launch_moe_fp4_generic(a);
+    if (rc != 0) return FP4W_ERR_LAUNCH;
+    if (m + step < M) next_part(a);
+  }
+  return FP4W_OK;
 }
 
 }  // namespace

@@ -358,7 +358,6 @@ int fp4w_block_norm(const void* x, int64_t M, int64_t K, const void* post_weight
 
 #define FP4W_MOE_MAX_EXPERTS 1024
 #define FP4W_MOE_MAX_TOPK 64
-#define FP4W_MOE_MAX_ASSIGNMENTS 4096 /* M * topk of one fp4w_moe / fp8w_moe call */
 
 typedef enum { FP4W_SCORE_SOFTMAX = 0, FP4W_SCORE_SIGMOID = 1 } fp4w_score;
 typedef enum { FP4W_ACT_SILU = 0, FP4W_ACT_GELU_TANH = 1 } fp4w_activation;
@@ -395,8 +394,8 @@ int fp4w_moe_route(const void* logits, int64_t M, int64_t E, int64_t topk, int s
 int64_t fp4w_moe_workspace(int64_t M, int64_t topk, int64_t K, int64_t I);
 
 /*
- * fp4w_moe - a whole mixture-of-experts layer on FP4 weights, for a few
- * tokens (decode, small batches).  With e = ids[m, j] and W1[e], W3[e] the
+ * fp4w_moe - a whole mixture-of-experts layer on FP4 weights, made for a few
+ * tokens (decode, small batches) and taking any number.  With e = ids[m, j] and W1[e], W3[e] the
  * first and last I rows of w13[e]:
  *   h    = act(A[m] . W1[e]^T) * (A[m] . W3[e]^T)
  *   Y[m] = sum_j weights[m, j] * (h . W2[e]^T)
@@ -422,7 +421,9 @@ int64_t fp4w_moe_workspace(int64_t M, int64_t topk, int64_t K, int64_t I);
  *                one each.
  *   Y            T[M, K] (written).
  * K and I must be even, E <= FP4W_MOE_MAX_EXPERTS, topk <= FP4W_MOE_MAX_TOPK
- * and M * topk <= FP4W_MOE_MAX_ASSIGNMENTS.  M == 0 or K == 0: FP4W_OK,
+ * and M, M * topk < 2^31.  A call works through its tokens in parts of at most
+ * 4096 choices, one after the other in the same workspace, and every part
+ * reads the weights of the experts that its tokens name.  M == 0 or K == 0: FP4W_OK,
  * nothing launched.  topk == 0, E == 0 or I == 0: Y = 0 (an empty sum).
  * Errors: FP4W_ERR_NULL, FP4W_ERR_SHAPE (also a workspace that is too small
  * or unaligned), FP4W_ERR_BLOCK, FP4W_ERR_DTYPE (also an unknown activation),

@@ -91,7 +91,7 @@ def test_moe_refusals(f):
     assert f(act=2) == fw.ERR_DTYPE
     assert f(bs=0) == fw.ERR_BLOCK
     for bad in (dict(M=-1), dict(K=-2), dict(E=-1), dict(I=-2), dict(topk=-1), dict(E=fw.MOE_MAX_EXPERTS + 1),
-                dict(topk=fw.MOE_MAX_TOPK + 1), dict(M=fw.MOE_MAX_ASSIGNMENTS // 2 + 1), dict(M=1 << 62),
+                dict(topk=fw.MOE_MAX_TOPK + 1), dict(M=1 << 30), dict(M=1 << 31, topk=0), dict(M=1 << 62),
                 dict(K=1 << 42), dict(K=1 << 30, I=1 << 30, E=1024)):
         assert f(**bad) == fw.ERR_SHAPE, bad
     for name in ("A", "ids", "w", "w13", "s13", "w2", "s2", "work", "Y"):
@@ -121,7 +121,10 @@ def test_workspace_size():
     assert fw.fp4w_moe_workspace(4, 8, 128, 64) >= 4 * 8 * 64 * 4
     assert fw.load_library().fp4w_moe_workspace(-1, 8, 128, 64) == fw.ERR_SHAPE
     with pytest.raises(fw.FP4WError):
-        fw.fp4w_moe_workspace(4096, 2, 128, 64)
+        fw.fp4w_moe_workspace(1 << 30, 2, 128, 64)
+    # many tokens are worked through in parts: the workspace stays that of one
+    assert fw.fp4w_moe_workspace(1 << 29, 2, 128, 64) == fw.fp4w_moe_workspace(2048, 2, 128, 64)
+    assert fw.fp4w_moe_workspace(2049, 2, 128, 64) <= fw.fp4w_moe_workspace(2048, 2, 128, 64)
 
 
 @pytest.mark.parametrize("fp8", [False, True])

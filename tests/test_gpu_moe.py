@@ -129,6 +129,26 @@ def test_all_tokens_to_one_expert(fp8):
 
 
 @pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+@pytest.mark.parametrize("size", [(520, 128, 64, 16, 8), (4097, 64, 64, 3, 1), (130, 64, 128, 70, 64), (65, 66, 34, 70, 64)],
+                         ids=ids_of)
+def test_tokens_beyond_one_part(size, fp8):
+    """More choices than the kernels sort at once: parts of the tokens, in one workspace, nothing behind the last row."""
+    require_gpu()
+    M, K, I, E, topk = size  # noqa: E741
+    c = make_moe(fp8, M, K, I, E, topk, "bf16", seed=M + E, masked=0.05)
+    want, tol = moe_want(c)
+    d = moe_on(c)
+    Y = torch.full((M + 2, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    moe_call(fw, c, d, out=Y[:M])
+    assert_within(Y[:M], want, tol, "bf16", f"{size}")
+    assert (Y[M:] == 7).all()
+    s = slice(M // 2, M // 2 + 9)  # a token's result does not hang on its part
+    e = {**d, **{k: d[k][s].contiguous() for k in ("A", "ids", "weights")}}
+    near, near_tol = want[s], tol[s]
+    assert_within(moe_call(fw, c, e), near, near_tol, "bf16", f"{size}")
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
 def test_empty(fp8):
     require_gpu()
     for M, K, I, E, topk in ((0, 128, 64, 4, 2), (3, 0, 64, 4, 2), (3, 128, 0, 4, 2), (3, 128, 64, 0, 2), (3, 128, 64, 4, 0)):  # noqa: E741
