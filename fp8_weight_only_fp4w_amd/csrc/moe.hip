@@ -43,6 +43,18 @@
 //  * FP8: E4M3 -> T is exact, a 128-k window (inside one scale block) is summed
 //    in a fresh accumulator and added times its FP32 scale.
 //
+// Measured (us of a layer, GPU time; in brackets the bytes of the experts named
+// at the 4.8 TB/s of a large copy): FP4, 1 token on 8 of 128 experts of 2048 x
+// 768: 13.5 (4.4); 4 tokens on 7168 x 2048: 136 (137); 32 on 2048 x 768: 68
+// (62); 128 on 32 experts of 2880 x 2880: 178 (93).  FP8, 1 token on 6 experts
+// of 2048 x 1408: 17.4 (11); 16 on 4096 x 1024: 177 (223); 100 on a quarter of
+// 64 experts of 5120 x 1280: 99 (68).  About 7 us of each of the two kernels
+// are launch, plan, token rows and first weights, 5 to 8 the combination; one
+// token saves the plan and the third launch.  Beyond some ten tokens an expert
+// the arithmetic takes longer than the bytes: with 16 each, of FP4 experts,
+// the first kernel takes 108 of its 118 us when the weights cost nothing, and
+// 97 when they are loaded but not multiplied.
+//
 // H is handed from up to down as two BF16 planes, high part and remainder (16
 // significand bits, FP32's exponent range): one BF16 or FP16 rounding of H
 // would double the output's error, and in FP16 gate * up may overflow.  The
@@ -342,9 +354,11 @@ constexpr int kAheadLoads = 2 * Q + 1;
 
 // RING: the weights travel through a private LDS ring instead, Q + 1 slots of a
 // unit, by direct loads of 8 rows x 128 bytes, whose requests are whole lines:
-// that streams 6.4 TB/s against 5.9 straight into registers (FP8, 128 experts
-// of 4096 x 1024: 169 against 181 us), where the token rows leave it 64 KiB
-// of LDS.  A row's chunks are loaded in the order chunk ^ (row & 7), so the
+// that streams 6.4 TB/s against 5.9 straight into registers (FP8, 16 tokens on
+// 128 experts of 4096 x 1024: 177 against 181 us; FP4, 8 tokens on 32 experts
+// of 2880 x 2880: 76.5 against 77.7).  It is taken where the token rows leave
+// it 80 KiB of LDS: rows that fit only without it would otherwise become more
+// passes, each of which reads the weights again.  A row's chunks are loaded in the order chunk ^ (row & 7), so the
 // reads are free of bank conflicts.
 constexpr uint32_t kSlotBytes = 2048;
 constexpr uint32_t kRingBytes = kWaves * (Q + 1) * kSlotBytes;
@@ -1110,12 +1124,14 @@ size_t rows_lds_bytes(int64_t rows, int planes, int windows) {
 
 // The K split of a tile over KS waves.  The larger it is, the smaller the
 // groups of tiles that are shared out and the better the shares' bytes match,
-// but every tile then ends with a join: measured (us of a layer; the split of
-// up) FP4 K = 7168, 28 units of a row: 152 at 1, 142 at 2, 139 at 4, 137 at 8;
-// FP4 K = 2048, 8 units: 73.6, 73.9, 80.9, 88.5; FP8 K = 4096, 32 units: 185,
-// 175, 173, 172; FP8 I = 1024 (down), 8 units: 171.7, 170.2, 173.0, 180.7.  So:
-// the largest split that leaves a wave four units of a tile, and beyond that
-// only as far as the workgroups would not fill the chip.
+// but every tile then ends with a join.  Measured, us of a layer with the split
+// of up at 1, 2, 4 and 8: FP4 K = 7168, 28 units of a row: 142.6, 135.8, 135.4,
+// 133.9; FP4 K = 2048, 8 units: 76.4, 75.9, 83.0, 99.3; FP8 K = 4096, 32 units:
+// 180.6, 176.7, 175.5, 178.0; FP4 K = 2880, 12 units: 183, 185, 209, 255.  And
+// with that of down at 2 and 4: FP8 I = 1024, 8 units: 178.2, 181.9; FP8 I =
+// 1280, 10 units: 99.1, 116.4.  So: the largest split that leaves a wave four
+// units of a tile, and beyond that only as far as the workgroups would not
+// fill the chip.
 int k_split(int NU, int64_t tiles, int64_t passes, int64_t cus) {
   int ks = 1;
   while (ks < kWaves && NU >= 8 * ks) ks *= 2;
