@@ -45,10 +45,10 @@
 //
 // Measured (us of a layer, GPU time; in brackets the bytes of the experts named
 // at the 4.8 TB/s of a large copy): FP4, 1 token on 8 of 128 experts of 2048 x
-// 768: 13.5 (4.4); 4 tokens on 7168 x 2048: 136 (137); 32 on 2048 x 768: 68
+// 768: 13.5 (4.4); 4 tokens on 7168 x 2048: 136 (137); 32 on 2048 x 768: 67
 // (62); 128 on 32 experts of 2880 x 2880: 178 (93).  FP8, 1 token on 6 experts
-// of 2048 x 1408: 17.4 (11); 16 on 4096 x 1024: 177 (223); 100 on a quarter of
-// 64 experts of 5120 x 1280: 99 (68).  About 7 us of each of the two kernels
+// of 2048 x 1408: 17.4 (11); 16 on 4096 x 1024: 175 (223); 100 on a quarter of
+// 64 experts of 5120 x 1280: 95.5 (68).  About 7 us of each of the two kernels
 // are launch, plan, token rows and first weights, 5 to 8 the combination; one
 // token saves the plan and the third launch.  Beyond some ten tokens an expert
 // the arithmetic takes longer than the bytes: with 16 each, of FP4 experts,
@@ -1055,7 +1055,9 @@ __global__ __launch_bounds__(kThreads) void moe_token_kernel(const MoeParams p, 
 
 // Y[m, c .. c + 3] = sum over j of weights[a] * (sum over s of P[s][a, c ..]), a = m * topk + j, in order.
 // A few microseconds of latency at these sizes: eight choices' loads at a
-// time, none of them behind a branch (what a masked choice holds is not used).
+// time, none of them behind a branch.  A masked choice reads the token's first
+// one instead of its own and does not use it: 100 tokens with three choices in
+// four masked take 95.5 us instead of 98.5, where none is masked nothing is lost.
 template <typename T>
 __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restrict__ P, const int32_t* __restrict__ ids,
                                                           const float* __restrict__ weights, T* __restrict__ Y, int M,
@@ -1071,17 +1073,19 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
       f32x4 x[8];
       float w[8];
       bool on[8];
+      size_t at[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int k = min(j0 + j, topk - 1);
-        x[j] = *reinterpret_cast<const f32x4*>(q + static_cast<size_t>(k) * K);
         w[j] = weights[m * topk + k];
         on[j] = j0 + j < topk && static_cast<uint32_t>(ids[m * topk + k]) < static_cast<uint32_t>(E);
+        at[j] = on[j] ? static_cast<size_t>(k) * K : 0;
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = *reinterpret_cast<const f32x4*>(q + at[j]);
       for (int s = 1; s < splits; ++s) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          x[j] += *reinterpret_cast<const f32x4*>(q + s * part + static_cast<size_t>(min(j0 + j, topk - 1)) * K);
+        for (int j = 0; j < 8; ++j) x[j] += *reinterpret_cast<const f32x4*>(q + s * part + at[j]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
