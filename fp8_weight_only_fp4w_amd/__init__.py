@@ -549,7 +549,7 @@ def fp4w_block_norm(x: torch.Tensor, residual: torch.Tensor = None, pre_weight: 
     if gate is not None:
         if gate.shape == shape:
             gate_rows = M
-        elif gate.dim() > 2 or gate.numel() != K:
+        elif gate.shape != (K,) and gate.shape != (1, K):
             raise ValueError(f"gate must be [{K}] or {tuple(shape)}, got {tuple(gate.shape)}")
         _typed(gate, "gate", dtype, gate.shape, dev)
     if not write_residual:
@@ -630,6 +630,9 @@ def _moe(fp8, A, ids, weights, w13, s13, g13, w2, s2, g2, block_size, activation
     if w13.dtype is not u8 or w2.dtype is not u8:
         w13, w2 = _bytes(w13), _bytes(w2)
     shape, chosen, size2 = A.shape, ids.shape, w2.shape
+    if not shape or chosen[:-1] != shape[:-1] or not chosen:
+        raise ValueError(f"A must be [..., K] and ids [..., topk] with the same leading dimensions, got {tuple(shape)} "
+                         f"and {tuple(chosen)}")
     K, topk = shape[-1], chosen[-1]
     M = A.numel() // K if K else shape[:-1].numel()
     if w13.dim() != 3 or len(size2) != 3:
@@ -638,8 +641,6 @@ def _moe(fp8, A, ids, weights, w13, s13, g13, w2, s2, g2, block_size, activation
     I = size2[2] * half  # noqa: E741
     if K % half or w13.shape != (E, 2 * I, K // half) or size2[1] != K:
         raise ValueError(f"w13 {tuple(w13.shape)} and w2 {tuple(size2)} do not fit A's K = {K}")
-    if chosen[:-1] != shape[:-1]:
-        raise ValueError(f"ids must be [..., topk] with A's leading dimensions, got {tuple(chosen)}")
     _need(A, "A", dev)
     _typed(ids, "ids", torch.int32, chosen, dev)
     _typed(weights, "weights", f32, chosen, dev)

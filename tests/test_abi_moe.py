@@ -176,6 +176,23 @@ def test_binding_refuses_norm_and_route_arguments():
         fw.fp4w_moe_route(logits, -1)
 
 
+def test_binding_refuses_a_column_as_the_row_of_gates():
+    """[K, 1] has K values, but they would be one for each row."""
+    x = torch.zeros(16, 16, dtype=torch.bfloat16)
+    for gate in (torch.zeros(16, 1), torch.zeros(4, 4), torch.zeros(1, 1, 16)):
+        with pytest.raises(ValueError, match="gate must be"):
+            fw.fp4w_block_norm(x, gate=gate.bfloat16())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_binding_refuses_tensors_without_dimensions(fp8):
+    c = make_moe(fp8, 2, 64, 32, 4, 2, "bf16", 1)
+    good = moe_on(c, "cpu")
+    for name in ("A", "ids"):
+        with pytest.raises(ValueError, match="leading dimensions"):
+            moe_call(fw, c, dict(good, **{name: good[name][0, 0]}))
+
+
 @pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
 def test_dispatch_moe_under_asan_ubsan(tmp_path):
     """The validation and dispatch, built with g++ under AddressSanitizer and
