@@ -685,8 +685,8 @@ def fp4w_moe(A: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: tor
              w13_scale_2: torch.Tensor, w2: torch.Tensor, w2_scale: torch.Tensor, w2_scale_2: torch.Tensor,
              block_size: int = 16, activation: str = "silu", out: torch.Tensor = None,
              workspace: torch.Tensor = None, path: int = PATH_AUTO) -> torch.Tensor:
-    """A whole mixture-of-experts layer on FP4 weights, for a few tokens: for
-    each token the sum over its choices j, e = ids[..., j], of
+    """A whole mixture-of-experts layer on FP4 weights, made for a few tokens and
+    taking any number: for each token the sum over its choices j, e = ids[..., j], of
 
         weights[..., j] * ((act(A w13[e, :I]^T) * (A w13[e, I:]^T)) w2[e]^T)
 
@@ -695,7 +695,7 @@ def fp4w_moe(A: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: tor
     nothing.  ``w13`` [E, 2 I, K/2], ``w2`` [E, K, I/2] packed E2M1 with E4M3
     scales per block and one float32 scale per expert.  ``workspace`` holds
     ``fp4w_moe_workspace(M, topk, K, I)`` bytes; it is allocated here when not
-    given."""
+    given.  Calls that may run at once need one each."""
     return _moe(False, A, ids, weights, w13, w13_scale, w13_scale_2, w2, w2_scale, w2_scale_2, block_size, activation,
                 out, workspace, path)
 

@@ -218,7 +218,7 @@ inline int64_t moe_down_splits(int64_t M, int64_t I) {
 // 0), block_size 16 (FP4) or a multiple of 128 (FP8); A, w13, w2, work and Y
 // 16-byte aligned, scales 4-byte; A, an expert's matrices and n x I x 4 below
 // 2^31 bytes.  Return 1, launching nothing, when a token's row does not fit in
-// LDS.
+// LDS, or the shares of the work cannot be counted in 32 bits.
 int launch_moe_fp4(const MoeArgs& a);
 int launch_moe_fp8(const MoeArgs& a);
 // any validated arguments with M, K > 0 (E, topk and I may be 0)
