@@ -35,6 +35,9 @@ namespace fp4w {
 namespace {
 
 constexpr int kRouteWaves = 4;  // rows per workgroup
+// Scores below exp of it (softmax: times the largest) count as 0: FP64, which
+// the keys are formed in, ends there.
+constexpr float kScoreEnd = -700.0f;
 
 template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
@@ -89,6 +92,9 @@ __device__ __forceinline__ uint64_t order_key(double x) {
   const uint64_t b = __builtin_bit_cast(uint64_t, x + 0.0);
   return b >> 63 ? ~b : b | (uint64_t(1) << 63);
 }
+__device__ __forceinline__ float from_order_key(uint32_t k) {
+  return __builtin_bit_cast(float, k >> 31 ? k & 0x7FFFFFFFu : ~k);
+}
 // exp(x - top), 1 where x is the top itself (+inf included)
 __device__ __forceinline__ float exp_below(float x, float top) { return x == top ? 1.0f : expf(x - top); }
 
@@ -114,7 +120,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(
 #pragma unroll
     for (int j = 0; j < PER; ++j) top_key = max(top_key, order_key(x[j]));
     top_key = wave_max(top_key);
-    if (top_key) top = __builtin_bit_cast(float, top_key >> 31 ? top_key & 0x7FFFFFFFu : ~top_key);
+    if (top_key) top = from_order_key(top_key);
     // the softmax's denominator, where it is needed
     float sum = 1.0f;
     double sum64 = 1.0;
@@ -193,12 +199,29 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(
       const float t = __shfl(x[j], from / PER, 64);
       if (from % PER == j) xs = t;
     }
+    // Renormalised scores count in units of exp(ref), where ref is the largest
+    // chosen logit: from 87 below 0 (the top) on FP32 would lose the scores,
+    // and their quotients with them.  Without a bias ref is the top, and with
+    // one it is looked for only where it is below 0 (the top).
+    const float most = sigmoid ? 0.0f : top;
+    float ref = most;
+    if constexpr (BIAS) {
+      if (renormalize && __ballot(my_id >= 0 && xs >= most) == 0) {
+        const uint32_t k = wave_max(my_id < 0 ? 0u : order_key(xs));
+        if (k) ref = from_order_key(k);
+      }
+    } else if (renormalize) {
+      ref = fminf(top, most);
+    }
     float w;
     if (sigmoid) {
       const float e = expf(-fabsf(xs));
-      w = (xs < 0.0f ? e : 1.0f) / (1.0f + e);
+      w = xs < 0.0f ? e : 1.0f;
+      if (ref < 0.0f) w = xs > kScoreEnd ? expf(xs - ref) : 0.0f;
+      w = w / (1.0f + e);
     } else {
-      w = exp_below(xs, top);
+      w = exp_below(xs, ref);
+      if (BIAS && ref < top && xs - top <= kScoreEnd) w = 0.0f;
     }
     if (my_id < 0) w = 0.0f;
     if (renormalize) {

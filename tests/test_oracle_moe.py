@@ -106,3 +106,17 @@ def test_block_norm_parts():
     assert y is None and r.tolist() == [[6.0, -8.0]]
     r, y, *_ = om.block_norm(x, None, np.array([1.0, 2.0]), eps=0.0)
     assert np.allclose(y, [[3 / math.sqrt(12.5), -8 / math.sqrt(12.5)]])
+
+
+def test_renormalised_weights_of_small_scores():
+    """sigmoid(x) is exp(x) to 1e-40 that far below 0, so the quotients are a softmax of the chosen logits."""
+    x = np.array([[-200.0, -201.0, -203.5, -200.0], [-600.0, -601.0, -640.0, -700.5]])
+    ids, w, _ = om.route(x, 3, "sigmoid")
+    assert ids.tolist() == [[0, 3, 1], [0, 1, 2]]
+    for m, z in enumerate(([0, 0, -1], [0, -1, -40])):
+        total = math.fsum(math.exp(v) for v in z)
+        assert np.allclose(w[m], [math.exp(v) / total for v in z], rtol=1e-12)
+    bias = np.array([-10.0, 1, 1, 2], np.float32)
+    ids, w, _ = om.route(np.array([[0.0, -120, -121, -119], [0, -760, -770, -800]]), 2, "softmax", bias)
+    assert ids.tolist() == [[3, 1]] * 2
+    assert np.allclose(w[0], [1 / (1 + math.exp(-1)), 1 / (1 + math.e)], rtol=1e-12) and (w[1] == 0).all()
