@@ -610,7 +610,7 @@ def fp4w_moe_route(logits: torch.Tensor, topk: int, score: str = "softmax", sele
 
 
 def fp4w_moe_workspace(M: int, topk: int, K: int, I: int) -> int:  # noqa: E741
-    """Bytes of workspace that fp4w_moe and fp8w_moe need."""
+    """Bytes of workspace that fp4w_moe and fp8w_moe need; enough for every smaller call too."""
     n = int(load_library().fp4w_moe_workspace(M, topk, K, I))
     if n < 0:
         raise FP4WError(n, "fp4w_moe_workspace")

@@ -66,10 +66,12 @@ bool stream_ok(bool fp8, const MoeArgs& a) {
 }
 
 // H (4 bytes a value), then the outputs of the single choices in FP32, once
-// for each part of the sum over I
+// for each part of the sum over I.  Sized for a full part wherever there are
+// tokens for one: the parts of a larger call may be smaller than the only part
+// of a smaller one, and a buffer has to serve every call below its own size.
 int64_t workspace_bytes(int64_t tokens, int64_t topk, int64_t K, int64_t I) {
-  const int64_t M = part_tokens(tokens, topk);
-  return align256(M * topk * I * 4) + fp4w::moe_down_splits(M, I) * align256(M * topk * K * 4);
+  const int64_t n = std::min(tokens * topk, kPartChoices);
+  return align256(n * I * 4) + fp4w::moe_down_splits(tokens, I) * align256(n * K * 4);
 }
 
 // The call's arguments for the tokens behind a's.

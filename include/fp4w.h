@@ -392,7 +392,9 @@ int fp4w_moe_route(const void* logits, int64_t M, int64_t E, int64_t topk, int s
 
 /*
  * Bytes of caller-owned workspace that fp4w_moe and fp8w_moe need for these
- * sizes, or a negative fp4w_status for illegal ones.  Host-only.
+ * sizes, or a negative fp4w_status for illegal ones.  It does not fall when a
+ * size grows, so what a largest batch needs serves every smaller call.
+ * Host-only.
  */
 int64_t fp4w_moe_workspace(int64_t M, int64_t topk, int64_t K, int64_t I);
 

@@ -127,6 +127,29 @@ def test_workspace_size():
     assert fw.fp4w_moe_workspace(2049, 2, 128, 64) <= fw.fp4w_moe_workspace(2048, 2, 128, 64)
 
 
+@pytest.mark.parametrize("topk", [1, 2, 3, 5, 8, 63, 64])
+@pytest.mark.parametrize("K,I", [(2048, 768), (128, 5120), (7168, 2048)])
+def test_a_workspace_serves_every_smaller_call(K, I, topk):  # noqa: E741
+    """Whatever the parts that a call's tokens are cut into: the size never falls as M, topk or I grows."""
+    size = fw.fp4w_moe_workspace
+    most = 4096 // topk
+    last = 0
+    for M in sorted({*range(0, 40), *(n * most + d for n in (1, 2, 3, 5) for d in (-2, -1, 0, 1, 2, 7)), 100000, 1 << 24}):
+        if M < 0:
+            continue
+        need = size(M, topk, K, I)
+        assert need >= last, M
+        last = need
+        if topk > 1:
+            assert size(M, topk - 1, K, I) <= need
+        assert size(M, topk, K, max(0, I - 64)) <= need and size(M, topk, K - 64, I) <= need
+    # the buffer of a large batch takes a call at which a part is full
+    lib = fw.load_library()
+    held = lib.fp4w_moe_workspace(most + 1, topk, K, I)
+    for M in (most - 1, most):
+        assert lib.fp4w_moe_workspace(M, topk, K, I) <= held
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_binding_refuses_what_does_not_fit(fp8):
     c = make_moe(fp8, 2, 64, 32, 4, 2, "bf16", 1)

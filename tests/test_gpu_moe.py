@@ -335,3 +335,16 @@ def test_a_whole_block(fp8):
         again = block(xs)
         for p, q in zip(kept, again):
             assert torch.equal(p, q), k
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+def test_a_workspace_of_the_largest_batch_serves_smaller_ones(fp8):
+    """513 tokens of 8 choices are two parts, 512 are one, larger than either."""
+    require_gpu()
+    ws = torch.full((fw.fp4w_moe_workspace(513, 8, 128, 64),), 0xFF, dtype=torch.uint8, device="cuda")
+    c = make_moe(fp8, 513, 128, 64, 16, 8, "bf16", seed=31, masked=0.05)
+    want, tol = moe_want(c)
+    d = moe_on(c)
+    for M in (513, 512, 40, 1):
+        part = {**d, **{k: d[k][:M].contiguous() for k in ("A", "ids", "weights")}}
+        assert_within(moe_call(fw, c, part, workspace=ws), want[:M], tol[:M], "bf16", f"M {M}")
