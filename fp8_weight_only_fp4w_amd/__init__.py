@@ -579,8 +579,9 @@ def fp4w_moe_route(logits: torch.Tensor, topk: int, score: str = "softmax", sele
     [..., E] in float16, bfloat16 or float32: the topk experts of each token,
     best first, ties to the lowest index, and scale * their scores
     (renormalised to a sum of scale by default).  ``select_bias`` (float32
-    [E]) takes part in the choice only.  Experts with a logit of -inf or NaN
-    are never chosen; places left over get id -1 and weight 0."""
+    [E]) takes part in the choice only.  Experts with a logit or a logit's score
+    plus bias of -inf or NaN are never chosen (those with such a bias alone keep
+    their share of a softmax); places left over get id -1 and weight 0."""
     lib = load_library()
     dev = logits.device
     code = F32 if logits.dtype == torch.float32 else _dtype_code(logits.dtype)

@@ -372,11 +372,13 @@ typedef enum { FP4W_ACT_SILU = 0, FP4W_ACT_GELU_TANH = 1 } fp4w_activation;
  * Renormalised weights are right however small the scores are, to where FP64
  * ends: a score below e^-700 (softmax: e^-700 times the row's largest) counts
  * as 0, so choices masked by the type's lowest value weigh nothing beside
- * others.  The bias only takes part in the choice.  An expert whose logit or key is
- * -inf or NaN is masked: it is never chosen (and adds nothing to a softmax).  Places that
- * no expert is left for get id -1 and weight 0, which fp4w_moe skips; a row
- * with every expert masked is all such places.  Logits of +inf share the
- * softmax among themselves.
+ * others.  The bias only takes part in the choice.  An expert whose logit or
+ * key is -inf or NaN is masked: it is never chosen.  Masked by its logit, it
+ * adds nothing to a softmax; masked by select_bias alone, its share of the
+ * softmax stays (it shows where `renormalize` is 0).  Places that no expert is
+ * left for get id -1 and weight 0, which fp4w_moe skips; a row with every
+ * expert masked is all such places.  Logits of +inf share the softmax among
+ * themselves.
  *
  *   logits       logits_dtype[M, E]: FP4W_F16, FP4W_BF16 or FP4W_F32.
  *   select_bias  float[E] or NULL.
