@@ -348,3 +348,18 @@ def test_a_workspace_of_the_largest_batch_serves_smaller_ones(fp8):
     for M in (513, 512, 40, 1):
         part = {**d, **{k: d[k][:M].contiguous() for k in ("A", "ids", "weights")}}
         assert_within(moe_call(fw, c, part, workspace=ws), want[:M], tol[:M], "bf16", f"M {M}")
+
+
+@pytest.mark.parametrize("block_size", [256, 384, 640, 4096])
+@pytest.mark.parametrize("size", [(1, 1152, 320, 6, 3), (3, 448, 1408, 4, 2), (17, 2048, 192, 3, 2), (40, 704, 576, 2, 1),
+                                  (64, 192, 192, 16, 8)], ids=ids_of)
+def test_fp8_blocks_of_several_windows(size, block_size):
+    """Scale blocks of 2, 3 and 5 windows, whole and partial, and one block per row, through the streaming kernels."""
+    require_gpu()
+    M, K, I, E, topk = size  # noqa: E741
+    c = make_moe(True, M, K, I, E, topk, "bf16", seed=K + block_size, block_size=block_size, masked=0.1 if M > 1 else 0.0)
+    # scales that differ by far: a block's neighbour in its place would show
+    for name in ("s13", "s2"):
+        c[name] *= 4.0 ** (np.arange(c[name].shape[2]) % 3 - 1).astype(np.float32)
+    want, tol = moe_want(c)
+    assert_within(run(c, path=STREAM[True]), want, tol, "bf16", f"{size} {block_size}")
