@@ -363,3 +363,21 @@ def test_fp8_blocks_of_several_windows(size, block_size):
         c[name] *= 4.0 ** (np.arange(c[name].shape[2]) % 3 - 1).astype(np.float32)
     want, tol = moe_want(c)
     assert_within(run(c, path=STREAM[True]), want, tol, "bf16", f"{size} {block_size}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("fp8", FORMATS, ids=["fp4", "fp8"])
+@pytest.mark.parametrize("size", [(64, 768, 70, 64), (128, 5120, 9, 8), (192, 8192, 7, 6), (64, 1024, 40, 40)], ids=ids_of)
+def test_one_token_whose_choices_do_not_fit_in_lds_together(size, fp8, dtype):
+    """The choices' rows of I pass LDS: a single token takes the kernels for several, a pass for each of its choices."""
+    require_gpu()
+    K, I, E, topk = size  # noqa: E741
+    assert topk * 2 * (-(-I // 128) * 256 + 16) > 160 * 1024
+    c = make_moe(fp8, 1, K, I, E, topk, dtype, seed=I + topk)
+    c["ids"][0, topk // 2] = -1
+    c["ids"][0, -1] = c["ids"][0, 1] = c["ids"][0, 0]
+    want, tol = moe_want(c)
+    assert_within(run(c, path=STREAM[fp8]), want, tol, dtype, f"{size}")
+    c["ids"][0] = E - 1
+    want, tol = moe_want(c)
+    assert_within(run(c, path=STREAM[fp8]), want, tol, dtype, f"{size} one expert")
