@@ -166,3 +166,39 @@ def test_leading_dimensions_stream_and_graph():
         again = call({}, 0.0, use=d)
         assert torch.equal(out[0], again[0]) and torch.equal(out[1], again[1]), k
     assert TORCH["bf16"] == out[0].dtype
+
+
+@pytest.mark.parametrize("K,post,pre", [(65, True, True), (65, False, True), (65, True, False), (65, False, False), (16385, True, True)])
+def test_more_rows_than_workgroups(K, post, pre):
+    """Rows past the 2^20 workgroups of a launch: some take a second row, with the sums of the first behind them."""
+    require_gpu()
+    M = (1 << 20) + 70
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_()
+    some = [slice(0, 70), slice(M - 140, M)]  # the rows that a workgroup takes first and second, and some between
+    c = {"x": (None, None)}
+    w = [rounded(1 + 0.3 * np.random.default_rng(K + i).standard_normal(K), "bf16") for i in range(2)]
+    x64 = np.concatenate([x[s].double().cpu().numpy() for s in some])
+    if post:
+        c["post"] = w[0]
+    if pre:
+        c["pre"] = w[1]
+    d = {k: v[1].cuda() for k, v in c.items() if k != "x"}
+    # in place where the rows are long (34 GB): one output
+    r, y = fw.fp4w_block_norm(x, None, d.get("pre"), d.get("post"), None, 0.5, 1e-5,
+                              **({"out": x, "write_residual": False} if K > 1000 else {}))
+    wr, wy, tr, ty = om.block_norm(x64, None, w[1][0] if pre else None, w[0][0] if post else None, None, 0.5, 1e-5)
+    for got, want, tol in ((r, wr, tr), (y, wy, ty)):
+        if got is not None:
+            assert_within(torch.cat([got[s] for s in some]), want, tol, "bf16", f"K {K}")
+
+
+def test_more_rows_than_waves():
+    """A wave per row: rows past 4 x 2^20."""
+    require_gpu()
+    M = (4 << 20) + 9
+    x = torch.empty(M, 8, dtype=torch.bfloat16, device="cuda").normal_()
+    pre64, pre = rounded(1 + 0.3 * np.random.default_rng(3).standard_normal(8), "bf16")
+    _, y = fw.fp4w_block_norm(x, pre_weight=pre.cuda(), eps=1e-5)
+    for s in (slice(0, 9), slice(M - 20, M)):
+        _, want, _, tol = om.block_norm(x[s].double().cpu().numpy(), None, pre64, eps=1e-5)
+        assert_within(y[s], want, tol, "bf16")

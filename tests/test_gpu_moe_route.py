@@ -182,3 +182,17 @@ def test_masks_by_the_bias_against_the_oracle():
     assert (w[:, :3].cpu().double().sum(1) < 0.9).all()
     assert torch.allclose(w[:, :3].cpu().double(), p.gather(1, ids[:, :3].cpu().long()), rtol=1e-5)
     assert (ids[:, 3:] == -1).all() and (w[:, 3:] == 0).all()
+
+
+@pytest.mark.parametrize("bias", [False, True])
+def test_more_rows_than_waves(bias):
+    """A wave per row: rows past the 4 x 2^20 of a launch are a wave's second."""
+    require_gpu()
+    M, E = (4 << 20) + 13, 3
+    x = torch.empty(M, E, device="cuda").normal_()
+    b = np.array([0.1, -0.2, 0.15], np.float32) if bias else None
+    ids, w = fw.fp4w_moe_route(x, 2, "sigmoid", None if b is None else torch.from_numpy(b).cuda())
+    for s in (slice(0, 13), slice(M - 40, M)):
+        want_ids, want_w, rel = om.route(x[s].double().cpu().numpy(), 2, "sigmoid", b)
+        assert np.array_equal(ids[s].cpu().numpy(), want_ids)
+        assert (np.abs(w[s].cpu().double().numpy() - want_w) <= rel * want_w).all()
