@@ -120,3 +120,36 @@ def test_renormalised_weights_of_small_scores():
     ids, w, _ = om.route(np.array([[0.0, -120, -121, -119], [0, -760, -770, -800]]), 2, "softmax", bias)
     assert ids.tolist() == [[3, 1]] * 2
     assert np.allclose(w[0], [1 / (1 + math.exp(-1)), 1 / (1 + math.e)], rtol=1e-12) and (w[1] == 0).all()
+
+
+@pytest.mark.parametrize("K", [37, 1000, 5120])
+def test_block_norm_bounds_hold_an_fp32_evaluation(K):
+    """r and y computed step by step in FP32 from FP32 inputs stay inside the bounds, sums in two orders."""
+    f = np.float32
+    rng = np.random.default_rng(K)
+    x, res, gate = (rng.standard_normal((4, K)).astype(f) for _ in range(3))
+    pre, post = (rng.standard_normal(K).astype(f) for _ in range(2))
+
+    def norm(v, w, total):
+        inv = f(1) / np.sqrt(total(v * v) * f(1.0 / K) + f(1e-6))
+        return v * (inv * (f(0.5) + w))
+
+    def one_by_one(v):
+        return np.cumsum(v, axis=1, dtype=f)[:, -1:]
+
+    def pairs(v):
+        return v.sum(axis=1, keepdims=True, dtype=f)
+
+    for has_post, has_gate, has_res in itertools.product((False, True), repeat=3):
+        r64, y64, tol_r, tol_y = om.block_norm(
+            x.astype(np.float64), res.astype(np.float64) if has_res else None, pre.astype(np.float64),
+            post.astype(np.float64) if has_post else None, gate.astype(np.float64) if has_gate else None, 0.22, 1e-6, 0.5)
+        for total in (one_by_one, pairs):
+            b = norm(x, post, total) if has_post else x
+            t = (f(0.22) * gate if has_gate else f(0.22)) * b
+            r = res + t if has_res else t
+            y = norm(r, pre, total)
+            assert r.dtype == f and y.dtype == f
+            assert (np.abs(r - r64) <= tol_r).all() and (np.abs(y - y64) <= tol_y).all()
+        # and they are no wider than FP32 needs
+        assert (tol_r <= 2e-3 * (np.abs(r64) + np.abs(x) + 1)).all() and (tol_y <= 4e-3 * (np.abs(y64) + 1)).all()
