@@ -15,7 +15,13 @@
 // hold it), and a sum is a wave reduction, one LDS exchange and one barrier.
 // Every value of a row is read before any is written, so the outputs may take
 // the place of x and residual.  Rows that the registers of a workgroup do not
-// hold take a kernel that reads the row once per sum and once for the result.
+// hold take a kernel that reads the row once per sum and once for the result:
+// those of more than 32768 values, and of more than 4096 where rows are not
+// whole aligned chunks of 8.  With 16 single values a thread (of 1024, so 128
+// registers) the compiler keeps 624 bytes a lane in scratch: 4096 rows of 8193
+// took 852 us that way and take 229 so, one row 30 and 12.  Four chunks a thread,
+// 16385 to 32768 values, spill too (152 bytes a lane), but 1024 rows of 24576 take
+// 75 us, and 181 in the other kernel; one row 11 and 28.
 // Measured: 8192 rows of 5120 with a residual and a norm before the next block
 // (336 MB) take 64.5 us, 5.2 TB/s, above the 4.8 that a large copy reaches.
 // 77 rows of 2049 with both norms and a full gate take 5.6 us, one row of 5120
@@ -245,8 +251,6 @@ void launch_t(const NormParams& p, hipStream_t s) {
     launch_rows<T, VEC, 2>(p, chunks, s);
   } else if (chunks <= 4096) {
     launch_rows<T, VEC, 4>(p, chunks, s);
-  } else if (VEC == 1 && chunks <= 16384) {
-    launch_rows<T, 1, 16>(p, chunks, s);
   } else {
     const int grid = static_cast<int>(p.M < kMaxGrid ? p.M : kMaxGrid);
     hipLaunchKernelGGL(block_norm_long_kernel<T>, dim3(grid), dim3(1024), 0, s, p);

@@ -202,3 +202,22 @@ def test_more_rows_than_waves():
     for s in (slice(0, 9), slice(M - 20, M)):
         _, want, _, tol = om.block_norm(x[s].double().cpu().numpy(), None, pre64, eps=1e-5)
         assert_within(y[s], want, tol, "bf16")
+
+
+@pytest.mark.parametrize("K,off", [(4095, 0), (4096, 1), (4097, 0), (8193, 0), (16384, 3), (16384, 0), (16392, 0), (32768, 0), (32776, 0)])
+def test_rows_at_the_borders_of_the_forms(K, off):
+    """Lengths where another form of the kernel begins, aligned and off 16 bytes, apart and in place."""
+    require_gpu()
+    c = make(3, K, True, True, 3, True, 0.0, "bf16", K)
+
+    def placed(t):
+        room = torch.empty(t.numel() + off, dtype=t.dtype, device="cuda")
+        return room[off:].view(t.shape).copy_(t)
+
+    x, res = placed(c["x"][1]), placed(c["residual"][1])
+    wr, wy, tr, ty = want(c, 0.0)
+    r, y = call(c, 0.0, use={"x": x, "residual": res})
+    assert_within(r, wr, tr, "bf16", "residual_out")
+    assert_within(y, wy, ty, "bf16", "y")
+    call(c, 0.0, use={"x": x, "residual": res}, residual_out=res, out=x)
+    assert torch.equal(res, r) and torch.equal(x, y)
