@@ -43,22 +43,26 @@
 //  * FP8: E4M3 -> T is exact, a 128-k window (inside one scale block) is summed
 //    in a fresh accumulator and added times its FP32 scale.
 //
-// Measured (us of a layer, GPU time; in brackets the bytes of the experts named
-// at the 4.8 TB/s of a large copy): FP4, 1 token on 8 of 128 experts of 2048 x
-// 768: 13.5 (4.4); 4 tokens on 7168 x 2048: 136 (137); 32 on 2048 x 768: 67
-// (62); 128 on 32 experts of 2880 x 2880: 178 (93).  FP8, 1 token on 6 experts
-// of 2048 x 1408: 17.4 (11); 16 on 4096 x 1024: 175 (223); 100 on a quarter of
-// 64 experts of 5120 x 1280: 95.5 (68).  About 7 us of each of the two kernels
-// are launch, plan, token rows and first weights, 5 to 8 the combination; one
-// token saves the plan and the third launch.  Beyond some ten tokens an expert
-// the arithmetic takes longer than the bytes: with 16 each, of FP4 experts,
-// the first kernel takes 108 of its 118 us when the weights cost nothing, and
-// 97 when they are loaded but not multiplied.
+// Measured (us of a layer, GPU time; in brackets the bytes of the experts that
+// the ids name, about, at the 4.8 TB/s of a large copy): FP4, 1 token on 8 of 128
+// experts of 2048 x 768: 13.5 (4.4); 4 tokens on 24 of 64, 7168 x 2048: 134 (124);
+// 32 on 89 of 128, 2048 x 768: 67 (49); 128 on 32 experts of 2880 x 2880: 178 (92).
+// FP8, 1 token on 6 experts of 2048 x 1408: 17.4 (11); 16 on 67 of 128, 4096 x
+// 1024: 175 (180); 100 on 15 of 16 held, 5120 x 1280: 95.5 (64).  About 7 us of
+// each of the two kernels are launch, plan, token rows and first weights, 5 to 8
+// the combination; one token saves the plan and the third launch.  Beyond some
+// ten tokens an expert the arithmetic takes longer than the bytes: with 16 each,
+// of FP4 experts, the first kernel takes 108 of its 118 us when the weights cost
+// nothing, and 97 when they are loaded but not multiplied.
 //
 // H is handed from up to down as two BF16 planes, high part and remainder (16
 // significand bits, FP32's exponent range): one BF16 or FP16 rounding of H
 // would double the output's error, and in FP16 gate * up may overflow.  The
-// down kernel runs both planes through the same decoded weights.
+// down kernel runs both planes through the same decoded weights.  Against 64
+// bits the layer's error is then that of its last rounding (128 tokens, BF16:
+// 1.663016e-3 of the norm, 1.663014e-3 with FP32 throughout or exactly); 2 to 3
+// of 1000 BF16 outputs lie beyond a rounding boundary, 1 to 3 with FP32
+// throughout.  A third plane would cost half as many products and LDS again.
 
 #include <hip/hip_runtime.h>
 
@@ -1135,7 +1139,8 @@ size_t rows_lds_bytes(int64_t rows, int planes, int windows) {
 // with that of down at 2 and 4: FP8 I = 1024, 8 units: 178.2, 181.9; FP8 I =
 // 1280, 10 units: 99.1, 116.4.  So: the largest split that leaves a wave four
 // units of a tile, and beyond that only as far as the workgroups would not
-// fill the chip.
+// fill the chip.  It is not the best of every row: FP4 K = 2880 gets 2 (1 is 1.1 %
+// faster), FP8 K = 4096 gets 8 (4 is 1.4 %), FP4 K = 7168 gets 4 (8 is 1.1 %).
 int k_split(int NU, int64_t tiles, int64_t passes, int64_t cus) {
   int ks = 1;
   while (ks < kWaves && NU >= 8 * ks) ks *= 2;

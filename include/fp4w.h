@@ -336,7 +336,8 @@ int fp8w_matmul_w8a8(const void* A, int64_t M, int64_t K, const uint8_t* B, int6
  *   r = residual + scale * gate * b                             (residual_out)
  *   y = r * rsqrt(mean(r^2) + eps) * (weight_offset + pre_weight)
  * Means are over a row's K values.  Everything is FP32; residual_out and y
- * are each rounded once, y from the unrounded r.
+ * are each rounded once, y from the unrounded r.  (So a row whose sum of
+ * squares passes FP32's range, with values of some 1e19, is normed to 0.)
  *
  *   x             T[M, K]: a block's output (or, alone, an embedding).
  *   post_weight   T[K] or NULL: no norm of x.
