@@ -37,6 +37,12 @@ The functions carry the C ABI's names (include/fp4w.h):
   ``fp4w_moe_route(logits, topk)``: its ids and weights from router logits;
   ``fp4w_block_norm(x, residual, pre_weight, ...)``: the norms after one block
   and before the next, with gate and residual scale.
+* ``fp4w_qk_norm_rope(q, k, ...)``: norms of query and key heads with the
+  rotation by position; ``fp8w_kv_append(k, v, cache, ...)``: new keys and
+  values (normed and rotated on the way) into a paged cache of E4M3 codes with
+  a power of two for each page and head (``fp8w_kv_cache`` makes one);
+  ``fp8w_attention(q, cache, ...)``: attention over it, for decoded tokens and
+  prompts.
 
 A keeps any leading dimensions; Y has A's leading dimensions, last dimension
 N and A's dtype.
@@ -44,6 +50,7 @@ N and A's dtype.
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -62,6 +69,7 @@ PATH_FP4_SKINNY, PATH_FP8_SKINNY = 12, 13
 PATH_FP8_DEQUANT_VEC, PATH_FP8_DEQUANT_GENERIC = 14, 15
 PATH_NVFP4_VEC, PATH_NVFP4_GENERIC = 16, 17
 PATH_MOE_FP4_STREAM, PATH_MOE_FP4_GENERIC, PATH_MOE_FP8_STREAM, PATH_MOE_FP8_GENERIC = 18, 19, 20, 21
+PATH_ATTN_DECODE, PATH_ATTN_PROMPT, PATH_ATTN_GENERIC = 22, 23, 24
 # operations (fp4w_op)
 OP_FP4_MATMUL, OP_FP8_MATMUL, OP_FP4_DEQUANT, OP_FP8_QDQ, OP_FP8_DEQUANT, OP_NVFP4_ACT = 0, 1, 2, 3, 4, 5
 # dtypes (fp4w_dtype)
@@ -70,6 +78,7 @@ F16, BF16, F32 = 0, 1, 2
 SCORES = {"softmax": 0, "sigmoid": 1}
 ACTIVATIONS = {"silu": 0, "gelu": 1}
 MOE_MAX_EXPERTS, MOE_MAX_TOPK = 1024, 64
+MAX_HEAD_SIZE = 1024  # FP8W_MAX_HEAD_SIZE
 
 EXPORTED = (
     "fp4w_matmul", "fp4w_matmul_ex", "fp8w_matmul", "fp8w_matmul_ex", "fp4w_dequant",
@@ -77,6 +86,7 @@ EXPORTED = (
     "fp4w_quantize_activation", "fp4w_quantize_activation_ex", "fp4w_qdq_activation", "fp4w_qdq_activation_ex",
     "fp4w_matmul_w4a4", "fp4w_matmul_w4a4_noalloc",
     "fp4w_block_norm", "fp4w_moe_route", "fp4w_moe_workspace", "fp4w_moe", "fp4w_moe_ex", "fp8w_moe", "fp8w_moe_ex",
+    "fp4w_qk_norm_rope", "fp8w_kv_append", "fp8w_attention", "fp8w_attention_ex", "fp8w_attention_workspace",
     "fp4w_select_path", "fp4w_status_string", "fp4w_path_name",
 )
 
@@ -146,6 +156,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     moe = [vp, i64, i64, vp, vp, i64, vp, vp, vp, vp, i64, i64, i64, i32, vp, i64, vp, i32, vp]
     lib.fp8w_moe.argtypes, lib.fp8w_moe.restype = moe, i32
     lib.fp8w_moe_ex.argtypes, lib.fp8w_moe_ex.restype = moe + [i32], i32
+    rope = [vp, vp, f32, f32, vp, vp, i64, i64, i32, vp]
+    cache = [vp, vp, vp, vp, i64, i64]
+    lib.fp4w_qk_norm_rope.argtypes = [vp, i64, i64, vp, i64, i64, i64, i64, *rope, vp, i64, vp, i64, i32, vp]
+    lib.fp4w_qk_norm_rope.restype = i32
+    lib.fp8w_kv_append.argtypes = [vp, i64, vp, i64, i64, i64, i64, vp, i64, i64, *rope, vp, i64, vp, i64, vp, vp, i64,
+                                   *cache, i32, vp]
+    lib.fp8w_kv_append.restype = i32
+    lib.fp8w_attention_workspace.argtypes = [i64] * 6
+    lib.fp8w_attention_workspace.restype = i64
+    attn = [vp, i64, i64, i64, i64, i64, vp, i64, vp, vp, i64, i64, *cache, f32, i32, i64, vp, i64, vp, vp, i32, vp]
+    lib.fp8w_attention.argtypes, lib.fp8w_attention.restype = attn, i32
+    lib.fp8w_attention_ex.argtypes, lib.fp8w_attention_ex.restype = attn + [i32], i32
     lib.fp4w_select_path.argtypes = [i32, i64, i64, i64, i64, i64]
     lib.fp4w_select_path.restype = i32
     lib.fp4w_status_string.argtypes = [i32]
@@ -708,3 +730,241 @@ def fp8w_moe(A: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, w13: tor
     float32 scales per ``block_size`` values of a row."""
     return _moe(True, A, ids, weights, w13, w13_scale, None, w2, w2_scale, None, block_size, activation, out,
                 workspace, path)
+
+
+# ---------------------------------------------------------------- between the projections of an attention block
+
+class KVCache(NamedTuple):
+    """A paged cache of keys and values: E4M3 codes ``k`` [pages, heads,
+    page_size, D] and ``v`` [pages, heads, D, page_size] (uint8 or
+    float8_e4m3fn), and a power of two for each page and head, ``k_scale`` and
+    ``v_scale`` [pages, heads] (uint8 or float8_e8m0fnu: 2^(byte - 127))."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def fp8w_kv_cache(num_pages: int, heads: int, page_size: int, head_size: int, device="cuda") -> KVCache:
+    """An empty cache (0.5 KB a token for 2 heads of 128): pages are filled by fp8w_kv_append."""
+    codes = torch.zeros(2, num_pages * heads * page_size * head_size, dtype=torch.uint8, device=device)
+    scale = torch.full((2, num_pages, heads), 127, dtype=torch.uint8, device=device)
+    return KVCache(codes[0].view(num_pages, heads, page_size, head_size),
+                   codes[1].view(num_pages, heads, head_size, page_size), scale[0], scale[1])
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_POWERS = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _cache(cache: KVCache, heads: int, D: int, device: torch.device):
+    """(pages, page_size) of a cache that fits; raises otherwise."""
+    k, v, ks, vs = cache
+    shape = k.shape
+    if len(shape) != 4 or shape[1] != heads or shape[3] != D or v.shape != (shape[0], heads, D, shape[2]):
+        raise ValueError(f"the cache must hold k [pages, {heads}, page_size, {D}] and v [pages, {heads}, {D}, page_size], "
+                         f"got {tuple(shape)} and {tuple(v.shape)}")
+    if ks.shape != shape[:2] or vs.shape != shape[:2]:
+        raise ValueError(f"the cache's scales must be [{shape[0]}, {heads}], got {tuple(ks.shape)} and {tuple(vs.shape)}")
+    for t, name, types in ((k, "k", _CODES), (v, "v", _CODES), (ks, "k_scale", _POWERS), (vs, "v_scale", _POWERS)):
+        if t.dtype not in types:
+            raise TypeError(f"the cache's {name} must be one of {types}, got {t.dtype}")
+        if not t.is_contiguous() or t.device != device:
+            _need(t, f"the cache's {name}", device)
+    return shape[0], shape[2]
+
+
+def _heads(t: torch.Tensor, name: str, M: int, D: int, dtype: torch.dtype, device: torch.device):
+    """(heads, token stride) of t [M, heads, D], whose tokens may be apart."""
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != M or shape[2] != D or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype} [{M}, heads, {D}], got {t.dtype} {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    H = shape[1]
+    if t.is_contiguous():
+        return H, H * D
+    stride = t.stride()
+    if (stride[2] != 1 and D > 1) or (stride[1] != D and H > 1):
+        raise ValueError(f"{name}'s heads must lie side by side, got strides {stride}")
+    return H, (stride[0] if M > 1 else H * D)
+
+
+def _rope_args(dtype, device, M, D, q_weight, k_weight, weight_offset, eps, cos, sin, interleaved, positions):
+    if q_weight is not None:
+        _typed(q_weight, "q_weight", dtype, (D,), device)
+    if k_weight is not None:
+        _typed(k_weight, "k_weight", dtype, (D,), device)
+    rows = dims = 0
+    if cos is not None or sin is not None:
+        if cos is None or sin is None or cos.dim() != 2 or not cos.numel():  # (no pointer to an empty table)
+            raise ValueError("cos and sin go together, each [positions, rotated values / 2] and not empty")
+        rows, dims = cos.shape[0], 2 * cos.shape[1]
+        if dims > D:
+            raise ValueError(f"cos has {dims // 2} angles, heads of {D} have at most {D // 2}")
+        _typed(cos, "cos", torch.float32, cos.shape, device)
+        _typed(sin, "sin", torch.float32, cos.shape, device)
+    if positions is not None:
+        _typed(positions, "positions", torch.int32, (M,), device)
+    return (_data(q_weight), _data(k_weight), weight_offset, eps, _data(cos), _data(sin), rows, dims, int(interleaved),
+            _data(positions))
+
+
+def fp4w_qk_norm_rope(q: torch.Tensor, k: torch.Tensor = None, q_weight: torch.Tensor = None,
+                      k_weight: torch.Tensor = None, cos: torch.Tensor = None, sin: torch.Tensor = None,
+                      positions: torch.Tensor = None, interleaved: bool = False, weight_offset: float = 0.0,
+                      eps: float = 1e-6, q_out: torch.Tensor = None, k_out: torch.Tensor = None):
+    """(q_out, k_out): the heads of q [M, Hq, D] and k [M, Hk, D] (or None)
+    normed, x * rsqrt(mean(x^2) + eps) * (weight_offset + weight), where their
+    weight is given, and rotated by the angles of ``cos`` and ``sin`` (float32
+    [positions, R / 2]) at ``positions`` (int32 [M]; None: 0, 1, ...): pairs
+    (i, i + R / 2) of the first R values, or (2 i, 2 i + 1) if ``interleaved``.
+    Tokens may be apart (views into a projection's output), and ``q_out`` and
+    ``k_out`` may be q and k."""
+    lib = load_library()
+    if q.dim() != 3:
+        raise ValueError(f"q must be [M, heads, D], got {tuple(q.shape)}")
+    dtype, dev, (M, _, D) = q.dtype, q.device, q.shape
+    code = _dtype_code(dtype)
+    Hq, q_stride = _heads(q, "q", M, D, dtype, dev)
+    if q_out is None:
+        q_out = torch.empty((M, Hq, D), dtype=dtype, device=dev)
+    n, qo_stride = _heads(q_out, "q_out", M, D, dtype, dev)
+    Hk = k_stride = ko_stride = 0
+    if k is not None:
+        Hk, k_stride = _heads(k, "k", M, D, dtype, dev)
+        if k_out is None:
+            k_out = torch.empty((M, Hk, D), dtype=dtype, device=dev)
+        nk, ko_stride = _heads(k_out, "k_out", M, D, dtype, dev)
+    else:
+        if k_out is not None or k_weight is not None:
+            raise ValueError("k_out and k_weight need a k")
+        nk = 0
+    if n != Hq or nk != Hk:
+        raise ValueError("q_out and k_out must have the shapes of q and k")
+    rope = _rope_args(dtype, dev, M, D, q_weight, k_weight, weight_offset, eps, cos, sin, interleaved, positions)
+    _call(dev, lib.fp4w_qk_norm_rope, "fp4w_qk_norm_rope", q.data_ptr(), q_stride, Hq, _data(k), k_stride, Hk, M, D, *rope,
+          q_out.data_ptr(), qo_stride, _data(k_out), ko_stride, code)
+    return q_out, k_out
+
+
+def _sequences(page_table, seq_lens, starts, M, device):
+    """(B, max_pages) of a batch that fits; raises otherwise."""
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be int32 [B, pages of a sequence], got {tuple(page_table.shape)}")
+    B, pages = page_table.shape
+    _typed(page_table, "page_table", torch.int32, (B, pages), device)
+    _typed(seq_lens, "seq_lens", torch.int32, (B,), device)
+    if starts is not None:
+        _typed(starts, "starts", torch.int32, (B + 1,), device)
+    elif B != M:
+        raise ValueError(f"without starts there is one new token for each sequence, got {M} for {B}")
+    return B, pages
+
+
+def fp8w_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                   starts: torch.Tensor = None, q: torch.Tensor = None, q_weight: torch.Tensor = None,
+                   k_weight: torch.Tensor = None, cos: torch.Tensor = None, sin: torch.Tensor = None,
+                   positions: torch.Tensor = None, interleaved: bool = False, weight_offset: float = 0.0,
+                   eps: float = 1e-6, q_out: torch.Tensor = None):
+    """Writes new keys and values [M, Hk, D] into the pages of their sequences,
+    the keys normed and rotated on the way as by fp4w_qk_norm_rope; returns
+    ``q`` [M, Hq, D] normed and rotated (``q_out``), or None without a q.
+
+    Sequence b's new tokens are rows starts[b] .. starts[b + 1] - 1 (int32
+    [B + 1]; None: one row each); ``seq_lens`` (int32 [B]) counts its tokens with
+    them, and ``page_table`` (int32 [B, pages]) names its pages.  The rotation
+    takes ``positions`` (int32 [M]), or a token's place in its sequence.  No page
+    may be named twice in one call (full pages that are only read later may)."""
+    lib = load_library()
+    if k.dim() != 3:
+        raise ValueError(f"k must be [M, heads, D], got {tuple(k.shape)}")
+    dtype, dev, (M, _, D) = k.dtype, k.device, k.shape
+    code = _dtype_code(dtype)
+    Hk, k_stride = _heads(k, "k", M, D, dtype, dev)
+    nv, v_stride = _heads(v, "v", M, D, dtype, dev)
+    if nv != Hk:
+        raise ValueError(f"v must have k's {Hk} heads, got {nv}")
+    pages, page = _cache(cache, Hk, D, dev)
+    B, max_pages = _sequences(page_table, seq_lens, starts, M, dev)
+    Hq = q_stride = qo_stride = 0
+    if q is not None:
+        Hq, q_stride = _heads(q, "q", M, D, dtype, dev)
+        if q_out is None:
+            q_out = torch.empty((M, Hq, D), dtype=dtype, device=dev)
+        nq, qo_stride = _heads(q_out, "q_out", M, D, dtype, dev)
+        if nq != Hq:
+            raise ValueError("q_out must have q's shape")
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need a q")
+    rope = _rope_args(dtype, dev, M, D, q_weight, k_weight, weight_offset, eps, cos, sin, interleaved, positions)
+    _call(dev, lib.fp8w_kv_append, "fp8w_kv_append", k.data_ptr(), k_stride, v.data_ptr(), v_stride, M, Hk, D, _data(q),
+          q_stride, Hq, *rope, _data(q_out), qo_stride, _data(starts), B, seq_lens.data_ptr(), page_table.data_ptr(),
+          max_pages, cache.k.data_ptr(), cache.k_scale.data_ptr(), cache.v.data_ptr(), cache.v_scale.data_ptr(), pages,
+          page, code)
+    return q_out
+
+
+def fp8w_attention_workspace(M: int, Hq: int, Hk: int, D: int, B: int, max_new: int) -> int:
+    """Bytes of workspace that fp8w_attention needs, however long the sequences are; enough for every smaller call too."""
+    n = int(load_library().fp8w_attention_workspace(M, Hq, Hk, D, B, max_new))
+    if n < 0:
+        raise FP4WError(n, "fp8w_attention_workspace")
+    return n
+
+
+def fp8w_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                   starts: torch.Tensor = None, max_new: int = None, scale: float = None, causal: bool = True,
+                   window: int = 0, out: torch.Tensor = None, lse: torch.Tensor = None, workspace: torch.Tensor = None,
+                   path: int = PATH_AUTO) -> torch.Tensor:
+    """Attention of the new tokens' q [M, Hq, D] over the cache, which holds
+    them already (fp8w_kv_append); [M, Hq, D].
+
+    Rows and sequences as in fp8w_kv_append.  A token attends the tokens of its
+    sequence up to its own position (all that are held if not ``causal``), of
+    those the last ``window`` if it is not 0; one that attends none gets zeros.
+    ``scale`` is D^-0.5 if None.  ``max_new`` (None: M, or 1 without ``starts``)
+    is at least every sequence's number of new tokens, and chooses the kernel:
+    rows behind it are left as they were.  ``lse`` (float32 [M, Hq]), where given,
+    gets the logarithm of each row's sum of exponentials.  ``workspace`` holds
+    ``fp8w_attention_workspace(M, Hq, Hk, D, B, max_new)`` bytes; it is allocated
+    here when not given.  Calls that may run at once need one each."""
+    lib = load_library()
+    if q.dim() != 3:
+        raise ValueError(f"q must be [M, heads, D], got {tuple(q.shape)}")
+    dtype, dev, (M, _, D) = q.dtype, q.device, q.shape
+    code = _dtype_code(dtype)
+    Hq, q_stride = _heads(q, "q", M, D, dtype, dev)
+    Hk = cache.k.shape[1] if cache.k.dim() == 4 else 0
+    pages, page = _cache(cache, Hk, D, dev)
+    B, max_pages = _sequences(page_table, seq_lens, starts, M, dev)
+    if max_new is None or max_new > M:
+        max_new = M
+    if starts is None:
+        max_new = 1
+    if window < 0 or max_new < 0:
+        raise ValueError("window and max_new must not be negative")
+    if out is None:
+        out = torch.empty((M, Hq, D), dtype=dtype, device=dev)
+    else:
+        _typed(out, "out", dtype, (M, Hq, D), dev)
+    if lse is not None:
+        _typed(lse, "lse", torch.float32, (M, Hq), dev)
+    if workspace is None:
+        held = lib.fp8w_attention_workspace(M, Hq, Hk, D, B, max_new)
+        if held < 0:
+            raise FP4WError(held, "fp8w_attention")
+        if held:
+            workspace = torch.empty(held, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", dev)
+        held = workspace.numel() * workspace.element_size()
+    args = (q.data_ptr(), q_stride, M, Hq, Hk, D, _data(starts), B, seq_lens.data_ptr(), page_table.data_ptr(), max_pages,
+            max_new, cache.k.data_ptr(), cache.k_scale.data_ptr(), cache.v.data_ptr(), cache.v_scale.data_ptr(), pages, page,
+            D ** -0.5 if scale is None and D else scale or 0.0, int(causal), window, _data(workspace), held, out.data_ptr(),
+            _data(lse), code)
+    if path == PATH_AUTO:
+        _call(dev, lib.fp8w_attention, "fp8w_attention", *args)
+    else:
+        _call(dev, lambda *a: lib.fp8w_attention_ex(*a, path), "fp8w_attention", *args)
+    return out

@@ -563,6 +563,9 @@ const char* fp4w_path_name(int path) {
     case FP4W_PATH_MOE_FP4_GENERIC: return "moe_fp4_generic";
     case FP4W_PATH_MOE_FP8_STREAM: return "moe_fp8_stream";
     case FP4W_PATH_MOE_FP8_GENERIC: return "moe_fp8_generic";
+    case FP4W_PATH_ATTN_DECODE: return "attn_decode";
+    case FP4W_PATH_ATTN_PROMPT: return "attn_prompt";
+    case FP4W_PATH_ATTN_GENERIC: return "attn_generic";
     default: return "unknown";
   }
 }

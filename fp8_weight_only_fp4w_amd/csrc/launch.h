@@ -8,6 +8,8 @@
 
 namespace fp4w {
 
+constexpr int kMaxHead = 1024;  // FP8W_MAX_HEAD_SIZE of the public header
+
 enum class Act : int { F16 = 0, BF16 = 1 };
 
 // Arguments of one matmul call after validation.  `scales` is uint8 E4M3
@@ -113,6 +115,76 @@ struct MoeArgs {
   void* Y;
   int64_t M, K, topk, E, I, block_size;
   int activation;
+  Act act;
+  void* stream;
+};
+
+// Norm and rotation of heads (fp4w_qk_norm_rope, and on the way in
+// fp8w_kv_append).  Strides in values of T.  cos / sin null: no rotation.
+struct RopeArgs {
+  const void* q_weight;
+  const void* k_weight;
+  const float* cos;
+  const float* sin;
+  const int32_t* positions;
+  int64_t rows, dims;
+  bool interleaved;
+  float weight_offset, eps;
+};
+
+// Which rows of a call belong to which sequence, and where its tokens are.
+// starts null: row b is sequence b's only new token.
+struct SeqArgs {
+  const int32_t* starts;
+  const int32_t* lens;
+  const int32_t* table;
+  int64_t B, max_pages, num_pages, page_size;
+};
+
+struct QkNormRopeArgs {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride, M, Hq, Hk, D;
+  RopeArgs rope;
+  Act act;
+  void* stream;
+};
+
+// q null or Hq 0: keys and values only.
+struct KvAppendArgs {
+  const void* k;
+  const void* v;
+  const void* q;
+  void* q_out;
+  int64_t k_stride, v_stride, q_stride, q_out_stride, M, Hk, Hq, D;
+  RopeArgs rope;
+  SeqArgs seq;
+  uint8_t* k_cache;
+  uint8_t* k_scale;
+  uint8_t* v_cache;
+  uint8_t* v_scale;
+  Act act;
+  void* stream;
+};
+
+// Attention over the cache.  window 0: none.  `work` holds
+// fp8w_attention_workspace() bytes.
+struct AttentionArgs {
+  const void* q;
+  int64_t q_stride, M, Hq, Hk, D, max_new;
+  SeqArgs seq;
+  const uint8_t* k_cache;
+  const uint8_t* k_scale;
+  const uint8_t* v_cache;
+  const uint8_t* v_scale;
+  float scale;
+  bool causal;
+  int64_t window;
+  void* work;
+  void* Y;
+  float* lse;
   Act act;
   void* stream;
 };
@@ -224,5 +296,18 @@ int launch_moe_fp8(const MoeArgs& a);
 // any validated arguments with M, K > 0 (E, topk and I may be 0)
 int launch_moe_fp4_generic(const MoeArgs& a);
 int launch_moe_fp8_generic(const MoeArgs& a);
+
+// M, D > 0, Hq + Hk > 0.  seq not null: positions (where rope.positions is
+// null) from the sequences, and rows of none left alone.  vec: every pointer (but positions) 16-byte aligned,
+// strides multiples of 8, D a power of two from 16 to 1024, and rope.dims and
+// D - rope.dims multiples of 16.
+int launch_qk_norm_rope(const QkNormRopeArgs& a, bool vec, const SeqArgs* seq);
+
+// M, B, D > 0.  vec: what launch_qk_norm_rope asks for, page_size % 16 == 0
+// and page_size * D <= 16384, cache codes 16-byte aligned.
+int launch_kv_append(const KvAppendArgs& a, bool vec);
+
+// any validated arguments with M, B, Hq, D > 0
+int launch_attention_generic(const AttentionArgs& a);
 
 }  // namespace fp4w

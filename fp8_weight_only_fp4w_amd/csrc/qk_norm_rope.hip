@@ -1,0 +1,96 @@
+// Norms of query and key heads with the rotation by position, in one pass:
+//
+//   n[d] = x[d]                                               without a weight
+//        = x[d] * rsqrt(mean(x^2) + eps) * (offset + w[d])    with one
+//   (n[i], n[j]) -> (n[i] c - n[j] s, n[j] c + n[i] s)        for the pairs of the first `dims` values
+//
+// in FP32, rounded once.
+
+#include <hip/hip_runtime.h>
+
+#include "heads.h"
+
+namespace fp4w {
+namespace {
+
+struct QkParams {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride, M;
+  int32_t Hq, Hk, D;
+  const void* q_weight;
+  const void* k_weight;
+  Rope rope;
+  Seqs seq;        // seq.lens not null: positions from the sequences
+};
+
+// Position of row m, and whether the row is to be written.
+__device__ __forceinline__ bool row_position(const QkParams& p, int64_t m, int64_t* position) {
+  if (p.seq.lens != nullptr) {
+    if (m >= seq_start(p.seq, p.seq.B)) return false;
+    const int b = last_not_above(p.seq.B, m, [&](int i) { return seq_start(p.seq, i); });
+    const SeqSpan s = seq_span(p.seq, b);
+    *position = static_cast<int64_t>(s.len) - s.rows + (m - s.first_row);
+  } else {
+    *position = m;
+  }
+  if (p.rope.positions) *position = p.rope.positions[m];
+  return true;
+}
+
+// Any D, alignment and stride: a wave per head, values through LDS.
+template <typename T>
+__global__ __launch_bounds__(256) void qk_norm_rope_generic_kernel(const QkParams p) {
+  __shared__ float buf[4][kMaxHead];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, heads = p.Hq + p.Hk;
+  const int64_t units = p.M * heads;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * 4; base < units; base += static_cast<int64_t>(gridDim.x) * 4) {
+    const int64_t u = base + wave;
+    const T* x = nullptr;
+    T* y = nullptr;
+    const T* w = nullptr;
+    int64_t position = 0;
+    if (u < units) {
+      const int64_t m = u / heads;
+      const int h = static_cast<int>(u - m * heads);
+      if (row_position(p, m, &position)) {
+        if (h < p.Hq) {
+          x = static_cast<const T*>(p.q) + m * p.q_stride + static_cast<int64_t>(h) * p.D;
+          y = static_cast<T*>(p.q_out) + m * p.q_out_stride + static_cast<int64_t>(h) * p.D;
+          w = static_cast<const T*>(p.q_weight);
+        } else {
+          x = static_cast<const T*>(p.k) + m * p.k_stride + static_cast<int64_t>(h - p.Hq) * p.D;
+          y = static_cast<T*>(p.k_out) + m * p.k_out_stride + static_cast<int64_t>(h - p.Hq) * p.D;
+          w = static_cast<const T*>(p.k_weight);
+        }
+      }
+    }
+    head_to_lds(x, p.D, w, p.rope, position, buf[wave]);
+    if (x)
+      for (int d = lane; d < p.D; d += 64) y[d] = round_to<T>(buf[wave][d]);
+    __syncthreads();
+  }
+}
+
+template <typename T>
+int launch_t(const QkParams& p, bool vec, hipStream_t s) {
+  const int64_t blocks = (p.M * (p.Hq + p.Hk) + 3) / 4;
+  const int grid = static_cast<int>(blocks < (1 << 20) ? blocks : 1 << 20);
+  hipLaunchKernelGGL(qk_norm_rope_generic_kernel<T>, dim3(grid), dim3(256), 0, s, p);
+  return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+int launch_qk_norm_rope(const QkNormRopeArgs& a, bool vec, const SeqArgs* seq) {
+  QkParams p{a.q, a.k, a.q_out, a.k_out, a.q_stride, a.k_stride, a.q_out_stride, a.k_out_stride, a.M,
+             static_cast<int32_t>(a.Hq), static_cast<int32_t>(a.Hk), static_cast<int32_t>(a.D),
+             a.rope.q_weight, a.rope.k_weight, make_rope(a.rope), Seqs{}};
+  if (seq) p.seq = make_seqs(*seq, a.M);
+  hipStream_t s = static_cast<hipStream_t>(a.stream);
+  return a.act == Act::BF16 ? launch_t<__bf16>(p, vec, s) : launch_t<_Float16>(p, vec, s);
+}
+
+}  // namespace fp4w

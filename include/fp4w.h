@@ -82,7 +82,10 @@ typedef enum {
   FP4W_PATH_MOE_FP4_STREAM = 18,  /* K % 64 == 0, I % 64 == 0, block_size 16 */
   FP4W_PATH_MOE_FP4_GENERIC = 19, /* any legal fp4w_moe arguments */
   FP4W_PATH_MOE_FP8_STREAM = 20,  /* K % 64 == 0, I % 64 == 0, block_size % 128 == 0 */
-  FP4W_PATH_MOE_FP8_GENERIC = 21  /* any legal fp8w_moe arguments */
+  FP4W_PATH_MOE_FP8_GENERIC = 21, /* any legal fp8w_moe arguments */
+  FP4W_PATH_ATTN_DECODE = 22,  /* max_new * Hq / Hk <= 64, D 64 or 128, page_size % 16 == 0 */
+  FP4W_PATH_ATTN_PROMPT = 23,  /* D 64 or 128, page_size % 16 == 0 */
+  FP4W_PATH_ATTN_GENERIC = 24  /* any legal fp8w_attention arguments */
 } fp4w_path;
 
 /* Operation selector for fp4w_select_path. */
@@ -470,6 +473,161 @@ int fp8w_moe_ex(const void* A, int64_t M, int64_t K, const int32_t* ids, const f
                 const float* w2_scale, int64_t E, int64_t I, int64_t block_size, int activation,
                 void* workspace, int64_t workspace_bytes, void* Y, int dtype, void* stream,
                 int path);
+
+/* ------------------------------------------------------------------------
+ * Between the projections of an attention block: norms and rotation of the
+ * query and key heads, a paged cache of keys and values in 8 bits, and
+ * attention over it.
+ *
+ * Rows.  q, k and v are [M, heads, D] with the D values of a head and the
+ * heads of a token side by side; the stride from one token to the next is an
+ * argument, in values, at least heads * D (so they may be parts of one
+ * projection's output).
+ *
+ * Rotation.  cos and sin are float[rope_rows, rope_dims / 2], the tables of a
+ * token's position; the first rope_dims (even, at most D) values of a head are
+ * rotated in pairs, (i, i + rope_dims / 2), or (2 i, 2 i + 1) if `interleaved`
+ * is nonzero:   (a, b) -> (a cos - b sin, b cos + a sin).
+ * Both NULL: no rotation.  A position outside [0, rope_rows) makes the token's
+ * rotated heads NaN.
+ *
+ * Cache.  Pages of page_size tokens:
+ *   k_cache  uint8[num_pages, Hk, page_size, D]   E4M3 "fn" codes
+ *   v_cache  uint8[num_pages, Hk, D, page_size]   (the tokens of one value side by side)
+ *   k_scale, v_scale  uint8[num_pages, Hk]        powers of two: 2^(byte - 127),
+ *                                                 NaN for 255 (OCP MX's E8M0)
+ * A stored value is its code times its page's scale for that head.  Powers of
+ * two cost a floating-point code nothing but the end of its range, and make
+ * scaling exact.
+ *
+ * Sequences.  Sequence b holds seq_lens[b] tokens, the new ones of the call
+ * among them; token t of it is in page page_table[b, t / page_size], slot
+ * t % page_size.  Its new tokens are the rows starts[b] .. starts[b + 1] - 1 of
+ * the call, in order, and are the last ones of the sequence.  starts (int32
+ * [B + 1], not falling, from 0 to at most M) may be NULL if M == B: one new
+ * token for each.  Rows from starts[B] on belong to no sequence: what would be
+ * written for them is left as it was.  Tokens at or behind max_pages *
+ * page_size, and those of a page id outside [0, num_pages), are absent: they
+ * are not written, and nobody attends them.
+ * ------------------------------------------------------------------------ */
+
+#define FP8W_MAX_HEAD_SIZE 1024
+
+/*
+ * fp4w_qk_norm_rope - norms of queries and keys for each head, with the
+ * rotation in the same pass:
+ *   n = x                                                       (weight NULL)
+ *     = x * rsqrt(mean(x^2) + eps) * (weight_offset + weight)
+ *   out = n with its first rope_dims values rotated
+ * in FP32, rounded once to T.  The mean is over a head's D values.
+ *
+ *   q  T[M, Hq, D]    k  T[M, Hk, D]   (Hq or Hk may be 0)
+ *   q_weight, k_weight  T[D] or NULL, each for itself.
+ *   positions  int32[M], or NULL: row m is position m.
+ *   q_out, k_out  T, as q and k with strides of their own (written).  An
+ *       output may be its input (with the same stride); any other overlap of
+ *       an output with an input or the other output is FP4W_ERR_ALIAS.
+ * M == 0 or D == 0 or no heads: FP4W_OK, nothing launched.  Errors:
+ * FP4W_ERR_NULL, FP4W_ERR_SHAPE (also D > FP8W_MAX_HEAD_SIZE, an odd or too
+ * large rope_dims, cos without sin), FP4W_ERR_DTYPE, FP4W_ERR_ALIAS,
+ * FP4W_ERR_LAUNCH.
+ */
+int fp4w_qk_norm_rope(const void* q, int64_t q_stride, int64_t Hq, const void* k, int64_t k_stride,
+                      int64_t Hk, int64_t M, int64_t D, const void* q_weight, const void* k_weight,
+                      float weight_offset, float eps, const float* cos, const float* sin,
+                      int64_t rope_rows, int64_t rope_dims, int interleaved,
+                      const int32_t* positions, void* q_out, int64_t q_out_stride, void* k_out,
+                      int64_t k_out_stride, int dtype, void* stream);
+
+/*
+ * fp8w_kv_append - new keys and values into the cache, with the norms and the
+ * rotation on the way (all optional):
+ *   k is normed by k_weight and rotated as above, in FP32 and not rounded
+ *   before it becomes codes; v is taken as it is; q, where given, goes to
+ *   q_out as in fp4w_qk_norm_rope.
+ * Per page and head, for keys and values apart:
+ *   e = the smallest integer >= -126 with |x| <= 448 * 2^e for every finite new
+ *       value x in the page; where the page also holds earlier tokens of the
+ *       sequence, not less than the page's exponent so far
+ *   code = e4m3(x * 2^-e), to nearest, ties to the even code; NaN for an
+ *       infinity or NaN
+ * Where e grew, the earlier tokens' codes become e4m3(code * 2^(old - e)),
+ * which is exact but for values below 2^(e - 6).  Other slots of the page keep
+ * what they hold.
+ *
+ *   k, v   T[M, Hk, D] with strides.   q  T[M, Hq, D] or NULL (then Hq = 0).
+ *   positions  int32[M] for the rotation, or NULL: the token's place in its
+ *          sequence.
+ *   q_out  T (written); may be q with the same stride.
+ * A page may be appended to through one place of the page table only: two
+ * sequences that name one page, or one that names it twice, race on it.
+ * Sequences that share full pages only read them.
+ * M == 0, B == 0 or D == 0: FP4W_OK, nothing launched.  Errors as above, and
+ * FP4W_ERR_SHAPE for a page_size < 1 or max_pages * page_size >= 2^31;
+ * FP4W_ERR_ALIAS if a part of the cache overlaps an input, q_out or another.
+ */
+int fp8w_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t M,
+                   int64_t Hk, int64_t D, const void* q, int64_t q_stride, int64_t Hq,
+                   const void* q_weight, const void* k_weight, float weight_offset, float eps,
+                   const float* cos, const float* sin, int64_t rope_rows, int64_t rope_dims,
+                   int interleaved, const int32_t* positions, void* q_out, int64_t q_out_stride,
+                   const int32_t* starts, int64_t B, const int32_t* seq_lens,
+                   const int32_t* page_table, int64_t max_pages, uint8_t* k_cache,
+                   uint8_t* k_scale, uint8_t* v_cache, uint8_t* v_scale, int64_t num_pages,
+                   int64_t page_size, int dtype, void* stream);
+
+/*
+ * Bytes of caller-owned workspace that fp8w_attention needs for these sizes,
+ * or a negative fp4w_status for illegal ones.  It does not depend on how long
+ * the sequences are, and does not fall when a size grows.  Host-only.
+ */
+int64_t fp8w_attention_workspace(int64_t M, int64_t Hq, int64_t Hk, int64_t D, int64_t B,
+                                 int64_t max_new);
+
+/*
+ * fp8w_attention - attention of the new tokens over the cache.  For row m, at
+ * position p = seq_lens[b] - (starts[b + 1] - starts[b]) + (m - starts[b]) of
+ * its sequence, and query head h, which reads the key and value head
+ * h / (Hq / Hk):
+ *   s_t = scale * sum_d q[m, h, d] * K_t[d]
+ *   Y[m, h] = sum_t exp(s_t) V_t / sum_t exp(s_t)
+ *   lse[m, h] = log sum_t exp(s_t)
+ * over the tokens t of the sequence that are held (t < seq_lens[b], their page
+ * present), with t <= p if `causal` is nonzero and t > p - window if window >
+ * 0.  Without any, Y is 0 and lse -inf.  What slots of other tokens hold, NaN
+ * among it, does not show.  Scores, softmax and sums are FP32; the softmax's
+ * numerators are rounded to T for their product with V; Y is rounded once.  The result for a
+ * row does not depend on the order in which the GPU works, but its last bits
+ * may on the rest of the batch (where its sum is cut).  With FP16, stored
+ * values are taken up to 2^16 (whatever was appended from FP16 is in range).
+ *
+ *   q        T[M, Hq, D] with a stride.   Hq is a multiple of Hk.
+ *   max_new  no sequence has more new tokens (rows behind it are left as they
+ *            were); it chooses the kernel.  1 if starts is NULL.
+ *   workspace  at least fp8w_attention_workspace(...) bytes, 16-byte aligned;
+ *            what it holds before does not matter.  Calls that may run at once
+ *            (two streams, two replayed graphs) need one each.
+ *   Y        T[M, Hq, D] (written), contiguous.   lse  float[M, Hq] (written) or NULL.
+ * M == 0, B == 0, Hq == 0 or D == 0: FP4W_OK, nothing launched.  Errors:
+ * FP4W_ERR_NULL, FP4W_ERR_SHAPE (also a workspace that is too small or
+ * unaligned), FP4W_ERR_DTYPE, FP4W_ERR_ALIAS, FP4W_ERR_LAUNCH.
+ */
+int fp8w_attention(const void* q, int64_t q_stride, int64_t M, int64_t Hq, int64_t Hk, int64_t D,
+                   const int32_t* starts, int64_t B, const int32_t* seq_lens,
+                   const int32_t* page_table, int64_t max_pages, int64_t max_new,
+                   const uint8_t* k_cache, const uint8_t* k_scale, const uint8_t* v_cache,
+                   const uint8_t* v_scale, int64_t num_pages, int64_t page_size, float scale,
+                   int causal, int64_t window, void* workspace, int64_t workspace_bytes, void* Y,
+                   float* lse, int dtype, void* stream);
+
+/* Path-forcing variant (FP4W_PATH_AUTO, _ATTN_DECODE, _ATTN_PROMPT, _ATTN_GENERIC). */
+int fp8w_attention_ex(const void* q, int64_t q_stride, int64_t M, int64_t Hq, int64_t Hk, int64_t D,
+                      const int32_t* starts, int64_t B, const int32_t* seq_lens,
+                      const int32_t* page_table, int64_t max_pages, int64_t max_new,
+                      const uint8_t* k_cache, const uint8_t* k_scale, const uint8_t* v_cache,
+                      const uint8_t* v_scale, int64_t num_pages, int64_t page_size, float scale,
+                      int causal, int64_t window, void* workspace, int64_t workspace_bytes, void* Y,
+                      float* lse, int dtype, void* stream, int path);
 
 /*
  * fp4w_select_path - the path FP4W_PATH_AUTO takes for these sizes, assuming
