@@ -1,0 +1,544 @@
+// Attention over the paged 8-bit cache, head sizes 64 and 128, for a few new
+// tokens of each sequence (decode, drafted tokens).
+//
+//   s_t = scale q . K_t    O = sum_t 2^(s_t' - m) V_t / sum_t 2^(s_t' - m),  s' = s log2(e), m the largest s' so far
+//
+// Every key and value code is read once, and little is computed on it: the
+// read of the cache is the bound.  So keys and values go from HBM to registers
+// in the operand layout of the MFMAs, with no LDS in between:
+//   * S^T = K Q^T by 16 x 16 x 32 MFMAs: a lane's 16 bytes of a key are its K
+//     operand of two MFMAs (the sum over d may run in any order as long as Q
+//     follows it).
+//   * The row that a lane has in the result is one query row, four keys of it
+//     a register quad.  Which key stands in which row of the K operand is
+//     free, and is chosen so that a lane's 16 scores in a tile of 64 keys are
+//     16 keys that lie side by side: those of the 16 bytes that it loads of
+//     V^T.  So P^T goes from the softmax into the second MFMA as it is, and V,
+//     which the cache holds transposed, needs no exchange either.
+//   * Those 16 keys lie in one page (page_size % 16 == 0), so a lane has one
+//     scale of K and one of V for a tile: K's is a factor of the scores, V's
+//     the exponent operand of the conversion to T.
+// The rows of a workgroup are the query heads of one key head, times the new
+// tokens: 16, 32 or 64 of them.  Four waves take the tiles of their workgroup
+// in turn, each with a softmax of its own, and join them in LDS.
+//
+// The tiles of all sequences, one after the other, are cut into equal shares,
+// one for each workgroup of a key head: lengths may differ as they like, the
+// host need not know them, and the workspace does not grow with them.  A
+// sequence that lies in several shares is joined by a second kernel from the
+// shares' partial results, in order, so a row's result does not depend on the
+// order of work.
+
+#include <hip/hip_runtime.h>
+
+#include "heads.h"
+
+namespace fp4w {
+namespace {
+
+constexpr int kTile = 64;         // keys
+constexpr int kWaves = 4;
+constexpr int kMinShare = 4;      // tiles: one for each wave
+
+struct DecodeParams {
+  const void* q;
+  int64_t q_stride;
+  int32_t Hq, Hk, G, max_new;
+  Seqs seq;
+  const uint8_t* k_cache;
+  const uint8_t* k_scale;
+  const uint8_t* v_cache;
+  const uint8_t* v_scale;
+  float c;          // |scale| * log2(e)
+  uint32_t flip;    // sign bits of a pair of T where scale < 0
+  bool causal;
+  int32_t window;
+  void* Y;
+  float* lse;
+  int32_t* plan;    // first tile of each sequence among all, kSeqsPerLaunch + 1
+  float* part;      // per workgroup two partial results
+  int32_t W;        // workgroups of a key head
+};
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// What differs by the type: P's range and V's exponent.
+template <typename T>
+struct AttnTraits;
+template <>
+struct AttnTraits<__bf16> {
+  static constexpr float kLift = 0.0f;      // numerators are 2^(s - m + kLift)
+  static constexpr uint32_t kDown = 0;      // V is held times 2^-kDown
+  static constexpr uint32_t kMostV = 246;   // 448 * 2^119 is below BF16's largest value
+  __device__ __forceinline__ static bf16x2 cvt(uint32_t w, float s, bool hi) {
+    return hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true) : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false);
+  }
+};
+template <>
+struct AttnTraits<_Float16> {
+  // FP16 ends at 2^-14: numerators down to 2^-22 keep all their bits so, and
+  // the largest value that FP16 data leads to, 2^16, stays finite at half of it
+  static constexpr float kLift = 8.0f;
+  static constexpr uint32_t kDown = 1;
+  static constexpr uint32_t kMostV = 135;
+  __device__ __forceinline__ static f16x2 cvt(uint32_t w, float s, bool hi) {
+    return hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, true) : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, false);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ typename ActTraits<T>::vec8 decode8_power(uint32_t lo, uint32_t hi, float s) {
+  const auto a = AttnTraits<T>::cvt(lo, s, false), b = AttnTraits<T>::cvt(lo, s, true);
+  const auto c = AttnTraits<T>::cvt(hi, s, false), d = AttnTraits<T>::cvt(hi, s, true);
+  typename ActTraits<T>::vec8 r;
+  r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
+  r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
+  return r;
+}
+
+// The tiles that sequence b's rows attend: [lo, lo + count).
+struct Tiles {
+  int lo, count;
+};
+
+__device__ __forceinline__ Tiles tiles_of(const DecodeParams& p, const SeqSpan& s) {
+  if (s.rows == 0) return Tiles{0, 0};
+  const int first = s.len - s.rows, rows = s.rows < p.max_new ? s.rows : p.max_new;
+  int end = s.len < p.seq.capacity ? s.len : p.seq.capacity;
+  if (p.causal && first + rows < end) end = first + rows;
+  int begin = 0;
+  if (p.window > 0 && first >= p.window) begin = first - p.window + 1;
+  const int lo = begin / kTile, hi = end > 0 ? (end + kTile - 1) / kTile : 0;
+  return Tiles{lo, hi > lo ? hi - lo : 1};  // rows that attend nothing still need their zeros
+}
+
+// 0x80 in each byte of w that is a NaN code.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// 0xff in the bytes j of a word with lo <= j < hi.
+__device__ __forceinline__ uint32_t byte_mask(int lo, int hi) {
+  lo = lo < 0 ? 0 : lo > 4 ? 4 : lo;
+  hi = hi < 0 ? 0 : hi > 4 ? 4 : hi;
+  const uint32_t below_hi = hi == 4 ? 0xffffffffu : (1u << (8 * hi)) - 1, below_lo = lo == 4 ? 0xffffffffu : (1u << (8 * lo)) - 1;
+  return below_hi & ~below_lo;
+}
+
+constexpr int part_floats(int rows, int D) { return rows * (D + 2); }
+
+// RT tiles of 16 rows: each wave has one of them, and 4 / RT waves share the
+// keys of each.  (One wave with several row tiles would convert the codes only
+// once, but needs more than the registers of two waves a SIMD: for D = 128 it
+// spills.)
+template <typename T, int D, int RT>
+__global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams p) {
+  constexpr int KL = D / 64, DT = D / 16, ROWS = 16 * RT, PITCH = D + 4, KG = kWaves / RT;
+  typedef typename ActTraits<T>::vec8 vec8;
+  __shared__ int prefix[kSeqsPerLaunch + 1];
+  __shared__ int wave_total[kWaves];
+  __shared__ float red_m[kWaves][16], red_l[kWaves][16];
+  __shared__ float4 exchange[kWaves * 16 * PITCH / 4];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 15, g = lane >> 4;
+  const int row_tile = wave / KG, key_group = wave % KG;
+  const int w = blockIdx.x / p.Hk, hk = blockIdx.x - w * p.Hk;
+
+  // first tile of each sequence among all
+  {
+    int own[kSeqsPerLaunch / 256], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kSeqsPerLaunch / 256; ++i) {
+      const int b = tid * (kSeqsPerLaunch / 256) + i;
+      own[i] = b < p.seq.B ? tiles_of(p, seq_span(p.seq, b)).count : 0;
+      sum += own[i];
+    }
+    int before = sum;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(before, off, 64);
+      if (lane >= off) before += o;
+    }
+    if (lane == 63) wave_total[wave] = before;
+    __syncthreads();
+    before -= sum;
+    for (int i = 0; i < wave; ++i) before += wave_total[i];
+#pragma unroll
+    for (int i = 0; i < kSeqsPerLaunch / 256; ++i) {
+      const int b = tid * (kSeqsPerLaunch / 256) + i;
+      if (b <= p.seq.B) prefix[b] = before;
+      before += own[i];
+    }
+    if (tid == 255 && p.seq.B == kSeqsPerLaunch) prefix[kSeqsPerLaunch] = before;
+    __syncthreads();
+  }
+  if (blockIdx.x == 0)
+    for (int b = tid; b <= p.seq.B; b += 256) p.plan[b] = prefix[b];
+  const int total = prefix[p.seq.B];
+  int share = (total + p.W - 1) / p.W;
+  share = share < kMinShare ? kMinShare : share;
+  int at = static_cast<int64_t>(w) * share < total ? w * share : total;
+  const int stop = at + share < total ? at + share : total;
+  if (at >= stop) return;
+  int b = last_not_above(p.seq.B, at, [&](int i) { return prefix[i]; });
+
+  const int64_t head_bytes = static_cast<int64_t>(p.seq.page) * D;
+  for (; at < stop; ++b) {
+    const int t_begin = at - prefix[b], count = prefix[b + 1] - prefix[b];
+    if (count <= t_begin) continue;
+    const int t_end = (stop < prefix[b + 1] ? stop : prefix[b + 1]) - prefix[b];
+    at = prefix[b] + t_end;
+    const SeqSpan span = seq_span(p.seq, b);
+    const int lo_tile = tiles_of(p, span).lo;
+    const int first = span.len - span.rows, rows_i = span.rows < p.max_new ? span.rows : p.max_new;
+    const int held = span.len < p.seq.capacity ? span.len : p.seq.capacity;
+
+    // this lane's row: its query, and the tokens that it attends
+    vec8 qf[KL][2];
+    int k_lo, k_hi;
+    {
+      const int row = 16 * row_tile + col, i = row / p.G, head = hk * p.G + (row - i * p.G);
+      const bool valid = i < rows_i;
+      const int pos = first + i;
+      k_hi = !valid ? 0 : p.causal && pos + 1 < held ? pos + 1 : held;
+      k_lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+      const T* q = static_cast<const T*>(p.q) + (static_cast<int64_t>(span.first_row) + i) * p.q_stride + static_cast<int64_t>(head) * D;
+#pragma unroll
+      for (int j = 0; j < KL; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          u32x4 v = {0, 0, 0, 0};
+          if (valid) v = *reinterpret_cast<const u32x4*>(q + 64 * j + 16 * g + 8 * e);
+          v ^= p.flip;
+          qf[j][e] = __builtin_bit_cast(vec8, v);
+        }
+    }
+    // tokens that every valid row attends, and that any does
+    const int last = first + rows_i - 1;
+    const int all_lo = p.window > 0 && last >= p.window ? last - p.window + 1 : 0;
+    const int all_hi = p.causal && first + 1 < held ? first + 1 : held;
+    const int any_lo = p.window > 0 && first >= p.window ? first - p.window + 1 : 0;
+    const int any_hi = p.causal && last + 1 < held ? last + 1 : held;
+
+    f32x4 acc[DT];
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) acc[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // pages of this lane's 16 keys as rows of a tile of K (chunk col / 4) and as keys of V (chunk g)
+    auto page_at = [&](int t, int chunk) {
+      return t < t_end ? page_of(p.seq, b, (lo_tile + t) * kTile + 16 * chunk) : -1;
+    };
+    auto slot_at = [&](int t, int chunk) {
+      const uint32_t token = static_cast<uint32_t>((lo_tile + t) * kTile + 16 * chunk);
+      return static_cast<int>(token - fdiv(token, p.seq.page_div) * static_cast<uint32_t>(p.seq.page));
+    };
+    u32x4 kreg[4][KL], vreg[DT];
+    uint32_t ks = 127, vs = 127;
+    auto load_k = [&](int t, int id_k, int id_v) {
+      const uint8_t* k = p.k_cache + (static_cast<int64_t>(id_k < 0 ? 0 : id_k) * p.Hk + hk) * head_bytes +
+                         static_cast<int64_t>(slot_at(t, col >> 2) + (col & 3)) * D + 16 * g;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < KL; ++j) kreg[i][j] = *reinterpret_cast<const u32x4*>(k + 4 * i * D + 64 * j);
+      const int64_t cell = static_cast<int64_t>(id_v < 0 ? 0 : id_v) * p.Hk + hk;
+      ks = p.k_scale[cell];
+      vs = p.v_scale[cell];
+    };
+    auto load_v = [&](int t, int id_v) {
+      const uint8_t* v = p.v_cache + (static_cast<int64_t>(id_v < 0 ? 0 : id_v) * p.Hk + hk) * head_bytes +
+                         static_cast<int64_t>(col) * p.seq.page + slot_at(t, g);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) vreg[d] = *reinterpret_cast<const u32x4*>(v + static_cast<int64_t>(16 * d) * p.seq.page);
+    };
+
+    // (without pages there is nothing to load, and no key to attend)
+    int t = t_begin + key_group;
+    if (p.seq.capacity > 0 && t < t_end) {
+      int id_k = page_at(t, col >> 2), id_v = page_at(t, g);
+      load_k(t, id_k, id_v);
+      load_v(t, id_v);
+      int next_k = page_at(t + KG, col >> 2), next_v = page_at(t + KG, g);
+      for (; t < t_end; t += KG) {
+        const int after_k = page_at(t + 2 * KG, col >> 2), after_v = page_at(t + 2 * KG, g);
+        f32x4 s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int j = 0; j < KL; ++j) {
+            s[i] = ActTraits<T>::mfma(ActTraits<T>::decode8_fp8(kreg[i][j].x, kreg[i][j].y), qf[j][0], s[i]);
+            s[i] = ActTraits<T>::mfma(ActTraits<T>::decode8_fp8(kreg[i][j].z, kreg[i][j].w), qf[j][1], s[i]);
+          }
+        }
+        const float factor = e8m0_to_f32(ks) * p.c;
+        uint32_t vs_now = vs;
+        if (t + KG < t_end) load_k(t + KG, next_k, next_v);
+
+        const int key0 = (lo_tile + t) * kTile;
+        const int my0 = key0 + 16 * g;  // this lane's 16 keys
+        const bool whole = key0 >= all_lo && key0 + kTile <= all_hi && __ballot(id_v < 0 || vs_now > AttnTraits<T>::kMostV) == 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[i][j] *= factor;
+        uint32_t nan_any = 0, seen = 0;
+        if (!whole) {
+          const bool bad = vs_now > AttnTraits<T>::kMostV;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int key = my0 + 4 * i + j;
+              const bool on = id_v >= 0 && key >= k_lo && key < k_hi;
+              s[i][j] = on ? s[i][j] : -INFINITY;
+              seen |= on ? 1u << (4 * i + j) : 0u;
+            }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t keep = id_v < 0 ? 0 : byte_mask(any_lo - (my0 + 4 * j), any_hi - (my0 + 4 * j));
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              const uint32_t word = (bad ? 0x7f7f7f7fu : vreg[d][j]) & keep;
+              vreg[d][j] = word;
+              nan_any |= nan_codes(word);
+            }
+          }
+          if (bad || id_v < 0) vs_now = 127;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top = fmaxf(top, s[i][j]);
+        top = fmaxf(top, __shfl_xor(top, 16, 64));
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        if (__ballot(top > m) != 0) {
+          const float now = fmaxf(m, top);
+          const float shrink = __builtin_amdgcn_exp2f(m - (now > -INFINITY ? now : 0.0f));
+          l *= shrink;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) acc[d] *= shrink;
+          m = now;
+        }
+        const float base = (m > -INFINITY ? m : 0.0f) - AttnTraits<T>::kLift;
+        float sum = 0.0f;
+        vec8 pf[2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float e = __builtin_amdgcn_exp2f(s[i][j] - base);
+            sum += e;
+            pf[i >> 1][4 * (i & 1) + j] = static_cast<T>(e);  // the one rounding between the products
+          }
+        l += sum;
+        if (!whole && __ballot(nan_any != 0) != 0) {
+          // A NaN among the values: 0 x NaN must not reach the rows that do not
+          // attend it.  Count for each output the NaN values that it attends,
+          // and take them out of the product.
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            f32x4 hits = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              vec8 flag, on;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint32_t n = nan_codes(vreg[d][2 * h + (j >> 2)]);
+                flag[j] = static_cast<T>((n >> (8 * (j & 3) + 7)) & 1 ? 1.0f : 0.0f);
+                on[j] = static_cast<T>((seen >> (8 * h + j)) & 1 ? 1.0f : 0.0f);
+              }
+              hits = ActTraits<T>::mfma(flag, on, hits);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              vreg[d][j] &= ~((nan_codes(vreg[d][j]) >> 7) * 0xffu);
+              acc[d][j] = hits[j] > 0.0f ? NAN : acc[d][j];
+            }
+          }
+        }
+        const float power = __uint_as_float((vs_now > AttnTraits<T>::kDown ? vs_now - AttnTraits<T>::kDown : 0u) << 23);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          acc[d] = ActTraits<T>::mfma(decode8_power<T>(vreg[d].x, vreg[d].y, power), pf[0], acc[d]);
+          acc[d] = ActTraits<T>::mfma(decode8_power<T>(vreg[d].z, vreg[d].w, power), pf[1], acc[d]);
+        }
+        if (t + KG < t_end) load_v(t + KG, next_v);
+        id_v = next_v;
+        next_k = after_k;
+        next_v = after_v;
+      }
+    }
+
+    // join the waves of a row tile
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    if (g == 0) {
+      red_m[wave][col] = m;
+      red_l[wave][col] = l;
+    }
+    __syncthreads();
+    {
+      float most = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < KG; ++v) most = fmaxf(most, red_m[row_tile * KG + v][col]);
+      const float shrink = exp2f(m - (most > -INFINITY ? most : 0.0f));
+      float* buf = reinterpret_cast<float*>(exchange) + (wave * 16 + col) * PITCH + 4 * g;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(buf + 16 * d) = acc[d] * shrink;
+    }
+    __syncthreads();
+    const bool whole_seq = t_begin == 0 && t_end == count;
+    float* part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (t_begin == 0 ? 1 : 0)) * part_floats(ROWS, D);
+    for (int i = tid; i < ROWS * (D / 4); i += 256) {
+      const int out = i / (D / 4), d4 = i - out * (D / 4), v0 = (out >> 4) * KG, row = out & 15;
+      const int ti = out / p.G;
+      if (ti >= rows_i) continue;
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int v = 0; v < KG; ++v) top = fmaxf(top, red_m[v0 + v][row]);
+      const float base = top > -INFINITY ? top : 0.0f;
+      f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int v = 0; v < KG; ++v) {
+        o += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(exchange) + ((v0 + v) * 16 + row) * PITCH + 4 * d4);
+        sum += red_l[v0 + v][row] * exp2f(red_m[v0 + v][row] - base);
+      }
+      if (whole_seq) {
+        const int64_t at_row = (static_cast<int64_t>(span.first_row) + ti) * p.Hq + hk * p.G + (out - ti * p.G);
+        const bool any = !(sum == 0.0f);
+        const float inv = any ? static_cast<float>(1 << AttnTraits<T>::kDown) / sum : 0.0f;
+        typedef T t4 __attribute__((ext_vector_type(4)));
+        t4 y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = round_to<T>(any ? o[j] * inv : 0.0f);
+        *reinterpret_cast<t4*>(static_cast<T*>(p.Y) + at_row * D + 4 * d4) = y;
+        if (p.lse && d4 == 0) p.lse[at_row] = any ? (top + log2f(sum) - AttnTraits<T>::kLift) * 0.693147180559945309f : -INFINITY;
+      } else {
+        *reinterpret_cast<f32x4*>(part + 2 * ROWS + out * D + 4 * d4) = o;
+        if (d4 == 0) {
+          part[out] = top;
+          part[ROWS + out] = sum;
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the partial results of the sequences that lie in several shares: a
+// wave per row and head.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(const DecodeParams p, int rows) {
+  constexpr int PER = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  const int row0 = seq_start(p.seq, 0), behind = seq_start(p.seq, p.seq.B);
+  const int64_t token = u / p.Hq;
+  const int h = static_cast<int>(u - token * p.Hq);
+  const int64_t row = row0 + token;
+  if (row >= behind) return;
+  const int b = last_not_above(p.seq.B, row, [&](int i) { return seq_start(p.seq, i); });
+  const int i = static_cast<int>(row) - seq_start(p.seq, b);
+  if (i >= p.max_new) return;
+  const int total = p.plan[p.seq.B], from = p.plan[b], to = p.plan[b + 1];
+  int share = (total + p.W - 1) / p.W;
+  share = share < kMinShare ? kMinShare : share;
+  const int w0 = from / share, w1 = (to - 1) / share;
+  if (to <= from || w0 == w1) return;
+  const int hk = h / p.G, mine = i * p.G + (h - hk * p.G);
+  auto part_of = [&](int w) {
+    return p.part + ((static_cast<int64_t>(w) * p.Hk + hk) * 2 + (w == w0 ? 1 : 0)) * part_floats(rows, D);
+  };
+  float top = -INFINITY;
+  for (int w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, part_of(w)[mine]);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+  const float base = top > -INFINITY ? top : 0.0f;
+  float sum = 0.0f, o[PER] = {};
+  for (int w = w0; w <= w1; w += 8) {
+    float f[8], s[8], v[8][PER];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float* part = part_of(w + j <= w1 ? w + j : w1);
+      f[j] = part[mine];
+      s[j] = part[rows + mine];
+#pragma unroll
+      for (int d = 0; d < PER; ++d) v[j][d] = part[2 * rows + mine * D + lane * PER + d];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (w + j > w1) continue;
+      const float e = exp2f(f[j] - base);
+      sum = fmaf(s[j], e, sum);
+#pragma unroll
+      for (int d = 0; d < PER; ++d) o[d] = fmaf(v[j][d], e, o[d]);
+    }
+  }
+  const bool any = !(sum == 0.0f);
+  const float inv = any ? static_cast<float>(1 << AttnTraits<T>::kDown) / sum : 0.0f;
+  const int64_t at_row = row * p.Hq + h;
+#pragma unroll
+  for (int d = 0; d < PER; ++d) static_cast<T*>(p.Y)[at_row * D + lane * PER + d] = round_to<T>(any ? o[d] * inv : 0.0f);
+  if (p.lse && lane == 0) p.lse[at_row] = any ? (top + log2f(sum) - AttnTraits<T>::kLift) * 0.693147180559945309f : -INFINITY;
+}
+
+template <typename T, int D, int RT>
+int launch_rows(DecodeParams p, int64_t rows, hipStream_t s) {
+  hipLaunchKernelGGL((attn_decode_kernel<T, D, RT>), dim3(p.W * p.Hk), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(static_cast<uint32_t>((rows * p.Hq + 3) / 4)), dim3(256), 0, s, p, 16 * RT);
+  return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+template <typename T, int D>
+int launch_t(const DecodeParams& p, int64_t rows, hipStream_t s) {
+  switch (attn_row_tiles(p.max_new, p.G)) {
+    case 1: return launch_rows<T, D, 1>(p, rows, s);
+    case 2: return launch_rows<T, D, 2>(p, rows, s);
+    default: return launch_rows<T, D, 4>(p, rows, s);
+  }
+}
+
+}  // namespace
+
+int launch_attention_decode(const AttentionArgs& a) {
+  DecodeParams p;
+  p.q = a.q;
+  p.q_stride = a.q_stride;
+  p.Hq = static_cast<int32_t>(a.Hq);
+  p.Hk = static_cast<int32_t>(a.Hk);
+  p.G = static_cast<int32_t>(a.Hq / a.Hk);
+  p.max_new = static_cast<int32_t>(a.max_new);
+  p.k_cache = a.k_cache;
+  p.k_scale = a.k_scale;
+  p.v_cache = a.v_cache;
+  p.v_scale = a.v_scale;
+  p.c = fabsf(a.scale) * 1.44269504088896341f;
+  p.flip = a.scale < 0.0f ? 0x80008000u : 0u;
+  p.causal = a.causal;
+  p.window = static_cast<int32_t>(a.window < 0x7fffffff ? a.window : 0);  // no sequence is longer
+  p.Y = a.Y;
+  p.lse = a.lse;
+  p.W = attn_groups(a.Hk);
+  p.plan = static_cast<int32_t*>(a.work);
+  p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.work) + kAttnPlanBytes);
+  hipStream_t s = static_cast<hipStream_t>(a.stream);
+  for (int64_t b = 0; b < a.seq.B; b += kSeqsPerLaunch) {
+    SeqArgs seq = a.seq;
+    seq.B = a.seq.B - b < kSeqsPerLaunch ? a.seq.B - b : kSeqsPerLaunch;
+    seq.lens += b;
+    if (seq.starts) seq.starts += b;
+    if (seq.table) seq.table += b * seq.max_pages;
+    p.seq = make_seqs(seq, a.M);
+    p.seq.row0 = static_cast<int32_t>(b);
+    const int64_t rows = seq.starts ? a.M : seq.B;
+    int rc;
+    if (a.D == 128)
+      rc = a.act == Act::BF16 ? launch_t<__bf16, 128>(p, rows, s) : launch_t<_Float16, 128>(p, rows, s);
+    else
+      rc = a.act == Act::BF16 ? launch_t<__bf16, 64>(p, rows, s) : launch_t<_Float16, 64>(p, rows, s);
+    if (rc != 0) return rc;
+  }
+  return 0;
+}
+
+}  // namespace fp4w

@@ -78,6 +78,17 @@ int64_t cache_codes(const SeqArgs& s, int64_t Hk, int64_t D) {
   return s.num_pages * s.page_size * Hk * D;
 }
 
+// Kernels made for heads of 64 and 128.
+bool tiled(int64_t D) { return D == 64 || D == 128; }
+
+constexpr int64_t kDecodeRows = 64;  // rows of a sequence and key head that the decode kernel takes
+
+int64_t attention_bytes(int64_t Hq, int64_t Hk, int64_t D, int64_t max_new) {
+  if (!tiled(D)) return 0;
+  const int64_t G = Hq / Hk, most = std::min(max_new, std::max<int64_t>(kDecodeRows / G, 1));
+  return fp4w::attn_decode_workspace(most, Hk, G, D);
+}
+
 bool rope_vec(const RopeArgs& r, int64_t D) {
   const int64_t dims = r.cos ? r.dims : 0;
   return D >= 16 && (D & (D - 1)) == 0 && dims % 16 == 0 && aligned(r.q_weight, 16) && aligned(r.k_weight, 16) &&
@@ -182,7 +193,7 @@ int64_t fp8w_attention_workspace(int64_t M, int64_t Hq, int64_t Hk, int64_t D, i
   if (st != FP4W_OK) return st;
   if (B < 0 || B >= kMax32 || max_new < 0) return FP4W_ERR_SHAPE;
   if (Hk == 0 ? Hq != 0 : Hq % Hk != 0) return FP4W_ERR_SHAPE;
-  return 0;
+  return Hk == 0 || Hq == 0 || M == 0 || B == 0 || max_new == 0 ? 0 : attention_bytes(Hq, Hk, D, max_new);
 }
 
 int fp8w_attention_ex(const void* q, int64_t q_stride, int64_t M, int64_t Hq, int64_t Hk, int64_t D,
@@ -225,10 +236,19 @@ int fp8w_attention_ex(const void* q, int64_t q_stride, int64_t M, int64_t Hq, in
     for (int j = 0; j < i; ++j)
       if (overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return FP4W_ERR_ALIAS;
   }
-  if (path == FP4W_PATH_ATTN_DECODE || path == FP4W_PATH_ATTN_PROMPT) return FP4W_ERR_PATH;
+  const bool fast = tiled(D) && page_size % 16 == 0 && rows_vec(qi) && aligned(k_cache, 16) && aligned(v_cache, 16) && aligned(Y, 16);
+  // (the tiles of a launch's sequences are counted in 32 bits)
+  const bool decode = fast && max_new * (Hq / Hk) <= kDecodeRows &&
+                      std::min<int64_t>(B, fp4w::kSeqsPerLaunch) * (max_pages * page_size / 64 + 2) < kMax32;
+  if ((path == FP4W_PATH_ATTN_DECODE && !decode) || path == FP4W_PATH_ATTN_PROMPT) return FP4W_ERR_PATH;
   const AttentionArgs a{q, q_stride, M, Hq, Hk, D, max_new, seq, k_cache, k_scale, v_cache, v_scale, scale, causal != 0,
                         window, workspace, Y, lse, static_cast<Act>(dtype), stream};
-  return fp4w::launch_attention_generic(a) == 0 ? FP4W_OK : FP4W_ERR_LAUNCH;
+  int rc;
+  if (decode && path != FP4W_PATH_ATTN_GENERIC)
+    rc = fp4w::launch_attention_decode(a);
+  else
+    rc = fp4w::launch_attention_generic(a);
+  return rc == 0 ? FP4W_OK : FP4W_ERR_LAUNCH;
 }
 
 int fp8w_attention(const void* q, int64_t q_stride, int64_t M, int64_t Hq, int64_t Hk, int64_t D, const int32_t* starts,

@@ -40,7 +40,7 @@ struct Seqs {
   const int32_t* starts;
   const int32_t* lens;
   const int32_t* table;
-  int32_t B, M, num_pages, page, capacity;
+  int32_t B, M, num_pages, page, capacity, row0;  // row0: sequence 0's row where starts is null
   int64_t max_pages;
   FastDiv page_div;
 };
@@ -54,6 +54,7 @@ inline Seqs make_seqs(const SeqArgs& s, int64_t M) {
   d.M = static_cast<int32_t>(M);
   d.num_pages = static_cast<int32_t>(s.num_pages);
   d.page = static_cast<int32_t>(s.page_size);
+  d.row0 = 0;
   d.capacity = s.num_pages > 0 ? static_cast<int32_t>(s.max_pages * s.page_size) : 0;
   d.max_pages = s.max_pages;
   d.page_div = make_fastdiv(static_cast<uint32_t>(s.page_size));
@@ -63,7 +64,7 @@ inline Seqs make_seqs(const SeqArgs& s, int64_t M) {
 // First row of sequence b (b = B: behind the last row), inside [0, M] whatever
 // the array holds.
 __device__ __forceinline__ int seq_start(const Seqs& s, int b) {
-  if (s.starts == nullptr) return b;
+  if (s.starts == nullptr) return s.row0 + b;
   const int v = s.starts[b];
   return v < 0 ? 0 : v > s.M ? s.M : v;
 }

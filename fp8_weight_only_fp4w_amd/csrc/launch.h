@@ -307,6 +307,23 @@ int launch_qk_norm_rope(const QkNormRopeArgs& a, bool vec, const SeqArgs* seq);
 // and page_size * D <= 16384, cache codes 16-byte aligned.
 int launch_kv_append(const KvAppendArgs& a, bool vec);
 
+// The decode kernel of attention: workgroups for each key head (two for each
+// compute unit in all), each with two partial results in the workspace behind
+// the plan of a launch's sequences.
+constexpr int kSeqsPerLaunch = 1024;
+constexpr int64_t kAttnPlanBytes = 4352;  // (kSeqsPerLaunch + 1) x 4, up to 256
+inline int attn_groups(int64_t Hk) { return Hk >= 512 ? 1 : static_cast<int>(512 / Hk); }
+// 16-row tiles of max_new tokens of G query heads: 1, 2 or 4 (up to 64 rows)
+inline int attn_row_tiles(int64_t max_new, int64_t G) {
+  const int64_t rows = max_new * G;
+  return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+}
+inline int64_t attn_decode_workspace(int64_t max_new, int64_t Hk, int64_t G, int64_t D) {
+  return kAttnPlanBytes + attn_groups(Hk) * Hk * 2 * 16 * attn_row_tiles(max_new, G) * (D + 2) * 4;
+}
+// D 64 or 128, page_size % 16 == 0, max_new * Hq / Hk <= 64; q, the cache's
+// codes, Y and work 16-byte aligned, q_stride % 8 == 0.
+int launch_attention_decode(const AttentionArgs& a);
 // any validated arguments with M, B, Hq, D > 0
 int launch_attention_generic(const AttentionArgs& a);
 

@@ -579,7 +579,7 @@ int fp8w_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_str
 /*
  * Bytes of caller-owned workspace that fp8w_attention needs for these sizes,
  * or a negative fp4w_status for illegal ones.  It does not depend on how long
- * the sequences are, and does not fall when a size grows.  Host-only.
+ * the sequences are, and does not fall when M, B or max_new grows.  Host-only.
  */
 int64_t fp8w_attention_workspace(int64_t M, int64_t Hq, int64_t Hk, int64_t D, int64_t B,
                                  int64_t max_new);
