@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kTile = 64;         // keys
 constexpr int kWaves = 4;
-constexpr int kMinShare = 4;      // tiles: one for each wave
+constexpr int64_t kWideJoinRows = 1024;  // up to so many rows, the join takes 256 threads for each
 
 struct DecodeParams {
   const void* q;
@@ -56,8 +56,9 @@ struct DecodeParams {
   void* Y;
   float* lse;
   int32_t* plan;    // first tile of each sequence among all, kSeqsPerLaunch + 1
-  float* part;      // per workgroup two partial results
-  int32_t W;        // workgroups of a key head
+  float* part;      // for each share and key head two partial results
+  int32_t W;        // shares of a key head
+  int32_t rows;     // max_new * G
 };
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
@@ -123,23 +124,65 @@ __device__ __forceinline__ uint32_t byte_mask(int lo, int hi) {
   return below_hi & ~below_lo;
 }
 
-constexpr int part_floats(int rows, int D) { return rows * (D + 2); }
+// A share's partial result of a sequence that it has a part of: the maxima and
+// sums of its p.rows rows, then their unnormalised outputs.  A share ends at
+// most one sequence that an earlier share began, and begins at most one that a
+// later share ends: two places.
+__device__ __forceinline__ float* part_of(const DecodeParams& p, int D, int hk, int w, bool begins) {
+  return p.part + ((static_cast<int64_t>(w) * p.Hk + hk) * 2 + (begins ? 1 : 0)) * attn_part_floats(p.rows, D);
+}
 
-// RT tiles of 16 rows: each wave has one of them, and 4 / RT waves share the
-// keys of each.  (One wave with several row tiles would convert the codes only
-// once, but needs more than the registers of two waves a SIMD: for D = 128 it
-// spills.)
+// (m, l, o) and (m2, l2, o2): maximum, sum and output of two sets of tokens.
+__device__ __forceinline__ void join(float& m, float& l, f32x4& o, float m2, float l2, f32x4 o2) {
+  const float now = fmaxf(m, m2), base = now > -INFINITY ? now : 0.0f;
+  const float a = __builtin_amdgcn_exp2f(m - base), c = __builtin_amdgcn_exp2f(m2 - base);
+  m = now;
+  l = l * a + l2 * c;
+  o = o * a + o2 * c;
+}
+
+// Four values of a row's output; no token attended: a sum of 0 and zeros.
+template <typename T>
+__device__ __forceinline__ void store_quad(const DecodeParams& p, int64_t at_row, int D, int d, float m, float l, f32x4 o) {
+  typedef T t4 __attribute__((ext_vector_type(4)));
+  const bool any = !(l == 0.0f);
+  const float inv = any ? static_cast<float>(1 << AttnTraits<T>::kDown) / l : 0.0f;
+  t4 y;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = round_to<T>(any ? o[j] * inv : 0.0f);
+  *reinterpret_cast<t4*>(static_cast<T*>(p.Y) + at_row * D + d) = y;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_lse(const DecodeParams& p, int64_t at_row, float m, float l) {
+  constexpr float kLn2 = 0.693147180559945309f;
+  if (p.lse) p.lse[at_row] = !(l == 0.0f) ? (m + log2f(l) - AttnTraits<T>::kLift) * kLn2 : -INFINITY;
+}
+
+// 16 codes.  Those that one wave alone reads bypass what they would evict (about
+// 3 % over 530 MB).
+template <bool ONCE>
+__device__ __forceinline__ u32x4 load_codes(const uint8_t* p) {
+  if constexpr (ONCE)
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  else
+    return *reinterpret_cast<const u32x4*>(p);
+}
+
+// RT tiles of 16 rows.  A wave has one of them and a share of the tiles of
+// keys; the RT waves of a workgroup with the same share read the same keys at
+// about the same time, from L2.  (One wave with several row tiles would convert
+// the codes once, but needs more than the registers of two waves a SIMD: for D =
+// 128 it spills.)
 template <typename T, int D, int RT>
 __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams p) {
-  constexpr int KL = D / 64, DT = D / 16, ROWS = 16 * RT, PITCH = D + 4, KG = kWaves / RT;
+  constexpr int KL = D / 64, DT = D / 16, SHARES = kWaves / RT;
   typedef typename ActTraits<T>::vec8 vec8;
   __shared__ int prefix[kSeqsPerLaunch + 1];
   __shared__ int wave_total[kWaves];
-  __shared__ float red_m[kWaves][16], red_l[kWaves][16];
-  __shared__ float4 exchange[kWaves * 16 * PITCH / 4];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 15, g = lane >> 4;
-  const int row_tile = wave / KG, key_group = wave % KG;
-  const int w = blockIdx.x / p.Hk, hk = blockIdx.x - w * p.Hk;
+  const int row_tile = wave / SHARES;
+  const int group = blockIdx.x / p.Hk, hk = blockIdx.x - group * p.Hk, w = group * SHARES + wave % SHARES;
 
   // first tile of each sequence among all
   {
@@ -173,7 +216,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
     for (int b = tid; b <= p.seq.B; b += 256) p.plan[b] = prefix[b];
   const int total = prefix[p.seq.B];
   int share = (total + p.W - 1) / p.W;
-  share = share < kMinShare ? kMinShare : share;
+  share = share < 1 ? 1 : share;
   int at = static_cast<int64_t>(w) * share < total ? w * share : total;
   const int stop = at + share < total ? at + share : total;
   if (at >= stop) return;
@@ -238,7 +281,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < KL; ++j) kreg[i][j] = *reinterpret_cast<const u32x4*>(k + 4 * i * D + 64 * j);
+        for (int j = 0; j < KL; ++j) kreg[i][j] = load_codes<RT == 1>(k + 4 * i * D + 64 * j);
       const int64_t cell = static_cast<int64_t>(id_v < 0 ? 0 : id_v) * p.Hk + hk;
       ks = p.k_scale[cell];
       vs = p.v_scale[cell];
@@ -247,18 +290,18 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
       const uint8_t* v = p.v_cache + (static_cast<int64_t>(id_v < 0 ? 0 : id_v) * p.Hk + hk) * head_bytes +
                          static_cast<int64_t>(col) * p.seq.page + slot_at(t, g);
 #pragma unroll
-      for (int d = 0; d < DT; ++d) vreg[d] = *reinterpret_cast<const u32x4*>(v + static_cast<int64_t>(16 * d) * p.seq.page);
+      for (int d = 0; d < DT; ++d) vreg[d] = load_codes<RT == 1>(v + static_cast<int64_t>(16 * d) * p.seq.page);
     };
 
     // (without pages there is nothing to load, and no key to attend)
-    int t = t_begin + key_group;
+    int t = t_begin;
     if (p.seq.capacity > 0 && t < t_end) {
       int id_k = page_at(t, col >> 2), id_v = page_at(t, g);
       load_k(t, id_k, id_v);
       load_v(t, id_v);
-      int next_k = page_at(t + KG, col >> 2), next_v = page_at(t + KG, g);
-      for (; t < t_end; t += KG) {
-        const int after_k = page_at(t + 2 * KG, col >> 2), after_v = page_at(t + 2 * KG, g);
+      int next_k = page_at(t + 1, col >> 2), next_v = page_at(t + 1, g);
+      for (; t < t_end; ++t) {
+        const int after_k = page_at(t + 2, col >> 2), after_v = page_at(t + 2, g);
         f32x4 s[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -271,7 +314,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
         }
         const float factor = e8m0_to_f32(ks) * p.c;
         uint32_t vs_now = vs;
-        if (t + KG < t_end) load_k(t + KG, next_k, next_v);
+        if (t + 1 < t_end) load_k(t + 1, next_k, next_v);
 
         const int key0 = (lo_tile + t) * kTile;
         const int my0 = key0 + 16 * g;  // this lane's 16 keys
@@ -362,139 +405,103 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
           acc[d] = ActTraits<T>::mfma(decode8_power<T>(vreg[d].x, vreg[d].y, power), pf[0], acc[d]);
           acc[d] = ActTraits<T>::mfma(decode8_power<T>(vreg[d].z, vreg[d].w, power), pf[1], acc[d]);
         }
-        if (t + KG < t_end) load_v(t + KG, next_v);
+        if (t + 1 < t_end) load_v(t + 1, next_v);
         id_v = next_v;
         next_k = after_k;
         next_v = after_v;
       }
     }
 
-    // join the waves of a row tile
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
-    if (g == 0) {
-      red_m[wave][col] = m;
-      red_l[wave][col] = l;
-    }
-    __syncthreads();
-    {
-      float most = -INFINITY;
+    const int out = 16 * row_tile + col, i = out / p.G;
+    if (i < rows_i) {
+      if (t_begin == 0 && t_end == count) {  // the whole sequence
+        const int64_t at_row = (static_cast<int64_t>(span.first_row) + i) * p.Hq + hk * p.G + (out - i * p.G);
 #pragma unroll
-      for (int v = 0; v < KG; ++v) most = fmaxf(most, red_m[row_tile * KG + v][col]);
-      const float shrink = exp2f(m - (most > -INFINITY ? most : 0.0f));
-      float* buf = reinterpret_cast<float*>(exchange) + (wave * 16 + col) * PITCH + 4 * g;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(buf + 16 * d) = acc[d] * shrink;
-    }
-    __syncthreads();
-    const bool whole_seq = t_begin == 0 && t_end == count;
-    float* part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (t_begin == 0 ? 1 : 0)) * part_floats(ROWS, D);
-    for (int i = tid; i < ROWS * (D / 4); i += 256) {
-      const int out = i / (D / 4), d4 = i - out * (D / 4), v0 = (out >> 4) * KG, row = out & 15;
-      const int ti = out / p.G;
-      if (ti >= rows_i) continue;
-      float top = -INFINITY, sum = 0.0f;
-#pragma unroll
-      for (int v = 0; v < KG; ++v) top = fmaxf(top, red_m[v0 + v][row]);
-      const float base = top > -INFINITY ? top : 0.0f;
-      f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int v = 0; v < KG; ++v) {
-        o += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(exchange) + ((v0 + v) * 16 + row) * PITCH + 4 * d4);
-        sum += red_l[v0 + v][row] * exp2f(red_m[v0 + v][row] - base);
-      }
-      if (whole_seq) {
-        const int64_t at_row = (static_cast<int64_t>(span.first_row) + ti) * p.Hq + hk * p.G + (out - ti * p.G);
-        const bool any = !(sum == 0.0f);
-        const float inv = any ? static_cast<float>(1 << AttnTraits<T>::kDown) / sum : 0.0f;
-        typedef T t4 __attribute__((ext_vector_type(4)));
-        t4 y;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = round_to<T>(any ? o[j] * inv : 0.0f);
-        *reinterpret_cast<t4*>(static_cast<T*>(p.Y) + at_row * D + 4 * d4) = y;
-        if (p.lse && d4 == 0) p.lse[at_row] = any ? (top + log2f(sum) - AttnTraits<T>::kLift) * 0.693147180559945309f : -INFINITY;
+        for (int d = 0; d < DT; ++d) store_quad<T>(p, at_row, D, 16 * d + 4 * g, m, l, acc[d]);
+        if (g == 0) store_lse<T>(p, at_row, m, l);
       } else {
-        *reinterpret_cast<f32x4*>(part + 2 * ROWS + out * D + 4 * d4) = o;
-        if (d4 == 0) {
-          part[out] = top;
-          part[ROWS + out] = sum;
+        float* part = part_of(p, D, hk, w, t_begin == 0);
+        float* row = part + attn_part_head(p.rows) + out * D + 4 * g;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(row + 16 * d) = acc[d];
+        if (g == 0) {
+          part[out] = m;
+          part[p.rows + out] = l;
         }
       }
     }
-    __syncthreads();
   }
 }
 
-// Joins the partial results of the sequences that lie in several shares: a
-// wave per row and head.
-template <typename T, int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(const DecodeParams p, int rows) {
-  constexpr int PER = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  const int row0 = seq_start(p.seq, 0), behind = seq_start(p.seq, p.seq.B);
-  const int64_t token = u / p.Hq;
-  const int h = static_cast<int>(u - token * p.Hq);
-  const int64_t row = row0 + token;
-  if (row >= behind) return;
+// Joins the partial results of the sequences that lie in several shares: THREADS
+// threads for a row of a head, D / 4 of them for one partial result.
+template <typename T, int D, int THREADS>
+__global__ __launch_bounds__(THREADS) void attn_join_kernel(const DecodeParams p) {
+  constexpr int LANES = D / 4, GROUPS = THREADS / LANES, AT_ONCE = 4;
+  __shared__ float red_m[GROUPS], red_l[GROUPS];
+  __shared__ f32x4 red_o[GROUPS][LANES];
+  const int tid = threadIdx.x, group = tid / LANES, lane = tid % LANES;
+  const int64_t row = seq_start(p.seq, 0) + blockIdx.x / p.Hq;
+  const int h = static_cast<int>(blockIdx.x % p.Hq);
+  if (row >= seq_start(p.seq, p.seq.B)) return;
   const int b = last_not_above(p.seq.B, row, [&](int i) { return seq_start(p.seq, i); });
   const int i = static_cast<int>(row) - seq_start(p.seq, b);
-  if (i >= p.max_new) return;
   const int total = p.plan[p.seq.B], from = p.plan[b], to = p.plan[b + 1];
   int share = (total + p.W - 1) / p.W;
-  share = share < kMinShare ? kMinShare : share;
+  share = share < 1 ? 1 : share;
   const int w0 = from / share, w1 = (to - 1) / share;
-  if (to <= from || w0 == w1) return;
+  if (i >= p.max_new || to <= from || w0 == w1) return;
   const int hk = h / p.G, mine = i * p.G + (h - hk * p.G);
-  auto part_of = [&](int w) {
-    return p.part + ((static_cast<int64_t>(w) * p.Hk + hk) * 2 + (w == w0 ? 1 : 0)) * part_floats(rows, D);
-  };
-  float top = -INFINITY;
-  for (int w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, part_of(w)[mine]);
+  float m = -INFINITY, l = 0.0f;
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int w = w0 + group; w <= w1; w += GROUPS * AT_ONCE) {
+    float pm[AT_ONCE], pl[AT_ONCE];
+    f32x4 po[AT_ONCE];
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-  const float base = top > -INFINITY ? top : 0.0f;
-  float sum = 0.0f, o[PER] = {};
-  for (int w = w0; w <= w1; w += 8) {
-    float f[8], s[8], v[8][PER];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float* part = part_of(w + j <= w1 ? w + j : w1);
-      f[j] = part[mine];
-      s[j] = part[rows + mine];
-#pragma unroll
-      for (int d = 0; d < PER; ++d) v[j][d] = part[2 * rows + mine * D + lane * PER + d];
+    for (int j = 0; j < AT_ONCE; ++j) {
+      const int v = w + j * GROUPS <= w1 ? w + j * GROUPS : w;
+      const float* part = part_of(p, D, hk, v, v == w0);
+      pm[j] = part[mine];
+      pl[j] = part[p.rows + mine];
+      po[j] = *reinterpret_cast<const f32x4*>(part + attn_part_head(p.rows) + mine * D + 4 * lane);
+      if (w + j * GROUPS > w1) pm[j] = -INFINITY, pl[j] = 0.0f, po[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (w + j > w1) continue;
-      const float e = exp2f(f[j] - base);
-      sum = fmaf(s[j], e, sum);
-#pragma unroll
-      for (int d = 0; d < PER; ++d) o[d] = fmaf(v[j][d], e, o[d]);
-    }
+    for (int j = 0; j < AT_ONCE; ++j) join(m, l, o, pm[j], pl[j], po[j]);
   }
-  const bool any = !(sum == 0.0f);
-  const float inv = any ? static_cast<float>(1 << AttnTraits<T>::kDown) / sum : 0.0f;
-  const int64_t at_row = row * p.Hq + h;
+  if (lane == 0) {
+    red_m[group] = m;
+    red_l[group] = l;
+  }
+  red_o[group][lane] = o;
+  __syncthreads();
+  if (group != 0) return;
 #pragma unroll
-  for (int d = 0; d < PER; ++d) static_cast<T*>(p.Y)[at_row * D + lane * PER + d] = round_to<T>(any ? o[d] * inv : 0.0f);
-  if (p.lse && lane == 0) p.lse[at_row] = any ? (top + log2f(sum) - AttnTraits<T>::kLift) * 0.693147180559945309f : -INFINITY;
+  for (int v = 1; v < GROUPS; ++v) join(m, l, o, red_m[v], red_l[v], red_o[v][lane]);
+  store_quad<T>(p, row * p.Hq + h, D, 4 * lane, m, l, o);
+  if (lane == 0) store_lse<T>(p, row * p.Hq + h, m, l);
 }
 
 template <typename T, int D, int RT>
-int launch_rows(DecodeParams p, int64_t rows, hipStream_t s) {
-  hipLaunchKernelGGL((attn_decode_kernel<T, D, RT>), dim3(p.W * p.Hk), dim3(256), 0, s, p);
-  hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(static_cast<uint32_t>((rows * p.Hq + 3) / 4)), dim3(256), 0, s, p, 16 * RT);
+int launch_rows(DecodeParams p, int64_t join_rows, hipStream_t s) {
+  p.W = attn_groups(p.Hk) * (kWaves / RT);
+  hipLaunchKernelGGL((attn_decode_kernel<T, D, RT>), dim3(attn_groups(p.Hk) * p.Hk), dim3(256), 0, s, p);
+  const dim3 grid(static_cast<uint32_t>(join_rows * p.Hq));
+  if (join_rows * p.Hq <= kWideJoinRows)
+    hipLaunchKernelGGL((attn_join_kernel<T, D, 256>), grid, dim3(256), 0, s, p);
+  else
+    hipLaunchKernelGGL((attn_join_kernel<T, D, 64>), grid, dim3(64), 0, s, p);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 template <typename T, int D>
-int launch_t(const DecodeParams& p, int64_t rows, hipStream_t s) {
+int launch_t(const DecodeParams& p, int64_t join_rows, hipStream_t s) {
   switch (attn_row_tiles(p.max_new, p.G)) {
-    case 1: return launch_rows<T, D, 1>(p, rows, s);
-    case 2: return launch_rows<T, D, 2>(p, rows, s);
-    default: return launch_rows<T, D, 4>(p, rows, s);
+    case 1: return launch_rows<T, D, 1>(p, join_rows, s);
+    case 2: return launch_rows<T, D, 2>(p, join_rows, s);
+    default: return launch_rows<T, D, 4>(p, join_rows, s);
   }
 }
 
@@ -518,7 +525,7 @@ int launch_attention_decode(const AttentionArgs& a) {
   p.window = static_cast<int32_t>(a.window < 0x7fffffff ? a.window : 0);  // no sequence is longer
   p.Y = a.Y;
   p.lse = a.lse;
-  p.W = attn_groups(a.Hk);
+  p.rows = p.max_new * p.G;
   p.plan = static_cast<int32_t*>(a.work);
   p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.work) + kAttnPlanBytes);
   hipStream_t s = static_cast<hipStream_t>(a.stream);

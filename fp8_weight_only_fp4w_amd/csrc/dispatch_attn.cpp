@@ -85,8 +85,7 @@ constexpr int64_t kDecodeRows = 64;  // rows of a sequence and key head that the
 
 int64_t attention_bytes(int64_t Hq, int64_t Hk, int64_t D, int64_t max_new) {
   if (!tiled(D)) return 0;
-  const int64_t G = Hq / Hk, most = std::min(max_new, std::max<int64_t>(kDecodeRows / G, 1));
-  return fp4w::attn_decode_workspace(most, Hk, G, D);
+  return fp4w::attn_decode_workspace(max_new, Hk, Hq / Hk, D);
 }
 
 bool rope_vec(const RopeArgs& r, int64_t D) {
@@ -237,8 +236,8 @@ int fp8w_attention_ex(const void* q, int64_t q_stride, int64_t M, int64_t Hq, in
       if (overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return FP4W_ERR_ALIAS;
   }
   const bool fast = tiled(D) && page_size % 16 == 0 && rows_vec(qi) && aligned(k_cache, 16) && aligned(v_cache, 16) && aligned(Y, 16);
-  // (the tiles of a launch's sequences are counted in 32 bits)
-  const bool decode = fast && max_new * (Hq / Hk) <= kDecodeRows &&
+  // (the tiles of a launch's sequences are counted in 32 bits, and so are a grid's threads)
+  const bool decode = fast && max_new * (Hq / Hk) <= kDecodeRows && M * Hq < (1 << 25) &&
                       std::min<int64_t>(B, fp4w::kSeqsPerLaunch) * (max_pages * page_size / 64 + 2) < kMax32;
   if ((path == FP4W_PATH_ATTN_DECODE && !decode) || path == FP4W_PATH_ATTN_PROMPT) return FP4W_ERR_PATH;
   const AttentionArgs a{q, q_stride, M, Hq, Hk, D, max_new, seq, k_cache, k_scale, v_cache, v_scale, scale, causal != 0,

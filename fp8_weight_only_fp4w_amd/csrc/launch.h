@@ -307,9 +307,9 @@ int launch_qk_norm_rope(const QkNormRopeArgs& a, bool vec, const SeqArgs* seq);
 // and page_size * D <= 16384, cache codes 16-byte aligned.
 int launch_kv_append(const KvAppendArgs& a, bool vec);
 
-// The decode kernel of attention: workgroups for each key head (two for each
-// compute unit in all), each with two partial results in the workspace behind
-// the plan of a launch's sequences.
+// The decode kernel of attention: workgroups of four waves for each key head
+// (two for each compute unit in all).  In the workspace, behind the plan of a
+// launch's sequences: two partial results for each share of a key head's tiles.
 constexpr int kSeqsPerLaunch = 1024;
 constexpr int64_t kAttnPlanBytes = 4352;  // (kSeqsPerLaunch + 1) x 4, up to 256
 inline int attn_groups(int64_t Hk) { return Hk >= 512 ? 1 : static_cast<int>(512 / Hk); }
@@ -318,8 +318,18 @@ inline int attn_row_tiles(int64_t max_new, int64_t G) {
   const int64_t rows = max_new * G;
   return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
 }
+// maxima and sums of `rows` rows in whole 16-byte units, then their outputs
+constexpr int64_t attn_part_head(int64_t rows) { return (2 * rows + 3) / 4 * 4; }
+constexpr int64_t attn_part_floats(int64_t rows, int64_t D) { return attn_part_head(rows) + rows * D; }
+// (more rows mean fewer shares: a buffer has to serve fewer new tokens too)
 inline int64_t attn_decode_workspace(int64_t max_new, int64_t Hk, int64_t G, int64_t D) {
-  return kAttnPlanBytes + attn_groups(Hk) * Hk * 2 * 16 * attn_row_tiles(max_new, G) * (D + 2) * 4;
+  int64_t most = 0;
+  for (int64_t rows = 16; rows <= 64; rows *= 2) {
+    const int64_t n = max_new < rows / G ? max_new : rows / G;
+    const int64_t floats = attn_groups(Hk) * 4 / attn_row_tiles(n, G) * Hk * 2 * attn_part_floats(n * G, D);
+    most = most > floats ? most : floats;
+  }
+  return kAttnPlanBytes + most * 4;
 }
 // D 64 or 128, page_size % 16 == 0, max_new * Hq / Hk <= 64; q, the cache's
 // codes, Y and work 16-byte aligned, q_stride % 8 == 0.
