@@ -1,0 +1,124 @@
+// What the attention kernels share (attention.hip, attention_prompt.hip): their
+// arguments, the types' traits, the join of partial results and the outputs.
+#pragma once
+
+#include "heads.h"
+
+namespace fp4w {
+
+constexpr int kTile = 64;  // keys
+
+struct AttnParams {
+  const void* q;
+  int64_t q_stride;
+  int32_t Hq, Hk, G, max_new;
+  Seqs seq;
+  const uint8_t* k_cache;
+  const uint8_t* k_scale;
+  const uint8_t* v_cache;
+  const uint8_t* v_scale;
+  float c;          // |scale| * log2(e)
+  uint32_t flip;    // sign bits of a pair of T where scale < 0
+  bool causal;
+  int32_t window;   // 0: none
+  void* Y;
+  float* lse;
+};
+
+inline AttnParams make_attn(const AttentionArgs& a) {
+  AttnParams p;
+  p.q = a.q;
+  p.q_stride = a.q_stride;
+  p.Hq = static_cast<int32_t>(a.Hq);
+  p.Hk = static_cast<int32_t>(a.Hk);
+  p.G = static_cast<int32_t>(a.Hq / a.Hk);
+  p.max_new = static_cast<int32_t>(a.max_new);
+  p.seq = make_seqs(a.seq, a.M);
+  p.k_cache = a.k_cache;
+  p.k_scale = a.k_scale;
+  p.v_cache = a.v_cache;
+  p.v_scale = a.v_scale;
+  p.c = fabsf(a.scale) * 1.44269504088896341f;
+  p.flip = a.scale < 0.0f ? 0x80008000u : 0u;
+  p.causal = a.causal;
+  p.window = static_cast<int32_t>(a.window < 0x7fffffff ? a.window : 0);  // no sequence is longer
+  p.Y = a.Y;
+  p.lse = a.lse;
+  return p;
+}
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// What differs by the type: P's range and V's exponent.
+template <typename T>
+struct AttnTraits;
+template <>
+struct AttnTraits<__bf16> {
+  static constexpr float kLift = 0.0f;      // numerators are 2^(s - m + kLift)
+  static constexpr uint32_t kDown = 0;      // V is held times 2^-kDown
+  static constexpr uint32_t kMostV = 246;   // 448 * 2^119 is below BF16's largest value
+  __device__ __forceinline__ static bf16x2 cvt(uint32_t w, float s, bool hi) {
+    return hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true) : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false);
+  }
+};
+template <>
+struct AttnTraits<_Float16> {
+  // FP16 ends at 2^-14: numerators down to 2^-22 keep all their bits so, and
+  // the largest value that FP16 data leads to, 2^16, stays finite at half of it
+  static constexpr float kLift = 8.0f;
+  static constexpr uint32_t kDown = 1;
+  static constexpr uint32_t kMostV = 135;
+  __device__ __forceinline__ static f16x2 cvt(uint32_t w, float s, bool hi) {
+    return hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, true) : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, false);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ typename ActTraits<T>::vec8 decode8_power(uint32_t lo, uint32_t hi, float s) {
+  const auto a = AttnTraits<T>::cvt(lo, s, false), b = AttnTraits<T>::cvt(lo, s, true);
+  const auto c = AttnTraits<T>::cvt(hi, s, false), d = AttnTraits<T>::cvt(hi, s, true);
+  typename ActTraits<T>::vec8 r;
+  r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
+  r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
+  return r;
+}
+
+// 0x80 in each byte of w that is a NaN code.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// 0xff in the bytes j of a word with lo <= j < hi.
+__device__ __forceinline__ uint32_t byte_mask(int lo, int hi) {
+  lo = lo < 0 ? 0 : lo > 4 ? 4 : lo;
+  hi = hi < 0 ? 0 : hi > 4 ? 4 : hi;
+  const uint32_t below_hi = hi == 4 ? 0xffffffffu : (1u << (8 * hi)) - 1, below_lo = lo == 4 ? 0xffffffffu : (1u << (8 * lo)) - 1;
+  return below_hi & ~below_lo;
+}
+
+// (m, l, o) and (m2, l2, o2): maximum, sum and output of two sets of tokens.
+__device__ __forceinline__ void join(float& m, float& l, f32x4& o, float m2, float l2, f32x4 o2) {
+  const float now = fmaxf(m, m2), base = now > -INFINITY ? now : 0.0f;
+  const float a = __builtin_amdgcn_exp2f(m - base), c = __builtin_amdgcn_exp2f(m2 - base);
+  m = now;
+  l = l * a + l2 * c;
+  o = o * a + o2 * c;
+}
+
+// Four values of a row's output; no token attended: a sum of 0 and zeros.
+template <typename T>
+__device__ __forceinline__ void store_quad(const AttnParams& p, int64_t at_row, int D, int d, float m, float l, f32x4 o) {
+  typedef T t4 __attribute__((ext_vector_type(4)));
+  const bool any = !(l == 0.0f);
+  const float inv = any ? static_cast<float>(1 << AttnTraits<T>::kDown) / l : 0.0f;
+  t4 y;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = round_to<T>(any ? o[j] * inv : 0.0f);
+  *reinterpret_cast<t4*>(static_cast<T*>(p.Y) + at_row * D + d) = y;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_lse(const AttnParams& p, int64_t at_row, float m, float l) {
+  constexpr float kLn2 = 0.693147180559945309f;
+  if (p.lse) p.lse[at_row] = !(l == 0.0f) ? (m + log2f(l) - AttnTraits<T>::kLift) * kLn2 : -INFINITY;
+}
+
+}  // namespace fp4w

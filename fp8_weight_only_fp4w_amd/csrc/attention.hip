@@ -31,71 +31,21 @@
 
 #include <hip/hip_runtime.h>
 
-#include "heads.h"
+#include "attention.h"
 
 namespace fp4w {
 namespace {
 
-constexpr int kTile = 64;         // keys
 constexpr int kWaves = 4;
 constexpr int64_t kWideJoinRows = 1024;  // up to so many rows, the join takes 256 threads for each
 
 struct DecodeParams {
-  const void* q;
-  int64_t q_stride;
-  int32_t Hq, Hk, G, max_new;
-  Seqs seq;
-  const uint8_t* k_cache;
-  const uint8_t* k_scale;
-  const uint8_t* v_cache;
-  const uint8_t* v_scale;
-  float c;          // |scale| * log2(e)
-  uint32_t flip;    // sign bits of a pair of T where scale < 0
-  bool causal;
-  int32_t window;
-  void* Y;
-  float* lse;
+  AttnParams a;
   int32_t* plan;    // first tile of each sequence among all, kSeqsPerLaunch + 1
   float* part;      // for each share and key head two partial results
   int32_t W;        // shares of a key head
   int32_t rows;     // max_new * G
 };
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-// What differs by the type: P's range and V's exponent.
-template <typename T>
-struct AttnTraits;
-template <>
-struct AttnTraits<__bf16> {
-  static constexpr float kLift = 0.0f;      // numerators are 2^(s - m + kLift)
-  static constexpr uint32_t kDown = 0;      // V is held times 2^-kDown
-  static constexpr uint32_t kMostV = 246;   // 448 * 2^119 is below BF16's largest value
-  __device__ __forceinline__ static bf16x2 cvt(uint32_t w, float s, bool hi) {
-    return hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true) : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false);
-  }
-};
-template <>
-struct AttnTraits<_Float16> {
-  // FP16 ends at 2^-14: numerators down to 2^-22 keep all their bits so, and
-  // the largest value that FP16 data leads to, 2^16, stays finite at half of it
-  static constexpr float kLift = 8.0f;
-  static constexpr uint32_t kDown = 1;
-  static constexpr uint32_t kMostV = 135;
-  __device__ __forceinline__ static f16x2 cvt(uint32_t w, float s, bool hi) {
-    return hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, true) : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, false);
-  }
-};
-
-template <typename T>
-__device__ __forceinline__ typename ActTraits<T>::vec8 decode8_power(uint32_t lo, uint32_t hi, float s) {
-  const auto a = AttnTraits<T>::cvt(lo, s, false), b = AttnTraits<T>::cvt(lo, s, true);
-  const auto c = AttnTraits<T>::cvt(hi, s, false), d = AttnTraits<T>::cvt(hi, s, true);
-  typename ActTraits<T>::vec8 r;
-  r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
-  r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
-  return r;
-}
 
 // The tiles that sequence b's rows attend: [lo, lo + count).
 struct Tiles {
@@ -104,24 +54,13 @@ struct Tiles {
 
 __device__ __forceinline__ Tiles tiles_of(const DecodeParams& p, const SeqSpan& s) {
   if (s.rows == 0) return Tiles{0, 0};
-  const int first = s.len - s.rows, rows = s.rows < p.max_new ? s.rows : p.max_new;
-  int end = s.len < p.seq.capacity ? s.len : p.seq.capacity;
-  if (p.causal && first + rows < end) end = first + rows;
+  const int first = s.len - s.rows, rows = s.rows < p.a.max_new ? s.rows : p.a.max_new;
+  int end = s.len < p.a.seq.capacity ? s.len : p.a.seq.capacity;
+  if (p.a.causal && first + rows < end) end = first + rows;
   int begin = 0;
-  if (p.window > 0 && first >= p.window) begin = first - p.window + 1;
+  if (p.a.window > 0 && first >= p.a.window) begin = first - p.a.window + 1;
   const int lo = begin / kTile, hi = end > 0 ? (end + kTile - 1) / kTile : 0;
   return Tiles{lo, hi > lo ? hi - lo : 1};  // rows that attend nothing still need their zeros
-}
-
-// 0x80 in each byte of w that is a NaN code.
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-
-// 0xff in the bytes j of a word with lo <= j < hi.
-__device__ __forceinline__ uint32_t byte_mask(int lo, int hi) {
-  lo = lo < 0 ? 0 : lo > 4 ? 4 : lo;
-  hi = hi < 0 ? 0 : hi > 4 ? 4 : hi;
-  const uint32_t below_hi = hi == 4 ? 0xffffffffu : (1u << (8 * hi)) - 1, below_lo = lo == 4 ? 0xffffffffu : (1u << (8 * lo)) - 1;
-  return below_hi & ~below_lo;
 }
 
 // A share's partial result of a sequence that it has a part of: the maxima and
@@ -129,34 +68,7 @@ __device__ __forceinline__ uint32_t byte_mask(int lo, int hi) {
 // most one sequence that an earlier share began, and begins at most one that a
 // later share ends: two places.
 __device__ __forceinline__ float* part_of(const DecodeParams& p, int D, int hk, int w, bool begins) {
-  return p.part + ((static_cast<int64_t>(w) * p.Hk + hk) * 2 + (begins ? 1 : 0)) * attn_part_floats(p.rows, D);
-}
-
-// (m, l, o) and (m2, l2, o2): maximum, sum and output of two sets of tokens.
-__device__ __forceinline__ void join(float& m, float& l, f32x4& o, float m2, float l2, f32x4 o2) {
-  const float now = fmaxf(m, m2), base = now > -INFINITY ? now : 0.0f;
-  const float a = __builtin_amdgcn_exp2f(m - base), c = __builtin_amdgcn_exp2f(m2 - base);
-  m = now;
-  l = l * a + l2 * c;
-  o = o * a + o2 * c;
-}
-
-// Four values of a row's output; no token attended: a sum of 0 and zeros.
-template <typename T>
-__device__ __forceinline__ void store_quad(const DecodeParams& p, int64_t at_row, int D, int d, float m, float l, f32x4 o) {
-  typedef T t4 __attribute__((ext_vector_type(4)));
-  const bool any = !(l == 0.0f);
-  const float inv = any ? static_cast<float>(1 << AttnTraits<T>::kDown) / l : 0.0f;
-  t4 y;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) y[j] = round_to<T>(any ? o[j] * inv : 0.0f);
-  *reinterpret_cast<t4*>(static_cast<T*>(p.Y) + at_row * D + d) = y;
-}
-
-template <typename T>
-__device__ __forceinline__ void store_lse(const DecodeParams& p, int64_t at_row, float m, float l) {
-  constexpr float kLn2 = 0.693147180559945309f;
-  if (p.lse) p.lse[at_row] = !(l == 0.0f) ? (m + log2f(l) - AttnTraits<T>::kLift) * kLn2 : -INFINITY;
+  return p.part + ((static_cast<int64_t>(w) * p.a.Hk + hk) * 2 + (begins ? 1 : 0)) * attn_part_floats(p.rows, D);
 }
 
 // 16 codes.  Those that one wave alone reads bypass what they would evict (about
@@ -182,7 +94,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
   __shared__ int wave_total[kWaves];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int row_tile = wave / SHARES;
-  const int group = blockIdx.x / p.Hk, hk = blockIdx.x - group * p.Hk, w = group * SHARES + wave % SHARES;
+  const int group = blockIdx.x / p.a.Hk, hk = blockIdx.x - group * p.a.Hk, w = group * SHARES + wave % SHARES;
 
   // first tile of each sequence among all
   {
@@ -190,7 +102,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
 #pragma unroll
     for (int i = 0; i < kSeqsPerLaunch / 256; ++i) {
       const int b = tid * (kSeqsPerLaunch / 256) + i;
-      own[i] = b < p.seq.B ? tiles_of(p, seq_span(p.seq, b)).count : 0;
+      own[i] = b < p.a.seq.B ? tiles_of(p, seq_span(p.a.seq, b)).count : 0;
       sum += own[i];
     }
     int before = sum;
@@ -206,59 +118,59 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
 #pragma unroll
     for (int i = 0; i < kSeqsPerLaunch / 256; ++i) {
       const int b = tid * (kSeqsPerLaunch / 256) + i;
-      if (b <= p.seq.B) prefix[b] = before;
+      if (b <= p.a.seq.B) prefix[b] = before;
       before += own[i];
     }
-    if (tid == 255 && p.seq.B == kSeqsPerLaunch) prefix[kSeqsPerLaunch] = before;
+    if (tid == 255 && p.a.seq.B == kSeqsPerLaunch) prefix[kSeqsPerLaunch] = before;
     __syncthreads();
   }
   if (blockIdx.x == 0)
-    for (int b = tid; b <= p.seq.B; b += 256) p.plan[b] = prefix[b];
-  const int total = prefix[p.seq.B];
+    for (int b = tid; b <= p.a.seq.B; b += 256) p.plan[b] = prefix[b];
+  const int total = prefix[p.a.seq.B];
   int share = (total + p.W - 1) / p.W;
   share = share < 1 ? 1 : share;
   int at = static_cast<int64_t>(w) * share < total ? w * share : total;
   const int stop = at + share < total ? at + share : total;
   if (at >= stop) return;
-  int b = last_not_above(p.seq.B, at, [&](int i) { return prefix[i]; });
+  int b = last_not_above(p.a.seq.B, at, [&](int i) { return prefix[i]; });
 
-  const int64_t head_bytes = static_cast<int64_t>(p.seq.page) * D;
+  const int64_t head_bytes = static_cast<int64_t>(p.a.seq.page) * D;
   for (; at < stop; ++b) {
     const int t_begin = at - prefix[b], count = prefix[b + 1] - prefix[b];
     if (count <= t_begin) continue;
     const int t_end = (stop < prefix[b + 1] ? stop : prefix[b + 1]) - prefix[b];
     at = prefix[b] + t_end;
-    const SeqSpan span = seq_span(p.seq, b);
+    const SeqSpan span = seq_span(p.a.seq, b);
     const int lo_tile = tiles_of(p, span).lo;
-    const int first = span.len - span.rows, rows_i = span.rows < p.max_new ? span.rows : p.max_new;
-    const int held = span.len < p.seq.capacity ? span.len : p.seq.capacity;
+    const int first = span.len - span.rows, rows_i = span.rows < p.a.max_new ? span.rows : p.a.max_new;
+    const int held = span.len < p.a.seq.capacity ? span.len : p.a.seq.capacity;
 
     // this lane's row: its query, and the tokens that it attends
     vec8 qf[KL][2];
     int k_lo, k_hi;
     {
-      const int row = 16 * row_tile + col, i = row / p.G, head = hk * p.G + (row - i * p.G);
+      const int row = 16 * row_tile + col, i = row / p.a.G, head = hk * p.a.G + (row - i * p.a.G);
       const bool valid = i < rows_i;
       const int pos = first + i;
-      k_hi = !valid ? 0 : p.causal && pos + 1 < held ? pos + 1 : held;
-      k_lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
-      const T* q = static_cast<const T*>(p.q) + (static_cast<int64_t>(span.first_row) + i) * p.q_stride + static_cast<int64_t>(head) * D;
+      k_hi = !valid ? 0 : p.a.causal && pos + 1 < held ? pos + 1 : held;
+      k_lo = p.a.window > 0 && pos >= p.a.window ? pos - p.a.window + 1 : 0;
+      const T* q = static_cast<const T*>(p.a.q) + (static_cast<int64_t>(span.first_row) + i) * p.a.q_stride + static_cast<int64_t>(head) * D;
 #pragma unroll
       for (int j = 0; j < KL; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           u32x4 v = {0, 0, 0, 0};
           if (valid) v = *reinterpret_cast<const u32x4*>(q + 64 * j + 16 * g + 8 * e);
-          v ^= p.flip;
+          v ^= p.a.flip;
           qf[j][e] = __builtin_bit_cast(vec8, v);
         }
     }
     // tokens that every valid row attends, and that any does
     const int last = first + rows_i - 1;
-    const int all_lo = p.window > 0 && last >= p.window ? last - p.window + 1 : 0;
-    const int all_hi = p.causal && first + 1 < held ? first + 1 : held;
-    const int any_lo = p.window > 0 && first >= p.window ? first - p.window + 1 : 0;
-    const int any_hi = p.causal && last + 1 < held ? last + 1 : held;
+    const int all_lo = p.a.window > 0 && last >= p.a.window ? last - p.a.window + 1 : 0;
+    const int all_hi = p.a.causal && first + 1 < held ? first + 1 : held;
+    const int any_lo = p.a.window > 0 && first >= p.a.window ? first - p.a.window + 1 : 0;
+    const int any_hi = p.a.causal && last + 1 < held ? last + 1 : held;
 
     f32x4 acc[DT];
     float m = -INFINITY, l = 0.0f;
@@ -267,35 +179,35 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
 
     // pages of this lane's 16 keys as rows of a tile of K (chunk col / 4) and as keys of V (chunk g)
     auto page_at = [&](int t, int chunk) {
-      return t < t_end ? page_of(p.seq, b, (lo_tile + t) * kTile + 16 * chunk) : -1;
+      return t < t_end ? page_of(p.a.seq, b, (lo_tile + t) * kTile + 16 * chunk) : -1;
     };
     auto slot_at = [&](int t, int chunk) {
       const uint32_t token = static_cast<uint32_t>((lo_tile + t) * kTile + 16 * chunk);
-      return static_cast<int>(token - fdiv(token, p.seq.page_div) * static_cast<uint32_t>(p.seq.page));
+      return static_cast<int>(token - fdiv(token, p.a.seq.page_div) * static_cast<uint32_t>(p.a.seq.page));
     };
     u32x4 kreg[4][KL], vreg[DT];
     uint32_t ks = 127, vs = 127;
     auto load_k = [&](int t, int id_k, int id_v) {
-      const uint8_t* k = p.k_cache + (static_cast<int64_t>(id_k < 0 ? 0 : id_k) * p.Hk + hk) * head_bytes +
+      const uint8_t* k = p.a.k_cache + (static_cast<int64_t>(id_k < 0 ? 0 : id_k) * p.a.Hk + hk) * head_bytes +
                          static_cast<int64_t>(slot_at(t, col >> 2) + (col & 3)) * D + 16 * g;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < KL; ++j) kreg[i][j] = load_codes<RT == 1>(k + 4 * i * D + 64 * j);
-      const int64_t cell = static_cast<int64_t>(id_v < 0 ? 0 : id_v) * p.Hk + hk;
-      ks = p.k_scale[cell];
-      vs = p.v_scale[cell];
+      const int64_t cell = static_cast<int64_t>(id_v < 0 ? 0 : id_v) * p.a.Hk + hk;
+      ks = p.a.k_scale[cell];
+      vs = p.a.v_scale[cell];
     };
     auto load_v = [&](int t, int id_v) {
-      const uint8_t* v = p.v_cache + (static_cast<int64_t>(id_v < 0 ? 0 : id_v) * p.Hk + hk) * head_bytes +
-                         static_cast<int64_t>(col) * p.seq.page + slot_at(t, g);
+      const uint8_t* v = p.a.v_cache + (static_cast<int64_t>(id_v < 0 ? 0 : id_v) * p.a.Hk + hk) * head_bytes +
+                         static_cast<int64_t>(col) * p.a.seq.page + slot_at(t, g);
 #pragma unroll
-      for (int d = 0; d < DT; ++d) vreg[d] = load_codes<RT == 1>(v + static_cast<int64_t>(16 * d) * p.seq.page);
+      for (int d = 0; d < DT; ++d) vreg[d] = load_codes<RT == 1>(v + static_cast<int64_t>(16 * d) * p.a.seq.page);
     };
 
     // (without pages there is nothing to load, and no key to attend)
     int t = t_begin;
-    if (p.seq.capacity > 0 && t < t_end) {
+    if (p.a.seq.capacity > 0 && t < t_end) {
       int id_k = page_at(t, col >> 2), id_v = page_at(t, g);
       load_k(t, id_k, id_v);
       load_v(t, id_v);
@@ -312,7 +224,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
             s[i] = ActTraits<T>::mfma(ActTraits<T>::decode8_fp8(kreg[i][j].z, kreg[i][j].w), qf[j][1], s[i]);
           }
         }
-        const float factor = e8m0_to_f32(ks) * p.c;
+        const float factor = e8m0_to_f32(ks) * p.a.c;
         uint32_t vs_now = vs;
         if (t + 1 < t_end) load_k(t + 1, next_k, next_v);
 
@@ -414,13 +326,13 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
 
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
-    const int out = 16 * row_tile + col, i = out / p.G;
+    const int out = 16 * row_tile + col, i = out / p.a.G;
     if (i < rows_i) {
       if (t_begin == 0 && t_end == count) {  // the whole sequence
-        const int64_t at_row = (static_cast<int64_t>(span.first_row) + i) * p.Hq + hk * p.G + (out - i * p.G);
+        const int64_t at_row = (static_cast<int64_t>(span.first_row) + i) * p.a.Hq + hk * p.a.G + (out - i * p.a.G);
 #pragma unroll
-        for (int d = 0; d < DT; ++d) store_quad<T>(p, at_row, D, 16 * d + 4 * g, m, l, acc[d]);
-        if (g == 0) store_lse<T>(p, at_row, m, l);
+        for (int d = 0; d < DT; ++d) store_quad<T>(p.a, at_row, D, 16 * d + 4 * g, m, l, acc[d]);
+        if (g == 0) store_lse<T>(p.a, at_row, m, l);
       } else {
         float* part = part_of(p, D, hk, w, t_begin == 0);
         float* row = part + attn_part_head(p.rows) + out * D + 4 * g;
@@ -443,17 +355,17 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(const DecodeParams p
   __shared__ float red_m[GROUPS], red_l[GROUPS];
   __shared__ f32x4 red_o[GROUPS][LANES];
   const int tid = threadIdx.x, group = tid / LANES, lane = tid % LANES;
-  const int64_t row = seq_start(p.seq, 0) + blockIdx.x / p.Hq;
-  const int h = static_cast<int>(blockIdx.x % p.Hq);
-  if (row >= seq_start(p.seq, p.seq.B)) return;
-  const int b = last_not_above(p.seq.B, row, [&](int i) { return seq_start(p.seq, i); });
-  const int i = static_cast<int>(row) - seq_start(p.seq, b);
-  const int total = p.plan[p.seq.B], from = p.plan[b], to = p.plan[b + 1];
+  const int64_t row = seq_start(p.a.seq, 0) + blockIdx.x / p.a.Hq;
+  const int h = static_cast<int>(blockIdx.x % p.a.Hq);
+  if (row >= seq_start(p.a.seq, p.a.seq.B)) return;
+  const int b = last_not_above(p.a.seq.B, row, [&](int i) { return seq_start(p.a.seq, i); });
+  const int i = static_cast<int>(row) - seq_start(p.a.seq, b);
+  const int total = p.plan[p.a.seq.B], from = p.plan[b], to = p.plan[b + 1];
   int share = (total + p.W - 1) / p.W;
   share = share < 1 ? 1 : share;
   const int w0 = from / share, w1 = (to - 1) / share;
-  if (i >= p.max_new || to <= from || w0 == w1) return;
-  const int hk = h / p.G, mine = i * p.G + (h - hk * p.G);
+  if (i >= p.a.max_new || to <= from || w0 == w1) return;
+  const int hk = h / p.a.G, mine = i * p.a.G + (h - hk * p.a.G);
   float m = -INFINITY, l = 0.0f;
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int w = w0 + group; w <= w1; w += GROUPS * AT_ONCE) {
@@ -480,16 +392,16 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(const DecodeParams p
   if (group != 0) return;
 #pragma unroll
   for (int v = 1; v < GROUPS; ++v) join(m, l, o, red_m[v], red_l[v], red_o[v][lane]);
-  store_quad<T>(p, row * p.Hq + h, D, 4 * lane, m, l, o);
-  if (lane == 0) store_lse<T>(p, row * p.Hq + h, m, l);
+  store_quad<T>(p.a, row * p.a.Hq + h, D, 4 * lane, m, l, o);
+  if (lane == 0) store_lse<T>(p.a, row * p.a.Hq + h, m, l);
 }
 
 template <typename T, int D, int RT>
 int launch_rows(DecodeParams p, int64_t join_rows, hipStream_t s) {
-  p.W = attn_groups(p.Hk) * (kWaves / RT);
-  hipLaunchKernelGGL((attn_decode_kernel<T, D, RT>), dim3(attn_groups(p.Hk) * p.Hk), dim3(256), 0, s, p);
-  const dim3 grid(static_cast<uint32_t>(join_rows * p.Hq));
-  if (join_rows * p.Hq <= kWideJoinRows)
+  p.W = attn_groups(p.a.Hk) * (kWaves / RT);
+  hipLaunchKernelGGL((attn_decode_kernel<T, D, RT>), dim3(attn_groups(p.a.Hk) * p.a.Hk), dim3(256), 0, s, p);
+  const dim3 grid(static_cast<uint32_t>(join_rows * p.a.Hq));
+  if (join_rows * p.a.Hq <= kWideJoinRows)
     hipLaunchKernelGGL((attn_join_kernel<T, D, 256>), grid, dim3(256), 0, s, p);
   else
     hipLaunchKernelGGL((attn_join_kernel<T, D, 64>), grid, dim3(64), 0, s, p);
@@ -498,7 +410,7 @@ int launch_rows(DecodeParams p, int64_t join_rows, hipStream_t s) {
 
 template <typename T, int D>
 int launch_t(const DecodeParams& p, int64_t join_rows, hipStream_t s) {
-  switch (attn_row_tiles(p.max_new, p.G)) {
+  switch (attn_row_tiles(p.a.max_new, p.a.G)) {
     case 1: return launch_rows<T, D, 1>(p, join_rows, s);
     case 2: return launch_rows<T, D, 2>(p, join_rows, s);
     default: return launch_rows<T, D, 4>(p, join_rows, s);
@@ -509,23 +421,8 @@ int launch_t(const DecodeParams& p, int64_t join_rows, hipStream_t s) {
 
 int launch_attention_decode(const AttentionArgs& a) {
   DecodeParams p;
-  p.q = a.q;
-  p.q_stride = a.q_stride;
-  p.Hq = static_cast<int32_t>(a.Hq);
-  p.Hk = static_cast<int32_t>(a.Hk);
-  p.G = static_cast<int32_t>(a.Hq / a.Hk);
-  p.max_new = static_cast<int32_t>(a.max_new);
-  p.k_cache = a.k_cache;
-  p.k_scale = a.k_scale;
-  p.v_cache = a.v_cache;
-  p.v_scale = a.v_scale;
-  p.c = fabsf(a.scale) * 1.44269504088896341f;
-  p.flip = a.scale < 0.0f ? 0x80008000u : 0u;
-  p.causal = a.causal;
-  p.window = static_cast<int32_t>(a.window < 0x7fffffff ? a.window : 0);  // no sequence is longer
-  p.Y = a.Y;
-  p.lse = a.lse;
-  p.rows = p.max_new * p.G;
+  p.a = make_attn(a);
+  p.rows = p.a.max_new * p.a.G;
   p.plan = static_cast<int32_t*>(a.work);
   p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(a.work) + kAttnPlanBytes);
   hipStream_t s = static_cast<hipStream_t>(a.stream);
@@ -535,8 +432,8 @@ int launch_attention_decode(const AttentionArgs& a) {
     seq.lens += b;
     if (seq.starts) seq.starts += b;
     if (seq.table) seq.table += b * seq.max_pages;
-    p.seq = make_seqs(seq, a.M);
-    p.seq.row0 = static_cast<int32_t>(b);
+    p.a.seq = make_seqs(seq, a.M);
+    p.a.seq.row0 = static_cast<int32_t>(b);
     const int64_t rows = seq.starts ? a.M : seq.B;
     int rc;
     if (a.D == 128)

@@ -83,9 +83,10 @@ bool tiled(int64_t D) { return D == 64 || D == 128; }
 
 constexpr int64_t kDecodeRows = 64;  // rows of a sequence and key head that the decode kernel takes
 
-int64_t attention_bytes(int64_t Hq, int64_t Hk, int64_t D, int64_t max_new) {
+int64_t attention_bytes(int64_t M, int64_t Hq, int64_t Hk, int64_t D, int64_t B, int64_t max_new) {
   if (!tiled(D)) return 0;
-  return fp4w::attn_decode_workspace(max_new, Hk, Hq / Hk, D);
+  const int64_t G = Hq / Hk;
+  return std::max(fp4w::attn_decode_workspace(max_new, Hk, G, D), fp4w::attn_prompt_workspace(M, G, B, Hk, D));
 }
 
 bool rope_vec(const RopeArgs& r, int64_t D) {
@@ -192,7 +193,7 @@ int64_t fp8w_attention_workspace(int64_t M, int64_t Hq, int64_t Hk, int64_t D, i
   if (st != FP4W_OK) return st;
   if (B < 0 || B >= kMax32 || max_new < 0) return FP4W_ERR_SHAPE;
   if (Hk == 0 ? Hq != 0 : Hq % Hk != 0) return FP4W_ERR_SHAPE;
-  return Hk == 0 || Hq == 0 || M == 0 || B == 0 || max_new == 0 ? 0 : attention_bytes(Hq, Hk, D, max_new);
+  return Hk == 0 || Hq == 0 || M == 0 || B == 0 || max_new == 0 ? 0 : attention_bytes(M, Hq, Hk, D, B, max_new);
 }
 
 int fp8w_attention_ex(const void* q, int64_t q_stride, int64_t M, int64_t Hq, int64_t Hk, int64_t D,
@@ -239,12 +240,16 @@ int fp8w_attention_ex(const void* q, int64_t q_stride, int64_t M, int64_t Hq, in
   // (the tiles of a launch's sequences are counted in 32 bits, and so are a grid's threads)
   const bool decode = fast && max_new * (Hq / Hk) <= kDecodeRows && M * Hq < (1 << 25) &&
                       std::min<int64_t>(B, fp4w::kSeqsPerLaunch) * (max_pages * page_size / 64 + 2) < kMax32;
-  if ((path == FP4W_PATH_ATTN_DECODE && !decode) || path == FP4W_PATH_ATTN_PROMPT) return FP4W_ERR_PATH;
+  const bool prompt = fast && max_pages * page_size < kMax32 - 128 &&
+                      (fp4w::attn_row_tiles_most(M, Hq / Hk, B) * Hk + 2 * fp4w::kPromptWork) * 256 < 2 * kMax32;
+  if ((path == FP4W_PATH_ATTN_DECODE && !decode) || (path == FP4W_PATH_ATTN_PROMPT && !prompt)) return FP4W_ERR_PATH;
   const AttentionArgs a{q, q_stride, M, Hq, Hk, D, max_new, seq, k_cache, k_scale, v_cache, v_scale, scale, causal != 0,
                         window, workspace, Y, lse, static_cast<Act>(dtype), stream};
   int rc;
-  if (decode && path != FP4W_PATH_ATTN_GENERIC)
+  if (decode && (path == FP4W_PATH_AUTO || path == FP4W_PATH_ATTN_DECODE))
     rc = fp4w::launch_attention_decode(a);
+  else if (prompt && path != FP4W_PATH_ATTN_GENERIC)
+    rc = fp4w::launch_attention_prompt(a);
   else
     rc = fp4w::launch_attention_generic(a);
   return rc == 0 ? FP4W_OK : FP4W_ERR_LAUNCH;

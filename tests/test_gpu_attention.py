@@ -21,8 +21,8 @@ def _gpu():
 def paths(D, page, rows):
     """The kernels that take heads of D, pages of `page` tokens and `rows` rows of a sequence and key head."""
     got = [fw.PATH_AUTO, fw.PATH_ATTN_GENERIC]
-    if D in (64, 128) and page % 16 == 0 and rows <= 64:
-        got.append(fw.PATH_ATTN_DECODE)
+    if D in (64, 128) and page % 16 == 0:
+        got += [fw.PATH_ATTN_PROMPT] + ([fw.PATH_ATTN_DECODE] if rows <= 64 else [])
     return got
 
 
@@ -217,7 +217,7 @@ def test_many_sequences(Hq, Hk):
     check(q, parts, starts, lens, table, "bf16")
 
 
-@pytest.mark.parametrize("path", [fw.PATH_ATTN_DECODE, fw.PATH_ATTN_GENERIC])
+@pytest.mark.parametrize("path", [fw.PATH_ATTN_DECODE, fw.PATH_ATTN_PROMPT, fw.PATH_ATTN_GENERIC])
 def test_same_bits_again_and_for_a_dirty_workspace(path):
     rng = np.random.default_rng(28)
     starts, lens, table, pages = batch(rng, [3000, 50, 1200], [2, 1, 2], 16)
