@@ -55,6 +55,7 @@ struct AttnTraits;
 template <>
 struct AttnTraits<__bf16> {
   static constexpr float kLift = 0.0f;      // numerators are 2^(s - m + kLift)
+  static constexpr float kLag = 8.0f;       // and m may be smaller than the largest s so far by kLag
   static constexpr uint32_t kDown = 0;      // V is held times 2^-kDown
   static constexpr uint32_t kMostV = 246;   // 448 * 2^119 is below BF16's largest value
   __device__ __forceinline__ static bf16x2 cvt(uint32_t w, float s, bool hi) {
@@ -66,6 +67,7 @@ struct AttnTraits<_Float16> {
   // FP16 ends at 2^-14: numerators down to 2^-22 keep all their bits so, and
   // the largest value that FP16 data leads to, 2^16, stays finite at half of it
   static constexpr float kLift = 8.0f;
+  static constexpr float kLag = 6.0f;
   static constexpr uint32_t kDown = 1;
   static constexpr uint32_t kMostV = 135;
   __device__ __forceinline__ static f16x2 cvt(uint32_t w, float s, bool hi) {

@@ -39,6 +39,12 @@ struct Mfma32<_Float16> {
   __device__ __forceinline__ static f32x16 run(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
 };
 
+// The larger of a lane's value and that of the lane 32 on.
+__device__ __forceinline__ float other_half_max(float x) {
+  const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1]));
+}
+
 // Row tiles are numbered from floor(starts[b] G / R) + b on for sequence b: n
 // tokens have at most n G / R + 1 of them, so two sequences never meet.
 template <int R>
@@ -81,7 +87,8 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(const PromptParams 
   __shared__ __attribute__((aligned(16))) T k_lds[2][kTile * KP];
   __shared__ __attribute__((aligned(16))) T v_lds[2][D * VP];
   __shared__ float scale_lds[2][4];
-  __shared__ int absent_lds[2], nan_lds[2];
+  __shared__ uint16_t nan_lds[2][D][4];  // which of a value's 16 keys of a chunk are NaN; for tiles of nan_tile - 1
+  __shared__ int absent_lds[2], nan_tile[2];
   const AttnParams& p = pp.a;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 31, h = lane >> 5;
   // the last row tiles of a prompt have the most keys: they come first
@@ -112,94 +119,90 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(const PromptParams 
       qf[i] = __builtin_bit_cast(vec8, v);
     }
   }
-  // of the wave's rows: tokens that all attend and that any does; of the workgroup's: that any does
+  // tokens that all of the wave's rows attend, and that any of the workgroup's does
   const int w_rows = r.rows - 32 * wave < 32 ? r.rows - 32 * wave : 32;
   const int w_low = r.first + (r.row0 + 32 * wave) / p.G, w_high = r.first + (r.row0 + 32 * wave + w_rows - 1) / p.G;
   const int all_lo = p.window > 0 && w_high >= p.window ? w_high - p.window + 1 : 0;
-  const int all_hi = p.causal && w_low + 1 < r.held ? w_low + 1 : r.held;
-  const int w_lo = p.window > 0 && w_low >= p.window ? w_low - p.window + 1 : 0;
-  const int w_hi = w_rows <= 0 ? 0 : p.causal && w_high + 1 < r.held ? w_high + 1 : r.held;
+  const int all_hi = w_rows <= 0 ? 0 : p.causal && w_low + 1 < r.held ? w_low + 1 : r.held;
   const int g_low = r.first + r.row0 / p.G, g_high = r.first + (r.row0 + r.rows - 1) / p.G;
   const int any_lo = p.window > 0 && g_low >= p.window ? g_low - p.window + 1 : 0;
   const int any_hi = p.causal && g_high + 1 < r.held ? g_high + 1 : r.held;
 
+  // A thread's pieces of a tile are of one chunk of 16 keys (so of one page): of K
+  // one key's 16 values each, of V one value's 16 keys.
+  const int chunk = tid & 3, piece = tid >> 2;
   const int64_t head_bytes = static_cast<int64_t>(p.seq.page) * D;
-  // this thread's pieces of a tile: K's key and 16 values, V's value and 16 keys
   u32x4 kreg[CHUNKS], vreg[CHUNKS];
-  uint32_t vscale[CHUNKS];
-  auto cell_of = [&](int64_t t, int chunk, bool* here) {
-    const int id = page_of(p.seq, r.b, static_cast<int>(t * kTile + 16 * chunk));
-    *here = id >= 0;
-    return static_cast<int64_t>(id < 0 ? 0 : id) * p.Hk + hk;
-  };
-  auto slot_of = [&](int64_t t, int chunk) {
+  uint32_t k_byte = 0, v_byte = 0;
+  int id = 0;  // page of the chunk in the registers, or -1
+  auto page_at = [&](int64_t t) { return t < t_end ? page_of(p.seq, r.b, static_cast<int>(t * kTile + 16 * chunk)) : -1; };
+  auto load = [&](int64_t t, int page_id) {
+    id = page_id;
     const uint32_t token_at = static_cast<uint32_t>(t * kTile + 16 * chunk);
-    return static_cast<int>(token_at - fdiv(token_at, p.seq.page_div) * static_cast<uint32_t>(p.seq.page));
-  };
-  constexpr int KROW = D / 16;  // pieces of a key
-  float my_scale = 0.0f;
-  int my_absent = 0;
-  auto load = [&](int64_t t) {
+    const uint32_t slot = token_at - fdiv(token_at, p.seq.page_div) * static_cast<uint32_t>(p.seq.page);
+    const int64_t cell = static_cast<int64_t>(id < 0 ? 0 : id) * p.Hk + hk;
+    const uint8_t* k = p.k_cache + cell * head_bytes + static_cast<int64_t>(slot) * D + 16 * piece;
+    const uint8_t* v = p.v_cache + cell * head_bytes + slot + static_cast<int64_t>(piece) * p.seq.page;
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-      const int piece = tid + 256 * i, key = piece / KROW, part = piece % KROW;
-      bool here;
-      const int64_t cell = cell_of(t, key >> 4, &here);
-      kreg[i] = *reinterpret_cast<const u32x4*>(p.k_cache + cell * head_bytes + static_cast<int64_t>(slot_of(t, key >> 4) + (key & 15)) * D + 16 * part);
+      kreg[i] = *reinterpret_cast<const u32x4*>(k + 1024 * i);
+      vreg[i] = *reinterpret_cast<const u32x4*>(v + static_cast<int64_t>(64 * i) * p.seq.page);
     }
-    bool here;
-    const int chunk = tid & 3;
-    const int64_t cell = cell_of(t, chunk, &here);
-    const int slot = slot_of(t, chunk);
-    const uint32_t byte = here ? p.v_scale[cell] : 127u;
-#pragma unroll
-    for (int i = 0; i < CHUNKS; ++i) {
-      const int d = (tid >> 2) + 64 * i;
-      vreg[i] = *reinterpret_cast<const u32x4*>(p.v_cache + cell * head_bytes + static_cast<int64_t>(d) * p.seq.page + slot);
-      vscale[i] = here ? byte : 256u;
-    }
-    my_scale = here ? e8m0_to_f32(p.k_scale[cell]) * p.c : 0.0f;
-    my_absent = here ? 0 : 1;
+    k_byte = p.k_scale[cell];
+    v_byte = p.v_scale[cell];
   };
   auto store = [&](int64_t t, int buf) {
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-      const int piece = tid + 256 * i, key = piece / KROW, part = piece % KROW;
-      const int at = (key & 32) | ((key >> 2 & 3) << 3) | ((key >> 4 & 1) << 2) | (key & 3);
-      vec8* to = reinterpret_cast<vec8*>(&k_lds[buf][at * KP + 16 * part]);
+      const int at = piece + 64 * i, key = at / (D / 16), part = at % (D / 16);  // key: of the chunk's 16
+      const int row = ((chunk >> 1) << 5) | ((key >> 2) << 3) | ((chunk & 1) << 2) | (key & 3);
+      vec8* to = reinterpret_cast<vec8*>(&k_lds[buf][row * KP + 16 * part]);
       to[0] = ActTraits<T>::decode8_fp8(kreg[i].x, kreg[i].y);
       to[1] = ActTraits<T>::decode8_fp8(kreg[i].z, kreg[i].w);
     }
-    const int chunk = tid & 3, key0 = static_cast<int>(t * kTile) + 16 * chunk;
-    uint32_t byte = vscale[0];
-    uint32_t nan_any = 0;
-    if (byte > AttnTraits<T>::kMostV || key0 < any_lo || key0 + 16 > any_hi) {
-      // values that nobody attends become 0 (whatever they hold), those of a
-      // page whose scale is no number (or too large for T) NaN
-      const bool here = byte < 256;
-      const bool bad = here && byte > AttnTraits<T>::kMostV;
+    const int key0 = static_cast<int>(t * kTile) + 16 * chunk;
+    const bool bad = v_byte > AttnTraits<T>::kMostV;
+    uint32_t byte = v_byte;
+    uint32_t nans[CHUNKS];
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) any |= nan_codes(vreg[i][j]);
+    const bool edge = id < 0 || bad || key0 < any_lo || key0 + 16 > any_hi || any != 0;
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) nans[i] = 0;
+    if (edge) {
+      // values that nobody attends become 0, whatever they hold; those of a page
+      // whose scale is no number (or too large for T) NaN; NaN is noted apart
+      asm volatile("" ::: "memory");
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t keep = here ? byte_mask(any_lo - (key0 + 4 * j), any_hi - (key0 + 4 * j)) : 0u;
+        const uint32_t keep = id < 0 ? 0u : byte_mask(any_lo - (key0 + 4 * j), any_hi - (key0 + 4 * j));
 #pragma unroll
-        for (int i = 0; i < CHUNKS; ++i) vreg[i][j] = (bad ? 0x7f7f7f7fu : vreg[i][j]) & keep;
+        for (int i = 0; i < CHUNKS; ++i) {
+          const uint32_t word = (bad ? 0x7f7f7f7fu : vreg[i][j]) & keep, n = nan_codes(word) >> 7;
+          vreg[i][j] = word & ~(n * 0xffu);
+          nans[i] |= ((n & 1) | (n >> 7 & 2) | (n >> 14 & 4) | (n >> 21 & 8)) << (4 * j);
+        }
       }
-      if (bad || !here) byte = 127;
+      if (bad || id < 0) byte = 127;
     }
     const float power = __uint_as_float((byte > AttnTraits<T>::kDown ? byte - AttnTraits<T>::kDown : 0u) << 23);
+    any = 0;
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-      const int d = (tid >> 2) + 64 * i;
+      const int d = piece + 64 * i;
       vec8* to = reinterpret_cast<vec8*>(&v_lds[buf][d * VP + 16 * chunk]);
       to[0] = decode8_power<T>(vreg[i].x, vreg[i].y, power);
       to[1] = decode8_power<T>(vreg[i].z, vreg[i].w, power);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) nan_any |= nan_codes(vreg[i][j]);
+      nan_lds[buf][d][chunk] = static_cast<uint16_t>(nans[i]);
+      any |= nans[i];
     }
-    if (tid < 4) scale_lds[buf][tid] = my_scale;
-    const uint64_t absent = __ballot(my_absent != 0);
+    if (tid < 4) scale_lds[buf][tid] = id < 0 ? 0.0f : e8m0_to_f32(k_byte) * p.c;
+    const uint64_t absent = __ballot(id < 0);
     if (tid == 0) absent_lds[buf] = static_cast<int>(absent & 15);
-    if (nan_any != 0) nan_lds[buf] = static_cast<int>(t) + 1;
+    if (any != 0) nan_tile[buf] = static_cast<int>(t) + 1;
   };
 
   f32x16 acc[DT];
@@ -210,109 +213,107 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(const PromptParams 
   float m = -INFINITY, l = 0.0f;
 
   if (p.seq.capacity > 0 && t_begin < t_end) {
-    if (tid < 2) nan_lds[tid] = 0;
+    if (tid < 2) nan_tile[tid] = 0;
+    load(t_begin, page_at(t_begin));
+    int next = page_at(t_begin + 1);
     __syncthreads();
-    load(t_begin);
     store(t_begin, 0);
     __syncthreads();
     int buf = 0;
     for (int64_t t = t_begin; t < t_end; ++t, buf ^= 1) {
-      if (t + 1 < t_end) load(t + 1);
+      const int after = page_at(t + 2);
+      if (t + 1 < t_end) load(t + 1, next);
+      next = after;
       const int key0 = static_cast<int>(t * kTile);
-      if (key0 < w_hi && key0 + kTile > w_lo) {
-        const T* ks = k_lds[buf];
-        const T* vs = v_lds[buf];
-        f32x16 s[2];
+      const T* ks = k_lds[buf] + col * KP + 8 * h;
+      const T* vs = v_lds[buf] + col * VP + 16 * h;
+      f32x16 s[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const f32x16 zero = {0.0f};
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          s[i] = Mfma32<T>::run(*reinterpret_cast<const vec8*>(ks + 32 * i * KP + 16 * k), qf[k], k == 0 ? zero : s[i]);
+      }
+      const int absent = absent_lds[buf];
+      float factor[2] = {scale_lds[buf][h], scale_lds[buf][2 + h]};
+      uint32_t seen = 0xffffffffu;
+      if (!(key0 >= all_lo && key0 + kTile <= all_hi && absent == 0)) {
+        asm volatile("" ::: "memory");
+        seen = 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) s[i][j] = 0.0f;
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-            s[i] = Mfma32<T>::run(*reinterpret_cast<const vec8*>(ks + (32 * i + col) * KP + 16 * k + 8 * h), qf[k], s[i]);
-        }
-        const int absent = absent_lds[buf];
-        const bool whole = key0 >= all_lo && key0 + kTile <= all_hi && absent == 0;
-        uint32_t seen = 0xffffffffu;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float factor = scale_lds[buf][2 * i + h];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) s[i][j] *= factor;
-        }
-        if (!whole) {
-          seen = 0;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const bool here = ((absent >> (2 * i + h)) & 1) == 0;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int key = key0 + 32 * i + 16 * h + j;
-              const bool on = here && key >= k_lo && key < k_hi;
-              s[i][j] = on ? s[i][j] : -INFINITY;
-              seen |= on ? 1u << (16 * i + j) : 0u;
-            }
-          }
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) top = fmaxf(top, s[i][j]);
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        if (__ballot(top > m) != 0) {
-          const float now = fmaxf(m, top);
-          const float shrink = __builtin_amdgcn_exp2f(m - (now > -INFINITY ? now : 0.0f));
-          l *= shrink;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) acc[d] *= shrink;
-          m = now;
-        }
-        const float base = (m > -INFINITY ? m : 0.0f) - AttnTraits<T>::kLift;
-        vec8 pf[4];
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
+          const bool here = ((absent >> (2 * i + h)) & 1) == 0;
+          const int my0 = key0 + 32 * i + 16 * h;
+          const int from = here ? k_lo - my0 : 16, to = k_hi - my0;  // this lane's 16 keys: [from, to) are attended
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float e = __builtin_amdgcn_exp2f(s[i][j] - base);
-            sum += e;
-            pf[2 * i + (j >> 3)][j & 7] = static_cast<T>(e);  // the one rounding between the products
+            const bool on = j >= from && j < to;
+            s[i][j] = on ? s[i][j] * factor[i] : -INFINITY;
+            seen |= on ? 1u << (16 * i + j) : 0u;
           }
-        l += sum;
-        if (nan_lds[buf] == static_cast<int>(t) + 1) {
-          // a NaN among the values: 0 x NaN must not reach the rows that do not
-          // attend it, so the NaN values that each output attends are counted
-          // apart and left out of the product
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            f32x16 hits;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) hits[j] = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              vec8 v = *reinterpret_cast<const vec8*>(vs + (32 * d + col) * VP + 16 * (2 * (k >> 1) + h) + 8 * (k & 1)), flag, on;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const bool nan = !(static_cast<float>(v[j]) == static_cast<float>(v[j]));
-                flag[j] = static_cast<T>(nan ? 1.0f : 0.0f);
-                v[j] = nan ? static_cast<T>(0.0f) : v[j];
-                on[j] = static_cast<T>((seen >> (8 * k + j)) & 1 ? 1.0f : 0.0f);
-              }
-              hits = Mfma32<T>::run(flag, on, hits);
-              acc[d] = Mfma32<T>::run(v, pf[k], acc[d]);
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) acc[d][j] = hits[j] > 0.0f ? NAN : acc[d][j];
-          }
-        } else {
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              acc[d] = Mfma32<T>::run(*reinterpret_cast<const vec8*>(vs + (32 * d + col) * VP + 16 * (2 * (k >> 1) + h) + 8 * (k & 1)), pf[k], acc[d]);
+          factor[i] = 1.0f;
         }
       }
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float most = s[i][0];
+#pragma unroll
+        for (int j = 1; j < 16; ++j) most = fmaxf(most, s[i][j]);
+        top = fmaxf(top, most * factor[i]);
+      }
+      top = other_half_max(top);
+      // The maximum that numerators are taken to may lag behind by kLag: they
+      // stay in T's range, and the outputs are seldom rescaled.
+      if (__ballot(top > m + AttnTraits<T>::kLag) != 0) {
+        asm volatile("" ::: "memory");
+        const float now = fmaxf(m, top);
+        const float shrink = __builtin_amdgcn_exp2f(m - (now > -INFINITY ? now : 0.0f));
+        l *= shrink;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) acc[d] *= shrink;
+        m = now;
+      }
+      const float base = AttnTraits<T>::kLift - (m > -INFINITY ? m : 0.0f);
+      vec8 pf[4];
+      float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float e = __builtin_amdgcn_exp2f(fmaf(s[i][j], factor[i], base));
+          sum[i] += e;
+          pf[2 * i + (j >> 3)][j & 7] = static_cast<T>(e);  // the one rounding between the products
+        }
+      l += sum[0] + sum[1];
+      if (nan_tile[buf] == static_cast<int>(t) + 1) {
+        // 0 x NaN must not reach the rows that do not attend it: the NaN values
+        // that each output attends are counted apart (they are 0 in v_lds)
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          f32x16 hits = {0.0f};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t at = nan_lds[buf][32 * d + col][2 * (k >> 1) + h] >> (8 * (k & 1)), bits = seen >> (8 * k);
+            vec8 flag, on;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              flag[j] = static_cast<T>((at >> j) & 1 ? 1.0f : 0.0f);
+              on[j] = static_cast<T>((bits >> j) & 1 ? 1.0f : 0.0f);
+            }
+            hits = Mfma32<T>::run(flag, on, hits);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) acc[d][j] = hits[j] > 0.0f ? NAN : acc[d][j];
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          acc[d] = Mfma32<T>::run(*reinterpret_cast<const vec8*>(vs + 32 * d * VP + 32 * (k >> 1) + 8 * (k & 1)), pf[k], acc[d]);
       if (t + 1 < t_end) store(t + 1, buf ^ 1);
       __syncthreads();
     }
