@@ -39,6 +39,14 @@ struct Mfma32<_Float16> {
   __device__ __forceinline__ static f32x16 run(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
 };
 
+// c + a + b.
+__device__ __forceinline__ float add_pair(__bf16 a, __bf16 b, float c) {
+  return __builtin_amdgcn_fdot2_f32_bf16(bf16x2{a, b}, bf16x2{static_cast<__bf16>(1.0f), static_cast<__bf16>(1.0f)}, c, false);
+}
+__device__ __forceinline__ float add_pair(_Float16 a, _Float16 b, float c) {
+  return __builtin_amdgcn_fdot2(f16x2{a, b}, f16x2{static_cast<_Float16>(1.0f), static_cast<_Float16>(1.0f)}, c, false);
+}
+
 // The larger of a lane's value and that of the lane 32 on.
 __device__ __forceinline__ float other_half_max(float x) {
   const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -55,7 +63,7 @@ __device__ __forceinline__ int64_t first_row_tile(const AttnParams& p, int b) {
 struct RowTile {
   int b, row0, rows, token0, first;  // rows row0 .. of sequence b's rows; its first new row and position
   int held;
-  int64_t lo, hi;  // key tiles
+  int lo, hi;  // key tiles
 };
 
 template <int R>
@@ -73,16 +81,17 @@ __device__ __forceinline__ bool row_tile_of(const AttnParams& p, int64_t unit, R
   const int low = r.first + r.row0 / p.G, high = r.first + (r.row0 + r.rows - 1) / p.G;  // positions
   const int64_t end = p.causal && static_cast<int64_t>(high) + 1 < r.held ? static_cast<int64_t>(high) + 1 : r.held;
   const int64_t begin = p.window > 0 && low >= p.window ? low - p.window + 1 : 0;
-  r.lo = begin / kTile;
-  r.hi = end > 0 ? (end + kTile - 1) / kTile : 0;
+  r.lo = static_cast<int>(begin / kTile);
+  r.hi = end > 0 ? static_cast<int>((end + kTile - 1) / kTile) : 0;
   if (r.hi < r.lo) r.hi = r.lo;
   return true;
 }
 
-template <typename T, int D>
-__global__ __launch_bounds__(256, 2) void attn_prompt_kernel(const PromptParams pp) {
-  constexpr int R = kPromptRows, KP = D + 8, VP = kTile + 8, KS = D / 16, DT = D / 32;
-  constexpr int CHUNKS = kTile * D / 16 / 256;  // 16-byte pieces of K (and of V) for each thread
+template <typename T, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt_kernel(const PromptParams pp) {
+  constexpr int R = 32 * WAVES, KP = D + 8, VP = kTile + 8, KS = D / 16, DT = D / 32;
+  constexpr int THREADS = 64 * WAVES, CHUNKS = kTile * D / 16 / THREADS;  // 16-byte pieces of K (and of V) for each thread
+  constexpr int STEP = THREADS / 4;                                       // from one piece of a thread to the next
   typedef typename ActTraits<T>::vec8 vec8;
   __shared__ __attribute__((aligned(16))) T k_lds[2][kTile * KP];
   __shared__ __attribute__((aligned(16))) T v_lds[2][D * VP];
@@ -98,9 +107,9 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(const PromptParams 
   const int split = static_cast<int>(block % pp.splits);
   RowTile r;
   if (!row_tile_of<R>(p, unit, r)) return;
-  const int64_t share = (r.hi - r.lo + pp.splits - 1) / pp.splits;
-  const int64_t t_begin = r.lo + share * split < r.hi ? r.lo + share * split : r.hi;
-  const int64_t t_end = t_begin + share < r.hi ? t_begin + share : r.hi;
+  const int share = (r.hi - r.lo + pp.splits - 1) / pp.splits;
+  const int t_begin = r.lo + share * split < r.hi ? r.lo + share * split : r.hi;
+  const int t_end = t_begin + share < r.hi ? t_begin + share : r.hi;
 
   // this lane's row
   const int mine = 32 * wave + col, row = r.row0 + mine;
@@ -119,63 +128,65 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(const PromptParams 
       qf[i] = __builtin_bit_cast(vec8, v);
     }
   }
-  // tokens that all of the wave's rows attend, and that any of the workgroup's does
+  // tokens that all of the wave's rows attend; that all of the workgroup's do, and that any does
   const int w_rows = r.rows - 32 * wave < 32 ? r.rows - 32 * wave : 32;
   const int w_low = r.first + (r.row0 + 32 * wave) / p.G, w_high = r.first + (r.row0 + 32 * wave + w_rows - 1) / p.G;
   const int all_lo = p.window > 0 && w_high >= p.window ? w_high - p.window + 1 : 0;
   const int all_hi = w_rows <= 0 ? 0 : p.causal && w_low + 1 < r.held ? w_low + 1 : r.held;
   const int g_low = r.first + r.row0 / p.G, g_high = r.first + (r.row0 + r.rows - 1) / p.G;
+  const int every_lo = p.window > 0 && g_high >= p.window ? g_high - p.window + 1 : 0;
+  const int every_hi = p.causal && g_low + 1 < r.held ? g_low + 1 : r.held;
   const int any_lo = p.window > 0 && g_low >= p.window ? g_low - p.window + 1 : 0;
   const int any_hi = p.causal && g_high + 1 < r.held ? g_high + 1 : r.held;
 
   // A thread's pieces of a tile are of one chunk of 16 keys (so of one page): of K
   // one key's 16 values each, of V one value's 16 keys.
-  const int chunk = tid & 3, piece = tid >> 2;
-  const int64_t head_bytes = static_cast<int64_t>(p.seq.page) * D;
+  const int chunk = (tid >> 4) & 3, piece = (tid & 15) | (wave << 4);
+  const uint32_t page_bytes = static_cast<uint32_t>(p.Hk) * p.seq.page * D;
+  const uint8_t* k_base = p.k_cache + static_cast<uint32_t>(hk * p.seq.page * D + 16 * piece);
+  const uint8_t* v_base = p.v_cache + static_cast<uint32_t>(hk * p.seq.page * D + piece * p.seq.page);
   u32x4 kreg[CHUNKS], vreg[CHUNKS];
   uint32_t k_byte = 0, v_byte = 0;
-  int id = 0;  // page of the chunk in the registers, or -1
-  auto page_at = [&](int64_t t) { return t < t_end ? page_of(p.seq, r.b, static_cast<int>(t * kTile + 16 * chunk)) : -1; };
-  auto load = [&](int64_t t, int page_id) {
-    id = page_id;
+  struct Place {
+    int id;         // page of this thread's chunk in a tile, or -1
+    uint32_t slot;  // its first token's
+  };
+  auto place_of = [&](int t) {
     const uint32_t token_at = static_cast<uint32_t>(t * kTile + 16 * chunk);
-    const uint32_t slot = token_at - fdiv(token_at, p.seq.page_div) * static_cast<uint32_t>(p.seq.page);
-    const int64_t cell = static_cast<int64_t>(id < 0 ? 0 : id) * p.Hk + hk;
-    const uint8_t* k = p.k_cache + cell * head_bytes + static_cast<int64_t>(slot) * D + 16 * piece;
-    const uint8_t* v = p.v_cache + cell * head_bytes + slot + static_cast<int64_t>(piece) * p.seq.page;
+    const uint32_t index = fdiv(token_at, p.seq.page_div);
+    Place at{-1, token_at - index * static_cast<uint32_t>(p.seq.page)};
+    if (t < t_end && token_at < static_cast<uint32_t>(p.seq.capacity)) at.id = p.seq.table[r.b * p.seq.max_pages + index];
+    if (at.id < 0 || at.id >= p.seq.num_pages) at.id = -1;
+    return at;
+  };
+  int id = -1;  // of the chunk in the registers
+  auto load = [&](Place at) {
+    id = at.id;
+    const uint32_t known = id < 0 ? 0 : id;
+    const uint8_t* k = k_base + static_cast<uint64_t>(known) * page_bytes + at.slot * D;
+    const uint8_t* v = v_base + static_cast<uint64_t>(known) * page_bytes + at.slot;
+    const uint64_t cell = static_cast<uint64_t>(known) * static_cast<uint32_t>(p.Hk) + hk;
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-      kreg[i] = *reinterpret_cast<const u32x4*>(k + 1024 * i);
-      vreg[i] = *reinterpret_cast<const u32x4*>(v + static_cast<int64_t>(64 * i) * p.seq.page);
+      kreg[i] = *reinterpret_cast<const u32x4*>(k + 16 * STEP * i);
+      vreg[i] = *reinterpret_cast<const u32x4*>(v + STEP * i * p.seq.page);
     }
     k_byte = p.k_scale[cell];
     v_byte = p.v_scale[cell];
   };
-  auto store = [&](int64_t t, int buf) {
-#pragma unroll
-    for (int i = 0; i < CHUNKS; ++i) {
-      const int at = piece + 64 * i, key = at / (D / 16), part = at % (D / 16);  // key: of the chunk's 16
-      const int row = ((chunk >> 1) << 5) | ((key >> 2) << 3) | ((chunk & 1) << 2) | (key & 3);
-      vec8* to = reinterpret_cast<vec8*>(&k_lds[buf][row * KP + 16 * part]);
-      to[0] = ActTraits<T>::decode8_fp8(kreg[i].x, kreg[i].y);
-      to[1] = ActTraits<T>::decode8_fp8(kreg[i].z, kreg[i].w);
-    }
-    const int key0 = static_cast<int>(t * kTile) + 16 * chunk;
+  auto store = [&](int t, int buf) {
     const bool bad = v_byte > AttnTraits<T>::kMostV;
+    const uint64_t odd = __ballot(id < 0 || bad);  // (every wave has all four chunks)
     uint32_t byte = v_byte;
-    uint32_t nans[CHUNKS];
-    uint32_t any = 0;
-#pragma unroll
-    for (int i = 0; i < CHUNKS; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) any |= nan_codes(vreg[i][j]);
-    const bool edge = id < 0 || bad || key0 < any_lo || key0 + 16 > any_hi || any != 0;
-#pragma unroll
-    for (int i = 0; i < CHUNKS; ++i) nans[i] = 0;
-    if (edge) {
-      // values that nobody attends become 0, whatever they hold; those of a page
-      // whose scale is no number (or too large for T) NaN; NaN is noted apart
+    if (t * kTile < every_lo || t * kTile + kTile > every_hi || odd != 0) {
+      // Not every row attends all of the tile.  Values that none does become 0,
+      // whatever they hold; those of a page whose scale is no number (or too
+      // large for T) become NaN; and NaN is noted apart, with 0 in its place.
       asm volatile("" ::: "memory");
+      const int key0 = t * kTile + 16 * chunk;
+      uint32_t nans[CHUNKS], any = 0;
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i) nans[i] = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t keep = id < 0 ? 0u : byte_mask(any_lo - (key0 + 4 * j), any_hi - (key0 + 4 * j));
@@ -187,22 +198,33 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(const PromptParams 
         }
       }
       if (bad || id < 0) byte = 127;
+#pragma unroll
+      for (int i = 0; i < CHUNKS; ++i) {
+        nan_lds[buf][piece + STEP * i][chunk] = static_cast<uint16_t>(nans[i]);
+        any |= nans[i];
+      }
+      if (any != 0) nan_tile[buf] = t + 1;
     }
-    const float power = __uint_as_float((byte > AttnTraits<T>::kDown ? byte - AttnTraits<T>::kDown : 0u) << 23);
-    any = 0;
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
-      const int d = piece + 64 * i;
-      vec8* to = reinterpret_cast<vec8*>(&v_lds[buf][d * VP + 16 * chunk]);
+      const int at = piece + STEP * i, key = at / (D / 16), part = at % (D / 16);  // key: of the chunk's 16
+      const int row = ((chunk >> 1) << 5) | ((key >> 2) << 3) | ((chunk & 1) << 2) | (key & 3);
+      vec8* to = reinterpret_cast<vec8*>(&k_lds[buf][row * KP + 16 * part]);
+      to[0] = ActTraits<T>::decode8_fp8(kreg[i].x, kreg[i].y);
+      to[1] = ActTraits<T>::decode8_fp8(kreg[i].z, kreg[i].w);
+    }
+    const float power = __uint_as_float((byte > AttnTraits<T>::kDown ? byte - AttnTraits<T>::kDown : 0u) << 23);
+#pragma unroll
+    for (int i = 0; i < CHUNKS; ++i) {
+      vec8* to = reinterpret_cast<vec8*>(&v_lds[buf][(piece + STEP * i) * VP + 16 * chunk]);
       to[0] = decode8_power<T>(vreg[i].x, vreg[i].y, power);
       to[1] = decode8_power<T>(vreg[i].z, vreg[i].w, power);
-      nan_lds[buf][d][chunk] = static_cast<uint16_t>(nans[i]);
-      any |= nans[i];
     }
-    if (tid < 4) scale_lds[buf][tid] = id < 0 ? 0.0f : e8m0_to_f32(k_byte) * p.c;
-    const uint64_t absent = __ballot(id < 0);
-    if (tid == 0) absent_lds[buf] = static_cast<int>(absent & 15);
-    if (any != 0) nan_tile[buf] = static_cast<int>(t) + 1;
+    if (wave == 0 && (lane & 15) == 0) scale_lds[buf][chunk] = id < 0 ? 0.0f : e8m0_to_f32(k_byte) * p.c;
+    if (wave == 0) {
+      const uint64_t absent = __ballot(id < 0);
+      if (tid == 0) absent_lds[buf] = static_cast<int>((absent & 1) | (absent >> 15 & 2) | (absent >> 30 & 4) | (absent >> 45 & 8));
+    }
   };
 
   f32x16 acc[DT];
@@ -214,27 +236,26 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(const PromptParams 
 
   if (p.seq.capacity > 0 && t_begin < t_end) {
     if (tid < 2) nan_tile[tid] = 0;
-    load(t_begin, page_at(t_begin));
-    int next = page_at(t_begin + 1);
+    load(place_of(t_begin));
+    Place next = place_of(t_begin + 1);
     __syncthreads();
     store(t_begin, 0);
     __syncthreads();
     int buf = 0;
-    for (int64_t t = t_begin; t < t_end; ++t, buf ^= 1) {
-      const int after = page_at(t + 2);
-      if (t + 1 < t_end) load(t + 1, next);
+    for (int t = t_begin; t < t_end; ++t, buf ^= 1) {
+      const Place after = place_of(t + 2);
+      if (t + 1 < t_end) load(next);
       next = after;
-      const int key0 = static_cast<int>(t * kTile);
+      const int key0 = t * kTile;
       const T* ks = k_lds[buf] + col * KP + 8 * h;
       const T* vs = v_lds[buf] + col * VP + 16 * h;
       f32x16 s[2];
+      const f32x16 zero = {0.0f};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const f32x16 zero = {0.0f};
+      for (int k = 0; k < KS; ++k)  // (two chains: an MFMA does not wait for the one before)
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+        for (int i = 0; i < 2; ++i)
           s[i] = Mfma32<T>::run(*reinterpret_cast<const vec8*>(ks + 32 * i * KP + 16 * k), qf[k], k == 0 ? zero : s[i]);
-      }
       const int absent = absent_lds[buf];
       float factor[2] = {scale_lds[buf][h], scale_lds[buf][2 + h]};
       uint32_t seen = 0xffffffffu;
@@ -277,17 +298,19 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(const PromptParams 
       }
       const float base = AttnTraits<T>::kLift - (m > -INFINITY ? m : 0.0f);
       vec8 pf[4];
-      float sum[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float e = __builtin_amdgcn_exp2f(fmaf(s[i][j], factor[i], base));
-          sum[i] += e;
-          pf[2 * i + (j >> 3)][j & 7] = static_cast<T>(e);  // the one rounding between the products
-        }
-      l += sum[0] + sum[1];
-      if (nan_tile[buf] == static_cast<int>(t) + 1) {
+        for (int j = 0; j < 16; ++j)  // the one rounding between the products
+          pf[2 * i + (j >> 3)][j & 7] = static_cast<T>(__builtin_amdgcn_exp2f(fmaf(s[i][j], factor[i], base)));
+      // the sum is that of the rounded numerators, so a row's weights add up to one
+      float sum[2] = {l, 0.0f};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) sum[k & 1] = add_pair(pf[k][j], pf[k][j + 1], sum[k & 1]);
+      l = sum[0] + sum[1];
+      if (nan_tile[buf] == t + 1) {
         // 0 x NaN must not reach the rows that do not attend it: the NaN values
         // that each output attends are counted apart (they are 0 in v_lds)
         asm volatile("" ::: "memory");
@@ -310,9 +333,9 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(const PromptParams 
         }
       }
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+      for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int d = 0; d < DT; ++d)
           acc[d] = Mfma32<T>::run(*reinterpret_cast<const vec8*>(vs + 32 * d * VP + 32 * (k >> 1) + 8 * (k & 1)), pf[k], acc[d]);
       if (t + 1 < t_end) store(t + 1, buf ^ 1);
       __syncthreads();
@@ -345,9 +368,9 @@ __global__ __launch_bounds__(256, 2) void attn_prompt_kernel(const PromptParams 
 
 // Joins the parts of every row: D / 4 lanes for a row, a workgroup for a row
 // tile and key head.
-template <typename T, int D>
+template <typename T, int D, int R>
 __global__ __launch_bounds__(256) void attn_prompt_join_kernel(const PromptParams pp) {
-  constexpr int R = kPromptRows, LANES = D / 4, ROWS = 256 / LANES;
+  constexpr int LANES = D / 4, ROWS = 256 / LANES;
   const AttnParams& p = pp.a;
   const int64_t unit = blockIdx.x / p.Hk;
   const int hk = static_cast<int>(blockIdx.x - unit * p.Hk), lane = threadIdx.x % LANES;
@@ -369,12 +392,22 @@ __global__ __launch_bounds__(256) void attn_prompt_join_kernel(const PromptParam
   }
 }
 
-template <typename T, int D>
-int launch_t(const PromptParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((attn_prompt_kernel<T, D>), dim3(static_cast<uint32_t>(p.units * p.a.Hk * p.splits)), dim3(256), 0, s, p);
+template <typename T, int D, int WAVES>
+int launch_waves(PromptParams p, int64_t M, int64_t capacity, hipStream_t s) {
+  constexpr int R = 32 * WAVES;
+  p.units = attn_row_tiles_most(M, p.a.G, p.a.seq.B, R);
+  p.splits = static_cast<int32_t>(attn_prompt_splits(p.units * p.a.Hk, capacity));
+  hipLaunchKernelGGL((attn_prompt_kernel<T, D, WAVES>), dim3(static_cast<uint32_t>(p.units * p.a.Hk * p.splits)), dim3(64 * WAVES), 0, s, p);
   if (p.splits > 1)
-    hipLaunchKernelGGL((attn_prompt_join_kernel<T, D>), dim3(static_cast<uint32_t>(p.units * p.a.Hk)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((attn_prompt_join_kernel<T, D, R>), dim3(static_cast<uint32_t>(p.units * p.a.Hk)), dim3(256), 0, s, p);
   return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+template <typename T>
+int launch_t(const PromptParams& p, const AttentionArgs& a, hipStream_t s) {
+  const int64_t capacity = a.seq.max_pages * a.seq.page_size;
+  if (a.D == 64) return launch_waves<T, 64, 4>(p, a.M, capacity, s);
+  return launch_waves<T, 128, 4>(p, a.M, capacity, s);
 }
 
 }  // namespace
@@ -382,12 +415,9 @@ int launch_t(const PromptParams& p, hipStream_t s) {
 int launch_attention_prompt(const AttentionArgs& a) {
   PromptParams p;
   p.a = make_attn(a);
-  p.units = attn_row_tiles_most(a.M, a.Hq / a.Hk, a.seq.B);
-  p.splits = static_cast<int32_t>(attn_prompt_splits(p.units * a.Hk, a.seq.max_pages * a.seq.page_size));
   p.part = static_cast<float*>(a.work);
   hipStream_t s = static_cast<hipStream_t>(a.stream);
-  if (a.D == 128) return a.act == Act::BF16 ? launch_t<__bf16, 128>(p, s) : launch_t<_Float16, 128>(p, s);
-  return a.act == Act::BF16 ? launch_t<__bf16, 64>(p, s) : launch_t<_Float16, 64>(p, s);
+  return a.act == Act::BF16 ? launch_t<__bf16>(p, a, s) : launch_t<_Float16>(p, a, s);
 }
 
 }  // namespace fp4w

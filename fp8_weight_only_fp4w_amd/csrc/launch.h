@@ -339,14 +339,14 @@ int launch_attention_decode(const AttentionArgs& a);
 // parts of at least 8 key tiles, whose results are in the workspace.
 constexpr int kPromptRows = 128;
 constexpr int64_t kPromptWork = 1024;  // workgroups that are wanted
-inline int64_t attn_row_tiles_most(int64_t M, int64_t G, int64_t B) { return M * G / kPromptRows + B; }
+inline int64_t attn_row_tiles_most(int64_t M, int64_t G, int64_t B, int64_t rows) { return M * G / rows + B; }
 inline int64_t attn_prompt_splits(int64_t tiles, int64_t capacity) {
   const int64_t want = (kPromptWork + tiles - 1) / tiles, most = capacity / (8 * 64);
   const int64_t n = want < most ? want : most;
   return n < 1 ? 1 : n < 16 ? n : 16;
 }
 inline int64_t attn_prompt_workspace(int64_t M, int64_t G, int64_t B, int64_t Hk, int64_t D) {
-  const int64_t tiles = attn_row_tiles_most(M, G, B) * Hk, most = 2 * kPromptWork;  // tiles * splits < most where splits > 1
+  const int64_t tiles = attn_row_tiles_most(M, G, B, kPromptRows) * Hk, most = 2 * kPromptWork;  // tiles * splits < most where splits > 1
   return (16 * tiles < most ? 16 * tiles : most) * attn_part_floats(kPromptRows, D) * 4;
 }
 // as launch_attention_decode, for any max_new; the grid and the row tiles in
