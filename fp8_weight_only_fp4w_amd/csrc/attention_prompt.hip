@@ -39,14 +39,6 @@ struct Mfma32<_Float16> {
   __device__ __forceinline__ static f32x16 run(f16x8 a, f16x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
 };
 
-// c + a + b.
-__device__ __forceinline__ float add_pair(__bf16 a, __bf16 b, float c) {
-  return __builtin_amdgcn_fdot2_f32_bf16(bf16x2{a, b}, bf16x2{static_cast<__bf16>(1.0f), static_cast<__bf16>(1.0f)}, c, false);
-}
-__device__ __forceinline__ float add_pair(_Float16 a, _Float16 b, float c) {
-  return __builtin_amdgcn_fdot2(f16x2{a, b}, f16x2{static_cast<_Float16>(1.0f), static_cast<_Float16>(1.0f)}, c, false);
-}
-
 // The larger of a lane's value and that of the lane 32 on.
 __device__ __forceinline__ float other_half_max(float x) {
   const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -298,18 +290,16 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt_kernel(const Prompt
       }
       const float base = AttnTraits<T>::kLift - (m > -INFINITY ? m : 0.0f);
       vec8 pf[4];
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 16; ++j)  // the one rounding between the products
-          pf[2 * i + (j >> 3)][j & 7] = static_cast<T>(__builtin_amdgcn_exp2f(fmaf(s[i][j], factor[i], base)));
-      // the sum is that of the rounded numerators, so a row's weights add up to one
-      float sum[2] = {l, 0.0f};
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) sum[k & 1] = add_pair(pf[k][j], pf[k][j + 1], sum[k & 1]);
-      l = sum[0] + sum[1];
+        for (int j = 0; j < 16; ++j) {
+          const float e = __builtin_amdgcn_exp2f(fmaf(s[i][j], factor[i], base));
+          sum[j & 3] += e;
+          pf[2 * i + (j >> 3)][j & 7] = static_cast<T>(e);  // the one rounding between the products
+        }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (nan_tile[buf] == t + 1) {
         // 0 x NaN must not reach the rows that do not attend it: the NaN values
         // that each output attends are counted apart (they are 0 in v_lds)
