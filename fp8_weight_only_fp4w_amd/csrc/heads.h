@@ -161,6 +161,97 @@ __device__ __forceinline__ void head_to_lds(const T* x, int D, const T* weight, 
   __syncthreads();
 }
 
+// A head by D / 16 lanes (a power of two up to 64), 16 values a lane: two chunks
+// of 8, chosen so that both values of a pair are in one lane.  Lane t < dims / 16
+// has the rotated chunks t and t + dims / 16, the others two that are not rotated.
+struct LaneChunks {
+  int a, b;
+  bool rotated;
+};
+
+__device__ __forceinline__ LaneChunks lane_chunks(int t, int D, int dims) {
+  const int half = dims >> 4;
+  if (t < half) return LaneChunks{t, t + half, true};
+  const int u = (dims >> 3) + t - half;
+  return LaneChunks{u, u + ((D - dims) >> 4), false};
+}
+
+// cos and sin of a lane's eight pairs at a position (NaN for an unknown one).
+struct LaneAngles {
+  float c[8], s[8];
+  __device__ __forceinline__ void load(const Rope& r, const LaneChunks& at, int64_t position) {
+    if (!at.rotated) return;
+    const bool known = position >= 0 && position < r.rows;
+    const int64_t row = (known ? position : 0) * (r.dims >> 1);
+    const int first = r.interleaved ? 4 * at.a : 8 * at.a, second = r.interleaved ? 4 * at.b : first + 4;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const f32x4 cv = *reinterpret_cast<const f32x4*>(r.cos + row + (i ? second : first));
+      const f32x4 sv = *reinterpret_cast<const f32x4*>(r.sin + row + (i ? second : first));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        c[4 * i + j] = known ? cv[j] : NAN;
+        s[4 * i + j] = known ? sv[j] : NAN;
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+  const float x = fmaf(a, c, -(b * s));
+  b = fmaf(b, c, a * s);
+  a = x;
+}
+
+template <typename T>
+struct LaneHead {
+  float v[16];
+  __device__ __forceinline__ void load(const T* x, const LaneChunks& at) {
+    typedef typename ActTraits<T>::vec8 vec8;
+    const vec8 a = *reinterpret_cast<const vec8*>(x + 8 * at.a), b = *reinterpret_cast<const vec8*>(x + 8 * at.b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = static_cast<float>(a[i]);
+      v[8 + i] = static_cast<float>(b[i]);
+    }
+  }
+  // every lane of the head's calls it
+  template <int LANES>
+  __device__ __forceinline__ void norm(const T* weight, const LaneChunks& at, const Rope& r) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum = fmaf(v[i], v[i], sum);
+#pragma unroll
+    for (int off = LANES / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+    const float inv = 1.0f / sqrtf(sum / static_cast<float>(16 * LANES) + r.eps);
+    LaneHead<T> w;
+    w.load(weight, at);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= inv * (r.offset + w.v[i]);
+  }
+  __device__ __forceinline__ void rotate(const LaneAngles& g, const LaneChunks& at, const Rope& r) {
+    if (!at.rotated) return;
+    if (r.interleaved) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) turn(v[2 * i], v[2 * i + 1], g.c[i], g.s[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) turn(v[i], v[8 + i], g.c[i], g.s[i]);
+    }
+  }
+  __device__ __forceinline__ void store(T* y, const LaneChunks& at) const {
+    typedef typename ActTraits<T>::vec8 vec8;
+    vec8 a, b;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      a[i] = round_to<T>(v[i]);
+      b[i] = round_to<T>(v[8 + i]);
+    }
+    *reinterpret_cast<vec8*>(y + 8 * at.a) = a;
+    *reinterpret_cast<vec8*>(y + 8 * at.b) = b;
+  }
+};
+
 // Two values as E4M3 codes in the low 16 bits, to nearest even; an infinity or
 // NaN becomes the NaN code.  Finite values are within +-448.
 __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {

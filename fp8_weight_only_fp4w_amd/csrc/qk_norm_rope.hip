@@ -8,37 +8,12 @@
 
 #include <hip/hip_runtime.h>
 
-#include "heads.h"
+#include "qk_rows.h"
 
 namespace fp4w {
 namespace {
 
-struct QkParams {
-  const void* q;
-  const void* k;
-  void* q_out;
-  void* k_out;
-  int64_t q_stride, k_stride, q_out_stride, k_out_stride, M;
-  int32_t Hq, Hk, D;
-  const void* q_weight;
-  const void* k_weight;
-  Rope rope;
-  Seqs seq;        // seq.lens not null: positions from the sequences
-};
-
-// Position of row m, and whether the row is to be written.
-__device__ __forceinline__ bool row_position(const QkParams& p, int64_t m, int64_t* position) {
-  if (p.seq.lens != nullptr) {
-    if (m >= seq_start(p.seq, p.seq.B)) return false;
-    const int b = last_not_above(p.seq.B, m, [&](int i) { return seq_start(p.seq, i); });
-    const SeqSpan s = seq_span(p.seq, b);
-    *position = static_cast<int64_t>(s.len) - s.rows + (m - s.first_row);
-  } else {
-    *position = m;
-  }
-  if (p.rope.positions) *position = p.rope.positions[m];
-  return true;
-}
+constexpr int64_t kManyWaves = 8192;  // one for each of the GPU's places; beyond, a wave takes four passes of heads
 
 // Any D, alignment and stride: a wave per head, values through LDS.
 template <typename T>
@@ -74,8 +49,44 @@ __global__ __launch_bounds__(256) void qk_norm_rope_generic_kernel(const QkParam
   }
 }
 
+// D a power of two from 16 to 1024, everything in 16-byte pieces: `step` waves
+// for a row.
+template <typename T, int LANES, int AT_ONCE>
+__global__ __launch_bounds__(256) void qk_norm_rope_kernel(const QkParams p, int step, FastDiv by_step) {
+  const int64_t waves = p.M * step;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); u < waves; u += static_cast<int64_t>(gridDim.x) * 4) {
+    const int64_t m = waves <= 0x7fffffff ? fdiv(static_cast<uint32_t>(u), by_step) : u / step;
+    qk_row<T, LANES, AT_ONCE>(p, m, static_cast<int>(u - m * step), step);
+  }
+}
+
+template <typename T, int LANES>
+int launch_lanes(const QkParams& p, hipStream_t s) {
+  const int passes = (p.Hq + p.Hk + 64 / LANES - 1) / (64 / LANES);
+  const bool many = p.M * passes > kManyWaves;
+  const int step = many ? (passes + 3) / 4 : passes;
+  const int64_t blocks = (p.M * step + 3) / 4;
+  const dim3 grid(static_cast<uint32_t>(blocks < (1 << 20) ? blocks : 1 << 20));
+  if (many)
+    hipLaunchKernelGGL((qk_norm_rope_kernel<T, LANES, 4>), grid, dim3(256), 0, s, p, step, make_fastdiv(step));
+  else
+    hipLaunchKernelGGL((qk_norm_rope_kernel<T, LANES, 1>), grid, dim3(256), 0, s, p, step, make_fastdiv(step));
+  return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
 template <typename T>
 int launch_t(const QkParams& p, bool vec, hipStream_t s) {
+  if (vec) {
+    switch (p.D) {
+      case 16: return launch_lanes<T, 1>(p, s);
+      case 32: return launch_lanes<T, 2>(p, s);
+      case 64: return launch_lanes<T, 4>(p, s);
+      case 128: return launch_lanes<T, 8>(p, s);
+      case 256: return launch_lanes<T, 16>(p, s);
+      case 512: return launch_lanes<T, 32>(p, s);
+      case 1024: return launch_lanes<T, 64>(p, s);
+    }
+  }
   const int64_t blocks = (p.M * (p.Hq + p.Hk) + 3) / 4;
   const int grid = static_cast<int>(blocks < (1 << 20) ? blocks : 1 << 20);
   hipLaunchKernelGGL(qk_norm_rope_generic_kernel<T>, dim3(grid), dim3(256), 0, s, p);
