@@ -49,6 +49,7 @@ N and A's dtype.
 """
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -766,10 +767,13 @@ def _cache(cache: KVCache, heads: int, D: int, device: torch.device):
                          f"got {tuple(shape)} and {tuple(v.shape)}")
     if ks.shape != shape[:2] or vs.shape != shape[:2]:
         raise ValueError(f"the cache's scales must be [{shape[0]}, {heads}], got {tuple(ks.shape)} and {tuple(vs.shape)}")
-    for t, name, types in ((k, "k", _CODES), (v, "v", _CODES), (ks, "k_scale", _POWERS), (vs, "v_scale", _POWERS)):
-        if t.dtype not in types:
-            raise TypeError(f"the cache's {name} must be one of {types}, got {t.dtype}")
-        if not t.is_contiguous() or t.device != device:
+    if k.dtype not in _CODES or v.dtype not in _CODES:
+        raise TypeError(f"the cache's k and v must be one of {_CODES}, got {k.dtype} and {v.dtype}")
+    if ks.dtype not in _POWERS or vs.dtype not in _POWERS:
+        raise TypeError(f"the cache's scales must be one of {_POWERS}, got {ks.dtype} and {vs.dtype}")
+    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous() and k.device == device
+            and v.device == device and ks.device == device and vs.device == device):
+        for t, name in ((k, "k"), (v, "v"), (ks, "k_scale"), (vs, "v_scale")):
             _need(t, f"the cache's {name}", device)
     return shape[0], shape[2]
 
@@ -790,6 +794,16 @@ def _heads(t: torch.Tensor, name: str, M: int, D: int, dtype: torch.dtype, devic
     return H, (stride[0] if M > 1 else H * D)
 
 
+def _heads_out(out, name: str, like: torch.Tensor, M: int, H: int, D: int, dtype: torch.dtype, device: torch.device):
+    """(out, token stride): what is given, or a new tensor of like's shape (whose heads lie side by side)."""
+    if out is None:
+        return torch.empty_like(like, memory_format=torch.contiguous_format), H * D
+    n, stride = _heads(out, name, M, D, dtype, device)
+    if n != H:
+        raise ValueError(f"{name} must have {H} heads, got {n}")
+    return out, stride
+
+
 def _rope_args(dtype, device, M, D, q_weight, k_weight, weight_offset, eps, cos, sin, interleaved, positions):
     if q_weight is not None:
         _typed(q_weight, "q_weight", dtype, (D,), device)
@@ -797,13 +811,14 @@ def _rope_args(dtype, device, M, D, q_weight, k_weight, weight_offset, eps, cos,
         _typed(k_weight, "k_weight", dtype, (D,), device)
     rows = dims = 0
     if cos is not None or sin is not None:
-        if cos is None or sin is None or cos.dim() != 2 or not cos.numel():  # (no pointer to an empty table)
+        shape = None if cos is None else cos.shape
+        if shape is None or sin is None or len(shape) != 2 or not shape[0] or not shape[1]:  # (no pointer to an empty table)
             raise ValueError("cos and sin go together, each [positions, rotated values / 2] and not empty")
-        rows, dims = cos.shape[0], 2 * cos.shape[1]
+        rows, dims = shape[0], 2 * shape[1]
         if dims > D:
             raise ValueError(f"cos has {dims // 2} angles, heads of {D} have at most {D // 2}")
-        _typed(cos, "cos", torch.float32, cos.shape, device)
-        _typed(sin, "sin", torch.float32, cos.shape, device)
+        _typed(cos, "cos", torch.float32, shape, device)
+        _typed(sin, "sin", torch.float32, shape, device)
     if positions is not None:
         _typed(positions, "positions", torch.int32, (M,), device)
     return (_data(q_weight), _data(k_weight), weight_offset, eps, _data(cos), _data(sin), rows, dims, int(interleaved),
@@ -827,21 +842,13 @@ def fp4w_qk_norm_rope(q: torch.Tensor, k: torch.Tensor = None, q_weight: torch.T
     dtype, dev, (M, _, D) = q.dtype, q.device, q.shape
     code = _dtype_code(dtype)
     Hq, q_stride = _heads(q, "q", M, D, dtype, dev)
-    if q_out is None:
-        q_out = torch.empty((M, Hq, D), dtype=dtype, device=dev)
-    n, qo_stride = _heads(q_out, "q_out", M, D, dtype, dev)
+    q_out, qo_stride = _heads_out(q_out, "q_out", q, M, Hq, D, dtype, dev)
     Hk = k_stride = ko_stride = 0
     if k is not None:
         Hk, k_stride = _heads(k, "k", M, D, dtype, dev)
-        if k_out is None:
-            k_out = torch.empty((M, Hk, D), dtype=dtype, device=dev)
-        nk, ko_stride = _heads(k_out, "k_out", M, D, dtype, dev)
-    else:
-        if k_out is not None or k_weight is not None:
-            raise ValueError("k_out and k_weight need a k")
-        nk = 0
-    if n != Hq or nk != Hk:
-        raise ValueError("q_out and k_out must have the shapes of q and k")
+        k_out, ko_stride = _heads_out(k_out, "k_out", k, M, Hk, D, dtype, dev)
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight need a k")
     rope = _rope_args(dtype, dev, M, D, q_weight, k_weight, weight_offset, eps, cos, sin, interleaved, positions)
     _call(dev, lib.fp4w_qk_norm_rope, "fp4w_qk_norm_rope", q.data_ptr(), q_stride, Hq, _data(k), k_stride, Hk, M, D, *rope,
           q_out.data_ptr(), qo_stride, _data(k_out), ko_stride, code)
@@ -890,11 +897,7 @@ def fp8w_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, page_table:
     Hq = q_stride = qo_stride = 0
     if q is not None:
         Hq, q_stride = _heads(q, "q", M, D, dtype, dev)
-        if q_out is None:
-            q_out = torch.empty((M, Hq, D), dtype=dtype, device=dev)
-        nq, qo_stride = _heads(q_out, "q_out", M, D, dtype, dev)
-        if nq != Hq:
-            raise ValueError("q_out must have q's shape")
+        q_out, qo_stride = _heads_out(q_out, "q_out", q, M, Hq, D, dtype, dev)
     elif q_out is not None or q_weight is not None:
         raise ValueError("q_out and q_weight need a q")
     rope = _rope_args(dtype, dev, M, D, q_weight, k_weight, weight_offset, eps, cos, sin, interleaved, positions)
@@ -905,9 +908,14 @@ def fp8w_kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, page_table:
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
+def _attention_workspace(*sizes):
+    return int(load_library().fp8w_attention_workspace(*sizes))
+
+
 def fp8w_attention_workspace(M: int, Hq: int, Hk: int, D: int, B: int, max_new: int) -> int:
     """Bytes of workspace that fp8w_attention needs, however long the sequences are; enough for every smaller call too."""
-    n = int(load_library().fp8w_attention_workspace(M, Hq, Hk, D, B, max_new))
+    n = _attention_workspace(M, Hq, Hk, D, B, max_new)
     if n < 0:
         raise FP4WError(n, "fp8w_attention_workspace")
     return n
@@ -945,13 +953,13 @@ def fp8w_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, se
     if window < 0 or max_new < 0:
         raise ValueError("window and max_new must not be negative")
     if out is None:
-        out = torch.empty((M, Hq, D), dtype=dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _typed(out, "out", dtype, (M, Hq, D), dev)
     if lse is not None:
         _typed(lse, "lse", torch.float32, (M, Hq), dev)
     if workspace is None:
-        held = lib.fp8w_attention_workspace(M, Hq, Hk, D, B, max_new)
+        held = _attention_workspace(M, Hq, Hk, D, B, max_new)
         if held < 0:
             raise FP4WError(held, "fp8w_attention")
         if held:

@@ -156,15 +156,15 @@ __device__ __forceinline__ u32x2 codes8(const float* v, float inv) {
 // registers between the maximum and the codes.  Values go through LDS to lie
 // along the tokens.  The workgroups behind the pages' have the queries.
 template <typename T, int LANES, int THREADS, int PASSES>
-__global__ __launch_bounds__(THREADS) void kv_append_kernel(const AppendParams p, const QkParams qp, uint32_t units, FastDiv by_heads, int q_step) {
+__global__ __launch_bounds__(THREADS) void kv_append_kernel(const AppendParams p, const QkParams qp, uint32_t units, FastDiv by_heads, int q_passes) {
   constexpr int D = 16 * LANES, TOKENS = THREADS / LANES, WAVES = THREADS / 64;
   extern __shared__ uint32_t turned[];  // [D][page + 4] bytes
   __shared__ float tops[WAVES];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, t = tid % LANES, page = p.seq.page;
   const uint32_t cells = units * p.Hk;
   if (blockIdx.x >= 2 * cells) {
-    const uint32_t u = (blockIdx.x - 2 * cells) * WAVES + wave, m = u / q_step;
-    if (m < qp.M) qk_row<T, LANES, 1>(qp, m, static_cast<int>(u - m * q_step), q_step);
+    const uint32_t u = (blockIdx.x - 2 * cells) * WAVES + wave, m = u / q_passes;
+    if (m < qp.M) qk_row<T, LANES>(qp, m, static_cast<int>(u - m * q_passes));
     return;
   }
   const bool value = blockIdx.x >= cells;
@@ -289,12 +289,12 @@ __global__ __launch_bounds__(THREADS) void kv_append_kernel(const AppendParams p
 template <typename T, int LANES, int THREADS, int PASSES>
 int launch_pages(const AppendParams& p, const QkParams& qp, hipStream_t s) {
   const int64_t units = most_units(p.seq);
-  const int step = qp.Hq > 0 ? (qp.Hq + 64 / LANES - 1) / (64 / LANES) : 1;  // waves of a row's queries
-  const int64_t q_blocks = qp.Hq > 0 ? (qp.M * step + THREADS / 64 - 1) / (THREADS / 64) : 0, blocks = 2 * units * p.Hk + q_blocks;
-  if (blocks * THREADS >= (int64_t(1) << 32) || qp.M * step >= (int64_t(1) << 32)) return 1;
+  const int passes = qp.Hq > 0 ? (qp.Hq + 64 / LANES - 1) / (64 / LANES) : 1;  // waves of a row's queries
+  const int64_t q_blocks = qp.Hq > 0 ? (qp.M * passes + THREADS / 64 - 1) / (THREADS / 64) : 0, blocks = 2 * units * p.Hk + q_blocks;
+  if (blocks * THREADS >= (int64_t(1) << 32) || qp.M * passes >= (int64_t(1) << 32)) return 1;
   const int lds = p.seq.starts ? 16 * LANES * (p.seq.page + 4) : 0;
   hipLaunchKernelGGL((kv_append_kernel<T, LANES, THREADS, PASSES>), dim3(static_cast<uint32_t>(blocks)), dim3(THREADS), lds, s, p, qp,
-                     static_cast<uint32_t>(units), make_fastdiv(static_cast<uint32_t>(p.Hk)), step);
+                     static_cast<uint32_t>(units), make_fastdiv(static_cast<uint32_t>(p.Hk)), passes);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

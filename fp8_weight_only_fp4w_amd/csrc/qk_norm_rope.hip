@@ -13,8 +13,6 @@
 namespace fp4w {
 namespace {
 
-constexpr int64_t kManyWaves = 8192;  // one for each of the GPU's places; beyond, a wave takes four passes of heads
-
 // Any D, alignment and stride: a wave per head, values through LDS.
 template <typename T>
 __global__ __launch_bounds__(256) void qk_norm_rope_generic_kernel(const QkParams p) {
@@ -49,28 +47,23 @@ __global__ __launch_bounds__(256) void qk_norm_rope_generic_kernel(const QkParam
   }
 }
 
-// D a power of two from 16 to 1024, everything in 16-byte pieces: `step` waves
+// D a power of two from 16 to 1024, everything in 16-byte pieces: `passes` waves
 // for a row.
-template <typename T, int LANES, int AT_ONCE>
-__global__ __launch_bounds__(256) void qk_norm_rope_kernel(const QkParams p, int step, FastDiv by_step) {
-  const int64_t waves = p.M * step;
+template <typename T, int LANES>
+__global__ __launch_bounds__(256) void qk_norm_rope_kernel(const QkParams p, int passes, FastDiv by_passes) {
+  const int64_t waves = p.M * passes;
   for (int64_t u = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); u < waves; u += static_cast<int64_t>(gridDim.x) * 4) {
-    const int64_t m = waves <= 0x7fffffff ? fdiv(static_cast<uint32_t>(u), by_step) : u / step;
-    qk_row<T, LANES, AT_ONCE>(p, m, static_cast<int>(u - m * step), step);
+    const int64_t m = waves <= 0x7fffffff ? fdiv(static_cast<uint32_t>(u), by_passes) : u / passes;
+    qk_row<T, LANES>(p, m, static_cast<int>(u - m * passes));
   }
 }
 
 template <typename T, int LANES>
 int launch_lanes(const QkParams& p, hipStream_t s) {
   const int passes = (p.Hq + p.Hk + 64 / LANES - 1) / (64 / LANES);
-  const bool many = p.M * passes > kManyWaves;
-  const int step = many ? (passes + 3) / 4 : passes;
-  const int64_t blocks = (p.M * step + 3) / 4;
+  const int64_t blocks = (p.M * passes + 3) / 4;
   const dim3 grid(static_cast<uint32_t>(blocks < (1 << 20) ? blocks : 1 << 20));
-  if (many)
-    hipLaunchKernelGGL((qk_norm_rope_kernel<T, LANES, 4>), grid, dim3(256), 0, s, p, step, make_fastdiv(step));
-  else
-    hipLaunchKernelGGL((qk_norm_rope_kernel<T, LANES, 1>), grid, dim3(256), 0, s, p, step, make_fastdiv(step));
+  hipLaunchKernelGGL((qk_norm_rope_kernel<T, LANES>), grid, dim3(256), 0, s, p, passes, make_fastdiv(passes));
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -33,40 +33,27 @@ __device__ __forceinline__ bool row_position(const QkParams& p, int64_t m, int64
   return true;
 }
 
-// A wave has one row's heads first, first + step, ... (in passes of 64 / LANES
-// heads, AT_ONCE passes loaded together), LANES = D / 16 lanes a head.  The
-// row's position and angles are looked up once.
-template <typename T, int LANES, int AT_ONCE>
-__device__ __forceinline__ void qk_row(const QkParams& p, int64_t m, int first, int step) {
-  constexpr int PASS = 64 / LANES;
-  const int lane = threadIdx.x & 63, t = lane % LANES, sub = lane / LANES, heads = p.Hq + p.Hk;
+// A wave has 64 / LANES heads of one row, LANES = D / 16 lanes a head: those of
+// `pass`.  (Several passes a wave, to look up position and angles once, are
+// slower: 51 to 59 us against 48 for 8192 rows of 48 heads of 128, for want of
+// waves.)
+template <typename T, int LANES>
+__device__ __forceinline__ void qk_row(const QkParams& p, int64_t m, int pass) {
+  const int lane = threadIdx.x & 63, h = pass * (64 / LANES) + lane / LANES;
   int64_t position = 0;
-  if (!row_position(p, m, &position)) return;
-  const LaneChunks at = lane_chunks(t, 16 * LANES, p.rope.dims);
+  if (!row_position(p, m, &position) || h >= p.Hq + p.Hk) return;
+  const LaneChunks at = lane_chunks(lane % LANES, 16 * LANES, p.rope.dims);
+  const bool query = h < p.Hq;
+  const int64_t head = static_cast<int64_t>(query ? h : h - p.Hq) * (16 * LANES);
+  const T* x = static_cast<const T*>(query ? p.q : p.k) + m * (query ? p.q_stride : p.k_stride) + head;
+  const T* weight = static_cast<const T*>(query ? p.q_weight : p.k_weight);
+  LaneHead<T> v;
+  v.load(x, at);
   LaneAngles angles;
   if (p.rope.cos) angles.load(p.rope, at, position);
-  const T* q = static_cast<const T*>(p.q) + m * p.q_stride;
-  const T* k = static_cast<const T*>(p.k) + m * p.k_stride;
-  T* q_out = static_cast<T*>(p.q_out) + m * p.q_out_stride;
-  T* k_out = static_cast<T*>(p.k_out) + m * p.k_out_stride;
-  for (int pass = first; pass * PASS < heads; pass += step * AT_ONCE) {
-    LaneHead<T> x[AT_ONCE];
-#pragma unroll
-    for (int i = 0; i < AT_ONCE; ++i) {
-      const int h = (pass + i * step) * PASS + sub;
-      if (h < heads) x[i].load(h < p.Hq ? q + h * (16 * LANES) : k + (h - p.Hq) * (16 * LANES), at);
-    }
-#pragma unroll
-    for (int i = 0; i < AT_ONCE; ++i) {
-      const int h = (pass + i * step) * PASS + sub;
-      if (h < heads) {  // the same on every lane of a head
-        const T* weight = static_cast<const T*>(h < p.Hq ? p.q_weight : p.k_weight);
-        if (weight) x[i].template norm<LANES>(weight, at, p.rope);
-        if (p.rope.cos) x[i].rotate(angles, at, p.rope);
-        x[i].store(h < p.Hq ? q_out + h * (16 * LANES) : k_out + (h - p.Hq) * (16 * LANES), at);
-      }
-    }
-  }
+  if (weight) v.template norm<LANES>(weight, at, p.rope);  // the same on every lane of a head
+  if (p.rope.cos) v.rotate(angles, at, p.rope);
+  v.store(static_cast<T*>(query ? p.q_out : p.k_out) + m * (query ? p.q_out_stride : p.k_out_stride) + head, at);
 }
 
 }  // namespace fp4w
