@@ -37,7 +37,7 @@ namespace fp4w {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int64_t kWideJoinRows = 1024;  // up to so many rows, the join takes 256 threads for each
+constexpr int64_t kWideJoinRows = 128;  // up to so many rows, the join takes 1024 threads for each
 
 struct DecodeParams {
   AttnParams a;
@@ -178,42 +178,50 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
     for (int d = 0; d < DT; ++d) acc[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     // pages of this lane's 16 keys as rows of a tile of K (chunk col / 4) and as keys of V (chunk g)
-    auto page_at = [&](int t, int chunk) {
-      return t < t_end ? page_of(p.a.seq, b, (lo_tile + t) * kTile + 16 * chunk) : -1;
+    struct Place {
+      int id;         // -1: none
+      uint32_t slot;  // of the chunk's first token
     };
-    auto slot_at = [&](int t, int chunk) {
-      const uint32_t token = static_cast<uint32_t>((lo_tile + t) * kTile + 16 * chunk);
-      return static_cast<int>(token - fdiv(token, p.a.seq.page_div) * static_cast<uint32_t>(p.a.seq.page));
+    const int32_t* pages = p.a.seq.table + b * p.a.seq.max_pages;
+    auto place_of = [&](int t, int chunk) {
+      Place at;
+      at.id = page_ahead(p.a.seq, pages, (lo_tile + t) * kTile + 16 * chunk, t < t_end, &at.slot);
+      return at;
     };
     u32x4 kreg[4][KL], vreg[DT];
     uint32_t ks = 127, vs = 127;
-    auto load_k = [&](int t, int id_k, int id_v) {
-      const uint8_t* k = p.a.k_cache + (static_cast<int64_t>(id_k < 0 ? 0 : id_k) * p.a.Hk + hk) * head_bytes +
-                         static_cast<int64_t>(slot_at(t, col >> 2) + (col & 3)) * D + 16 * g;
+    auto load_k = [&](Place at_k, Place at_v) {
+      const uint8_t* k = p.a.k_cache + (static_cast<int64_t>(at_k.id < 0 ? 0 : at_k.id) * p.a.Hk + hk) * head_bytes +
+                         static_cast<int64_t>(at_k.slot + (col & 3)) * D + 16 * g;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < KL; ++j) kreg[i][j] = load_codes<RT == 1>(k + 4 * i * D + 64 * j);
-      const int64_t cell = static_cast<int64_t>(id_v < 0 ? 0 : id_v) * p.a.Hk + hk;
+      const int64_t cell = static_cast<int64_t>(at_v.id < 0 ? 0 : at_v.id) * p.a.Hk + hk;
       ks = p.a.k_scale[cell];
       vs = p.a.v_scale[cell];
     };
-    auto load_v = [&](int t, int id_v) {
-      const uint8_t* v = p.a.v_cache + (static_cast<int64_t>(id_v < 0 ? 0 : id_v) * p.a.Hk + hk) * head_bytes +
-                         static_cast<int64_t>(col) * p.a.seq.page + slot_at(t, g);
+    auto load_v = [&](Place at) {
+      const uint8_t* v = p.a.v_cache + (static_cast<int64_t>(at.id < 0 ? 0 : at.id) * p.a.Hk + hk) * head_bytes +
+                         static_cast<int64_t>(col) * p.a.seq.page + at.slot;
 #pragma unroll
       for (int d = 0; d < DT; ++d) vreg[d] = load_codes<RT == 1>(v + static_cast<int64_t>(16 * d) * p.a.seq.page);
     };
 
-    // (without pages there is nothing to load, and no key to attend)
+    // Loads run ahead by a tile, and past the last one they go on at page 0: a
+    // branch around them would make the compiler wait for all loads in flight
+    // wherever it waits for any (3.5 us a tile instead of about 1.5).
+    // (Without pages there is nothing to load, and no key to attend.)
     int t = t_begin;
     if (p.a.seq.capacity > 0 && t < t_end) {
-      int id_k = page_at(t, col >> 2), id_v = page_at(t, g);
-      load_k(t, id_k, id_v);
-      load_v(t, id_v);
-      int next_k = page_at(t + 1, col >> 2), next_v = page_at(t + 1, g);
+      Place next_k = place_of(t, col >> 2), next_v = place_of(t, g);
+      int id_v = next_v.id;
+      load_k(next_k, next_v);
+      load_v(next_v);
+      next_k = place_of(t + 1, col >> 2);
+      next_v = place_of(t + 1, g);
       for (; t < t_end; ++t) {
-        const int after_k = page_at(t + 2, col >> 2), after_v = page_at(t + 2, g);
+        const Place after_k = place_of(t + 2, col >> 2), after_v = place_of(t + 2, g);
         f32x4 s[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -226,7 +234,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
         }
         const float factor = e8m0_to_f32(ks) * p.a.c;
         uint32_t vs_now = vs;
-        if (t + 1 < t_end) load_k(t + 1, next_k, next_v);
+        load_k(next_k, next_v);
 
         const int key0 = (lo_tile + t) * kTile;
         const int my0 = key0 + 16 * g;  // this lane's 16 keys
@@ -317,8 +325,8 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
           acc[d] = ActTraits<T>::mfma(decode8_power<T>(vreg[d].x, vreg[d].y, power), pf[0], acc[d]);
           acc[d] = ActTraits<T>::mfma(decode8_power<T>(vreg[d].z, vreg[d].w, power), pf[1], acc[d]);
         }
-        if (t + 1 < t_end) load_v(t + 1, next_v);
-        id_v = next_v;
+        load_v(next_v);
+        id_v = next_v.id;
         next_k = after_k;
         next_v = after_v;
       }
@@ -348,10 +356,11 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
 }
 
 // Joins the partial results of the sequences that lie in several shares: THREADS
-// threads for a row of a head, D / 4 of them for one partial result.
-template <typename T, int D, int THREADS>
+// threads for a row of a head, D / 4 of them for one partial result, AT_ONCE
+// results of each loaded together.
+template <typename T, int D, int THREADS, int AT_ONCE>
 __global__ __launch_bounds__(THREADS) void attn_join_kernel(const DecodeParams p) {
-  constexpr int LANES = D / 4, GROUPS = THREADS / LANES, AT_ONCE = 4;
+  constexpr int LANES = D / 4, GROUPS = THREADS / LANES;
   __shared__ float red_m[GROUPS], red_l[GROUPS];
   __shared__ f32x4 red_o[GROUPS][LANES];
   const int tid = threadIdx.x, group = tid / LANES, lane = tid % LANES;
@@ -383,15 +392,20 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(const DecodeParams p
 #pragma unroll
     for (int j = 0; j < AT_ONCE; ++j) join(m, l, o, pm[j], pl[j], po[j]);
   }
-  if (lane == 0) {
-    red_m[group] = m;
-    red_l[group] = l;
-  }
-  red_o[group][lane] = o;
-  __syncthreads();
-  if (group != 0) return;
+  // pairwise, so that the order does not hang on how many there are
 #pragma unroll
-  for (int v = 1; v < GROUPS; ++v) join(m, l, o, red_m[v], red_l[v], red_o[v][lane]);
+  for (int half = GROUPS / 2; half > 0; half >>= 1) {
+    if (group >= half && group < 2 * half) {
+      if (lane == 0) {
+        red_m[group] = m;
+        red_l[group] = l;
+      }
+      red_o[group][lane] = o;
+    }
+    __syncthreads();
+    if (group < half) join(m, l, o, red_m[group + half], red_l[group + half], red_o[group + half][lane]);
+  }
+  if (group != 0) return;
   store_quad<T>(p.a, row * p.a.Hq + h, D, 4 * lane, m, l, o);
   if (lane == 0) store_lse<T>(p.a, row * p.a.Hq + h, m, l);
 }
@@ -401,10 +415,14 @@ int launch_rows(DecodeParams p, int64_t join_rows, hipStream_t s) {
   p.W = attn_groups(p.a.Hk) * (kWaves / RT);
   hipLaunchKernelGGL((attn_decode_kernel<T, D, RT>), dim3(attn_groups(p.a.Hk) * p.a.Hk), dim3(256), 0, s, p);
   const dim3 grid(static_cast<uint32_t>(join_rows * p.a.Hq));
-  if (join_rows * p.a.Hq <= kWideJoinRows)
-    hipLaunchKernelGGL((attn_join_kernel<T, D, 256>), grid, dim3(256), 0, s, p);
+  // few rows may have many partial results each, many rows have few
+  const int64_t rows = join_rows * p.a.Hq, most = p.a.seq.capacity / kTile;
+  if (rows <= kWideJoinRows && most > 64)
+    hipLaunchKernelGGL((attn_join_kernel<T, D, 1024, 8>), grid, dim3(1024), 0, s, p);
+  else if (rows <= 8 * kWideJoinRows)
+    hipLaunchKernelGGL((attn_join_kernel<T, D, 256, 4>), grid, dim3(256), 0, s, p);
   else
-    hipLaunchKernelGGL((attn_join_kernel<T, D, 64>), grid, dim3(64), 0, s, p);
+    hipLaunchKernelGGL((attn_join_kernel<T, D, 64, 4>), grid, dim3(64), 0, s, p);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -80,7 +80,7 @@ __device__ __forceinline__ bool row_tile_of(const AttnParams& p, int64_t unit, R
 }
 
 template <typename T, int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt_kernel(const PromptParams pp) {
+__global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kernel(const PromptParams pp) {
   constexpr int R = 32 * WAVES, KP = D + 8, VP = kTile + 8, KS = D / 16, DT = D / 32;
   constexpr int THREADS = 64 * WAVES, CHUNKS = kTile * D / 16 / THREADS;  // 16-byte pieces of K (and of V) for each thread
   constexpr int STEP = THREADS / 4;                                       // from one piece of a thread to the next
@@ -143,12 +143,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt_kernel(const Prompt
     int id;         // page of this thread's chunk in a tile, or -1
     uint32_t slot;  // its first token's
   };
+  const int32_t* pages = p.seq.table + r.b * p.seq.max_pages;
   auto place_of = [&](int t) {
-    const uint32_t token_at = static_cast<uint32_t>(t * kTile + 16 * chunk);
-    const uint32_t index = fdiv(token_at, p.seq.page_div);
-    Place at{-1, token_at - index * static_cast<uint32_t>(p.seq.page)};
-    if (t < t_end && token_at < static_cast<uint32_t>(p.seq.capacity)) at.id = p.seq.table[r.b * p.seq.max_pages + index];
-    if (at.id < 0 || at.id >= p.seq.num_pages) at.id = -1;
+    Place at;
+    at.id = page_ahead(p.seq, pages, t * kTile + 16 * chunk, t < t_end, &at.slot);
     return at;
   };
   int id = -1;  // of the chunk in the registers
@@ -166,7 +164,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt_kernel(const Prompt
     k_byte = p.k_scale[cell];
     v_byte = p.v_scale[cell];
   };
-  auto store = [&](int t, int buf) {
+  float power = 1.0f;  // of the values in the registers
+  // What the rows of a tile's edge, absent pages and odd scales need, for the
+  // tile in the registers, which goes to buffer buf.
+  auto prepare = [&](int t, int buf) {
     const bool bad = v_byte > AttnTraits<T>::kMostV;
     const uint64_t odd = __ballot(id < 0 || bad);  // (every wave has all four chunks)
     uint32_t byte = v_byte;
@@ -197,6 +198,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt_kernel(const Prompt
       }
       if (any != 0) nan_tile[buf] = t + 1;
     }
+    power = __uint_as_float((byte > AttnTraits<T>::kDown ? byte - AttnTraits<T>::kDown : 0u) << 23);
+    if (wave == 0) {
+      if ((lane & 15) == 0) scale_lds[buf][chunk] = id < 0 ? 0.0f : e8m0_to_f32(k_byte) * p.c;
+      const uint64_t absent = __ballot(id < 0);
+      if (tid == 0) absent_lds[buf] = static_cast<int>((absent & 1) | (absent >> 15 & 2) | (absent >> 30 & 4) | (absent >> 45 & 8));
+    }
+  };
+  auto convert = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
       const int at = piece + STEP * i, key = at / (D / 16), part = at % (D / 16);  // key: of the chunk's 16
@@ -205,17 +214,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt_kernel(const Prompt
       to[0] = ActTraits<T>::decode8_fp8(kreg[i].x, kreg[i].y);
       to[1] = ActTraits<T>::decode8_fp8(kreg[i].z, kreg[i].w);
     }
-    const float power = __uint_as_float((byte > AttnTraits<T>::kDown ? byte - AttnTraits<T>::kDown : 0u) << 23);
 #pragma unroll
     for (int i = 0; i < CHUNKS; ++i) {
       vec8* to = reinterpret_cast<vec8*>(&v_lds[buf][(piece + STEP * i) * VP + 16 * chunk]);
       to[0] = decode8_power<T>(vreg[i].x, vreg[i].y, power);
       to[1] = decode8_power<T>(vreg[i].z, vreg[i].w, power);
-    }
-    if (wave == 0 && (lane & 15) == 0) scale_lds[buf][chunk] = id < 0 ? 0.0f : e8m0_to_f32(k_byte) * p.c;
-    if (wave == 0) {
-      const uint64_t absent = __ballot(id < 0);
-      if (tid == 0) absent_lds[buf] = static_cast<int>((absent & 1) | (absent >> 15 & 2) | (absent >> 30 & 4) | (absent >> 45 & 8));
     }
   };
 
@@ -231,13 +234,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt_kernel(const Prompt
     load(place_of(t_begin));
     Place next = place_of(t_begin + 1);
     __syncthreads();
-    store(t_begin, 0);
+    prepare(t_begin, 0);
+    convert(0);
+    load(next);
+    next = place_of(t_begin + 2);
     __syncthreads();
     int buf = 0;
     for (int t = t_begin; t < t_end; ++t, buf ^= 1) {
-      const Place after = place_of(t + 2);
-      if (t + 1 < t_end) load(next);
-      next = after;
+      if (t + 1 < t_end) prepare(t + 1, buf ^ 1);
       const int key0 = t * kTile;
       const T* ks = k_lds[buf] + col * KP + 8 * h;
       const T* vs = v_lds[buf] + col * VP + 16 * h;
@@ -248,6 +252,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt_kernel(const Prompt
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           s[i] = Mfma32<T>::run(*reinterpret_cast<const vec8*>(ks + 32 * i * KP + 16 * k), qf[k], k == 0 ? zero : s[i]);
+      // (behind the last tile: once more what is there already, and page 0; a
+      // branch would make the compiler wait for newer loads too)
+      convert(buf ^ 1);
+      load(next);
+      next = place_of(t + 3);
       const int absent = absent_lds[buf];
       float factor[2] = {scale_lds[buf][h], scale_lds[buf][2 + h]};
       uint32_t seen = 0xffffffffu;
@@ -327,7 +336,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void attn_prompt_kernel(const Prompt
 #pragma unroll
         for (int d = 0; d < DT; ++d)
           acc[d] = Mfma32<T>::run(*reinterpret_cast<const vec8*>(vs + 32 * d * VP + 32 * (k >> 1) + 8 * (k & 1)), pf[k], acc[d]);
-      if (t + 1 < t_end) store(t + 1, buf ^ 1);
       __syncthreads();
     }
   }

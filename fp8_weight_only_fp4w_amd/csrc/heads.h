@@ -86,6 +86,17 @@ __device__ __forceinline__ int page_of(const Seqs& s, int b, int t) {
   return id >= 0 && id < s.num_pages ? id : -1;
 }
 
+// The same for t >= 0 where there are pages, without a branch: a load under one
+// makes the compiler wait for every load in flight where it waits for an older
+// one.  *slot: t % page.
+__device__ __forceinline__ int page_ahead(const Seqs& s, const int32_t* row, int t, bool wanted, uint32_t* slot) {
+  const bool inside = wanted && t < s.capacity;
+  const uint32_t at = vgpr(inside ? static_cast<uint32_t>(t) : 0u), index = fdiv(at, s.page_div);
+  *slot = at - index * static_cast<uint32_t>(s.page);
+  const int id = row[index];
+  return inside && id >= 0 && id < s.num_pages ? id : -1;
+}
+
 // The largest b in [0, B) with at(b) <= u, for a function that does not fall
 // and at(0) <= u; every lane of the wave calls it with the same u.  64 probes
 // at a time: two rounds of loads up to B = 4096.
