@@ -241,7 +241,7 @@ int fp8w_attention_ex(const void* q, int64_t q_stride, int64_t M, int64_t Hq, in
   const bool decode = fast && max_new * (Hq / Hk) <= kDecodeRows && M * Hq < (1 << 25) &&
                       std::min<int64_t>(B, fp4w::kSeqsPerLaunch) * (max_pages * page_size / 64 + 2) < kMax32;
   const bool prompt = fast && max_pages * page_size < kMax32 - 128 && mul_ok(Hk, page_size) && Hk * page_size * D < kMax32 &&
-                      (fp4w::attn_row_tiles_most(M, Hq / Hk, B, fp4w::kPromptRows) * Hk + 2 * fp4w::kPromptWork) * 512 < 2 * kMax32;
+                      (fp4w::attn_row_tiles_most(M, Hq / Hk, B) * Hk + 2 * fp4w::kPromptWork) * 256 < 2 * kMax32;
   if ((path == FP4W_PATH_ATTN_DECODE && !decode) || (path == FP4W_PATH_ATTN_PROMPT && !prompt)) return FP4W_ERR_PATH;
   const AttentionArgs a{q, q_stride, M, Hq, Hk, D, max_new, seq, k_cache, k_scale, v_cache, v_scale, scale, causal != 0,
                         window, workspace, Y, lse, static_cast<Act>(dtype), stream};

@@ -334,19 +334,24 @@ inline int64_t attn_decode_workspace(int64_t max_new, int64_t Hk, int64_t G, int
 // D 64 or 128, page_size % 16 == 0, max_new * Hq / Hk <= 64; q, the cache's
 // codes, Y and work 16-byte aligned, q_stride % 8 == 0.
 int launch_attention_decode(const AttentionArgs& a);
-// The prompt kernel: row tiles of kPromptRows rows of a sequence and key head;
-// where they leave compute units idle, a tile's keys are cut into up to 16
-// parts of at least 8 key tiles, whose results are in the workspace.
+// The prompt kernel: row tiles of kPromptRows rows of a sequence and key head.
+// Where there are fewer than the GPU has places for (two workgroups a compute
+// unit), their keys are cut into up to 16 parts of at least 8 key tiles, whose
+// results are in the workspace.  A part costs 133 KB of traffic for D = 128:
+// with 784 row tiles, two parts each took 85 us and whole ones 56; with 360 of
+// some 240 key tiles, one to three parts took 420, 353 and 329 us.
 constexpr int kPromptRows = 128;
-constexpr int64_t kPromptWork = 1024;  // workgroups that are wanted
-inline int64_t attn_row_tiles_most(int64_t M, int64_t G, int64_t B, int64_t rows) { return M * G / rows + B; }
+constexpr int64_t kPromptPlaces = 512, kPromptWork = 768;  // workgroups that are wanted where there are too few
+inline int64_t attn_row_tiles_most(int64_t M, int64_t G, int64_t B) { return M * G / kPromptRows + B; }
 inline int64_t attn_prompt_splits(int64_t tiles, int64_t capacity) {
+  if (tiles >= kPromptPlaces) return 1;
   const int64_t want = (kPromptWork + tiles - 1) / tiles, most = capacity / (8 * 64);
   const int64_t n = want < most ? want : most;
   return n < 1 ? 1 : n < 16 ? n : 16;
 }
 inline int64_t attn_prompt_workspace(int64_t M, int64_t G, int64_t B, int64_t Hk, int64_t D) {
-  const int64_t tiles = attn_row_tiles_most(M, G, B, kPromptRows) * Hk, most = 2 * kPromptWork;  // tiles * splits < most where splits > 1
+  const int64_t tiles = attn_row_tiles_most(M, G, B) * Hk;
+  const int64_t most = kPromptWork + kPromptPlaces;  // tiles * splits is less where there are several
   return (16 * tiles < most ? 16 * tiles : most) * attn_part_floats(kPromptRows, D) * 4;
 }
 // as launch_attention_decode, for any max_new; the grid and the row tiles in
