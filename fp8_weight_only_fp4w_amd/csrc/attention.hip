@@ -19,15 +19,20 @@
 //     scale of K and one of V for a tile: K's is a factor of the scores, V's
 //     the exponent operand of the conversion to T.
 // The rows of a workgroup are the query heads of one key head, times the new
-// tokens: 16, 32 or 64 of them.  Four waves take the tiles of their workgroup
-// in turn, each with a softmax of its own, and join them in LDS.
+// tokens: up to 64 of them.
 //
 // The tiles of all sequences, one after the other, are cut into equal shares,
-// one for each workgroup of a key head: lengths may differ as they like, the
-// host need not know them, and the workspace does not grow with them.  A
-// sequence that lies in several shares is joined by a second kernel from the
-// shares' partial results, in order, so a row's result does not depend on the
-// order of work.
+// one for each wave (or each group of waves with other rows of the same share):
+// lengths may differ as they like, the host need not know them, and the
+// workspace does not grow with them.  A sequence that lies in several shares is
+// joined by a second kernel from the shares' partial results, in order, so a
+// row's result does not depend on the order of work.
+//
+// Measured with BF16, 8 key heads of 128, both kernels: a token after 131000
+// (268 MB of cache) 56 us, 4.8 TB/s; 64 tokens of 64 sequences of up to 8192
+// (533 MB) 105 us, 5.1 TB/s, what a large copy reaches; 7 sequences of up to 260
+// tokens 11 us, where two launches, the scan of the lengths and three loads that
+// wait for each other (pages, codes, partial results) are the time.
 
 #include <hip/hip_runtime.h>
 
@@ -81,18 +86,20 @@ __device__ __forceinline__ u32x4 load_codes(const uint8_t* p) {
     return *reinterpret_cast<const u32x4*>(p);
 }
 
-// RT tiles of 16 rows.  A wave has one of them and a share of the tiles of
+// RT x NR tiles of 16 rows: a wave has NR of them and a share of the tiles of
 // keys; the RT waves of a workgroup with the same share read the same keys at
-// about the same time, from L2.  (One wave with several row tiles would convert
-// the codes once, but needs more than the registers of two waves a SIMD: for D =
-// 128 it spills.)
-template <typename T, int D, int RT>
-__global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams p) {
+// about the same time, from L2.  A wave has the tiles of DEPTH steps ahead in
+// registers; with DEPTH 2 it takes a SIMD for itself, and NR 2 converts each
+// code once for 32 rows.  (launch_t() has the choice and its figures.)
+// What is the same on a wave's lanes goes through readfirstlane, so that it
+// stays in scalar registers (3 % with 64 rows).
+template <typename T, int D, int RT, int NR, int DEPTH>
+__global__ __launch_bounds__(256, DEPTH == 1 ? 2 : 1) void attn_decode_kernel(const DecodeParams p) {
   constexpr int KL = D / 64, DT = D / 16, SHARES = kWaves / RT;
   typedef typename ActTraits<T>::vec8 vec8;
   __shared__ int prefix[kSeqsPerLaunch + 1];
   __shared__ int wave_total[kWaves];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, col = lane & 15, g = lane >> 4;
   const int row_tile = wave / SHARES;
   const int group = blockIdx.x / p.a.Hk, hk = blockIdx.x - group * p.a.Hk, w = group * SHARES + wave % SHARES;
 
@@ -126,34 +133,36 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
   }
   if (blockIdx.x == 0)
     for (int b = tid; b <= p.a.seq.B; b += 256) p.plan[b] = prefix[b];
-  const int total = prefix[p.a.seq.B];
+  const int total = __builtin_amdgcn_readfirstlane(prefix[p.a.seq.B]);
   int share = (total + p.W - 1) / p.W;
   share = share < 1 ? 1 : share;
   int at = static_cast<int64_t>(w) * share < total ? w * share : total;
   const int stop = at + share < total ? at + share : total;
   if (at >= stop) return;
-  int b = last_not_above(p.a.seq.B, at, [&](int i) { return prefix[i]; });
+  int b = __builtin_amdgcn_readfirstlane(last_not_above(p.a.seq.B, at, [&](int i) { return prefix[i]; }));
 
   const int64_t head_bytes = static_cast<int64_t>(p.a.seq.page) * D;
   for (; at < stop; ++b) {
-    const int t_begin = at - prefix[b], count = prefix[b + 1] - prefix[b];
+    const int from = __builtin_amdgcn_readfirstlane(prefix[b]), to = __builtin_amdgcn_readfirstlane(prefix[b + 1]);
+    const int t_begin = at - from, count = to - from;
     if (count <= t_begin) continue;
-    const int t_end = (stop < prefix[b + 1] ? stop : prefix[b + 1]) - prefix[b];
-    at = prefix[b] + t_end;
+    const int t_end = (stop < to ? stop : to) - from;
+    at = from + t_end;
     const SeqSpan span = seq_span(p.a.seq, b);
     const int lo_tile = tiles_of(p, span).lo;
     const int first = span.len - span.rows, rows_i = span.rows < p.a.max_new ? span.rows : p.a.max_new;
     const int held = span.len < p.a.seq.capacity ? span.len : p.a.seq.capacity;
 
-    // this lane's row: its query, and the tokens that it attends
-    vec8 qf[KL][2];
-    int k_lo, k_hi;
-    {
-      const int row = 16 * row_tile + col, i = row / p.a.G, head = hk * p.a.G + (row - i * p.a.G);
+    // this lane's rows: their queries, and the tokens that they attend
+    vec8 qf[NR][KL][2];
+    int k_lo[NR], k_hi[NR];
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int row = 16 * (NR * row_tile + r) + col, i = row / p.a.G, head = hk * p.a.G + (row - i * p.a.G);
       const bool valid = i < rows_i;
       const int pos = first + i;
-      k_hi = !valid ? 0 : p.a.causal && pos + 1 < held ? pos + 1 : held;
-      k_lo = p.a.window > 0 && pos >= p.a.window ? pos - p.a.window + 1 : 0;
+      k_hi[r] = !valid ? 0 : p.a.causal && pos + 1 < held ? pos + 1 : held;
+      k_lo[r] = p.a.window > 0 && pos >= p.a.window ? pos - p.a.window + 1 : 0;
       const T* q = static_cast<const T*>(p.a.q) + (static_cast<int64_t>(span.first_row) + i) * p.a.q_stride + static_cast<int64_t>(head) * D;
 #pragma unroll
       for (int j = 0; j < KL; ++j)
@@ -162,7 +171,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
           u32x4 v = {0, 0, 0, 0};
           if (valid) v = *reinterpret_cast<const u32x4*>(q + 64 * j + 16 * g + 8 * e);
           v ^= p.a.flip;
-          qf[j][e] = __builtin_bit_cast(vec8, v);
+          qf[r][j][e] = __builtin_bit_cast(vec8, v);
         }
     }
     // tokens that every valid row attends, and that any does
@@ -172,10 +181,15 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
     const int any_lo = p.a.window > 0 && first >= p.a.window ? first - p.a.window + 1 : 0;
     const int any_hi = p.a.causal && last + 1 < held ? last + 1 : held;
 
-    f32x4 acc[DT];
-    float m = -INFINITY, l = 0.0f;
+    f32x4 acc[NR][DT];
+    float m[NR], l[NR];
 #pragma unroll
-    for (int d = 0; d < DT; ++d) acc[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int r = 0; r < NR; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) acc[r][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
 
     // pages of this lane's 16 keys as rows of a tile of K (chunk col / 4) and as keys of V (chunk g)
     struct Place {
@@ -188,167 +202,223 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(const DecodeParams 
       at.id = page_ahead(p.a.seq, pages, (lo_tile + t) * kTile + 16 * chunk, t < t_end, &at.slot);
       return at;
     };
-    u32x4 kreg[4][KL], vreg[DT];
-    uint32_t ks = 127, vs = 127;
-    auto load_k = [&](Place at_k, Place at_v) {
+    struct Tile {
+      u32x4 k[4][KL], v[DT];
+      uint32_t ks, vs;
+      int id;  // page of this lane's chunk of V
+    };
+    auto load_k = [&](Tile& x, Place at_k, Place at_v) {
       const uint8_t* k = p.a.k_cache + (static_cast<int64_t>(at_k.id < 0 ? 0 : at_k.id) * p.a.Hk + hk) * head_bytes +
                          static_cast<int64_t>(at_k.slot + (col & 3)) * D + 16 * g;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < KL; ++j) kreg[i][j] = load_codes<RT == 1>(k + 4 * i * D + 64 * j);
+        for (int j = 0; j < KL; ++j) x.k[i][j] = load_codes<RT == 1>(k + 4 * i * D + 64 * j);
       const int64_t cell = static_cast<int64_t>(at_v.id < 0 ? 0 : at_v.id) * p.a.Hk + hk;
-      ks = p.a.k_scale[cell];
-      vs = p.a.v_scale[cell];
+      x.ks = p.a.k_scale[cell];
+      x.vs = p.a.v_scale[cell];
     };
-    auto load_v = [&](Place at) {
+    auto load_v = [&](Tile& x, Place at) {
       const uint8_t* v = p.a.v_cache + (static_cast<int64_t>(at.id < 0 ? 0 : at.id) * p.a.Hk + hk) * head_bytes +
                          static_cast<int64_t>(col) * p.a.seq.page + at.slot;
 #pragma unroll
-      for (int d = 0; d < DT; ++d) vreg[d] = load_codes<RT == 1>(v + static_cast<int64_t>(16 * d) * p.a.seq.page);
+      for (int d = 0; d < DT; ++d) x.v[d] = load_codes<RT == 1>(v + static_cast<int64_t>(16 * d) * p.a.seq.page);
+      x.id = at.id;
     };
 
-    // Loads run ahead by a tile, and past the last one they go on at page 0: a
-    // branch around them would make the compiler wait for all loads in flight
-    // wherever it waits for any (3.5 us a tile instead of about 1.5).
-    // (Without pages there is nothing to load, and no key to attend.)
-    int t = t_begin;
-    if (p.a.seq.capacity > 0 && t < t_end) {
-      Place next_k = place_of(t, col >> 2), next_v = place_of(t, g);
-      int id_v = next_v.id;
-      load_k(next_k, next_v);
-      load_v(next_v);
-      next_k = place_of(t + 1, col >> 2);
-      next_v = place_of(t + 1, g);
-      for (; t < t_end; ++t) {
-        const Place after_k = place_of(t + 2, col >> 2), after_v = place_of(t + 2, g);
-        f32x4 s[4];
+    // A tile's work; the registers then take the tile at (at_k, at_v).
+    auto step = [&](Tile& x, int t, Place at_k, Place at_v) {
+      f32x4 s[NR][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i = 0; i < 4; ++i) {
 #pragma unroll
-          for (int j = 0; j < KL; ++j) {
-            s[i] = ActTraits<T>::mfma(ActTraits<T>::decode8_fp8(kreg[i][j].x, kreg[i][j].y), qf[j][0], s[i]);
-            s[i] = ActTraits<T>::mfma(ActTraits<T>::decode8_fp8(kreg[i][j].z, kreg[i][j].w), qf[j][1], s[i]);
+        for (int r = 0; r < NR; ++r) s[r][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < KL; ++j) {
+          const vec8 a0 = ActTraits<T>::decode8_fp8(x.k[i][j].x, x.k[i][j].y), a1 = ActTraits<T>::decode8_fp8(x.k[i][j].z, x.k[i][j].w);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            s[r][i] = ActTraits<T>::mfma(a0, qf[r][j][0], s[r][i]);
+            s[r][i] = ActTraits<T>::mfma(a1, qf[r][j][1], s[r][i]);
           }
         }
-        const float factor = e8m0_to_f32(ks) * p.a.c;
-        uint32_t vs_now = vs;
-        load_k(next_k, next_v);
+      }
+      const float factor = e8m0_to_f32(x.ks) * p.a.c;
+      uint32_t vs_now = x.vs;
+      const int id_v = x.id;
+      load_k(x, at_k, at_v);
 
-        const int key0 = (lo_tile + t) * kTile;
-        const int my0 = key0 + 16 * g;  // this lane's 16 keys
-        const bool whole = key0 >= all_lo && key0 + kTile <= all_hi && __ballot(id_v < 0 || vs_now > AttnTraits<T>::kMostV) == 0;
+      const int key0 = (lo_tile + t) * kTile;
+      const int my0 = key0 + 16 * g;  // this lane's 16 keys
+      const bool whole = key0 >= all_lo && key0 + kTile <= all_hi && __ballot(id_v < 0 || vs_now > AttnTraits<T>::kMostV) == 0;
+#pragma unroll
+      for (int r = 0; r < NR; ++r)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[i][j] *= factor;
-        uint32_t nan_any = 0, seen = 0;
-        if (!whole) {
-          const bool bad = vs_now > AttnTraits<T>::kMostV;
+          for (int j = 0; j < 4; ++j) s[r][i][j] *= factor;
+      uint32_t nan_any = 0, seen[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) seen[r] = 0;
+      if (!whole) {
+        const bool bad = vs_now > AttnTraits<T>::kMostV;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const int lo = id_v < 0 ? 16 : k_lo[r] - my0, hi = k_hi[r] - my0;  // of this lane's keys, [lo, hi) are attended
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int key = my0 + 4 * i + j;
-              const bool on = id_v >= 0 && key >= k_lo && key < k_hi;
-              s[i][j] = on ? s[i][j] : -INFINITY;
-              seen |= on ? 1u << (4 * i + j) : 0u;
+              const bool on = 4 * i + j >= lo && 4 * i + j < hi;
+              s[r][i][j] = on ? s[r][i][j] : -INFINITY;
+              seen[r] |= on ? 1u << (4 * i + j) : 0u;
             }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t keep = id_v < 0 ? 0 : byte_mask(any_lo - (my0 + 4 * j), any_hi - (my0 + 4 * j));
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              const uint32_t word = (bad ? 0x7f7f7f7fu : vreg[d][j]) & keep;
-              vreg[d][j] = word;
-              nan_any |= nan_codes(word);
-            }
-          }
-          if (bad || id_v < 0) vs_now = 127;
         }
-        float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) top = fmaxf(top, s[i][j]);
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64));
-        if (__ballot(top > m) != 0) {
-          const float now = fmaxf(m, top);
-          const float shrink = __builtin_amdgcn_exp2f(m - (now > -INFINITY ? now : 0.0f));
-          l *= shrink;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) acc[d] *= shrink;
-          m = now;
-        }
-        const float base = (m > -INFINITY ? m : 0.0f) - AttnTraits<T>::kLift;
-        float sum = 0.0f;
-        vec8 pf[2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float e = __builtin_amdgcn_exp2f(s[i][j] - base);
-            sum += e;
-            pf[i >> 1][4 * (i & 1) + j] = static_cast<T>(e);  // the one rounding between the products
-          }
-        l += sum;
-        if (!whole && __ballot(nan_any != 0) != 0) {
-          // A NaN among the values: 0 x NaN must not reach the rows that do not
-          // attend it.  Count for each output the NaN values that it attends,
-          // and take them out of the product.
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t keep = id_v < 0 ? 0 : byte_mask(any_lo - (my0 + 4 * j), any_hi - (my0 + 4 * j));
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
-            f32x4 hits = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              vec8 flag, on;
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const uint32_t n = nan_codes(vreg[d][2 * h + (j >> 2)]);
-                flag[j] = static_cast<T>((n >> (8 * (j & 3) + 7)) & 1 ? 1.0f : 0.0f);
-                on[j] = static_cast<T>((seen >> (8 * h + j)) & 1 ? 1.0f : 0.0f);
-              }
-              hits = ActTraits<T>::mfma(flag, on, hits);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              vreg[d][j] &= ~((nan_codes(vreg[d][j]) >> 7) * 0xffu);
-              acc[d][j] = hits[j] > 0.0f ? NAN : acc[d][j];
-            }
+            const uint32_t word = (bad ? 0x7f7f7f7fu : x.v[d][j]) & keep;
+            x.v[d][j] = word;
+            nan_any |= nan_codes(word);
           }
         }
-        const float power = __uint_as_float((vs_now > AttnTraits<T>::kDown ? vs_now - AttnTraits<T>::kDown : 0u) << 23);
+        if (bad || id_v < 0) vs_now = 127;
+      }
+      float top[NR];
+      bool grown = false;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        top[r] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top[r] = fmaxf(top[r], s[r][i][j]);
+        top[r] = fmaxf(top[r], __shfl_xor(top[r], 16, 64));
+        top[r] = fmaxf(top[r], __shfl_xor(top[r], 32, 64));
+        grown = grown || top[r] > m[r];
+      }
+      if (__ballot(grown) != 0) {
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float now = fmaxf(m[r], top[r]);
+          const float shrink = __builtin_amdgcn_exp2f(m[r] - (now > -INFINITY ? now : 0.0f));
+          l[r] *= shrink;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) acc[r][d] *= shrink;
+          m[r] = now;
+        }
+      }
+      vec8 pf[NR][2];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float base = (m[r] > -INFINITY ? m[r] : 0.0f) - AttnTraits<T>::kLift;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float e = __builtin_amdgcn_exp2f(s[r][i][j] - base);
+            sum += e;
+            pf[r][i >> 1][4 * (i & 1) + j] = static_cast<T>(e);  // the one rounding between the products
+          }
+        l[r] += sum;
+      }
+      if (!whole && __ballot(nan_any != 0) != 0) {
+        // A NaN among the values: 0 x NaN must not reach the rows that do not
+        // attend it.  Count for each output the NaN values that it attends,
+        // and take them out of the product.
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          acc[d] = ActTraits<T>::mfma(decode8_power<T>(vreg[d].x, vreg[d].y, power), pf[0], acc[d]);
-          acc[d] = ActTraits<T>::mfma(decode8_power<T>(vreg[d].z, vreg[d].w, power), pf[1], acc[d]);
+          f32x4 hits[NR];
+#pragma unroll
+          for (int r = 0; r < NR; ++r) hits[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            vec8 flag;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t n = nan_codes(x.v[d][2 * h + (j >> 2)]);
+              flag[j] = static_cast<T>((n >> (8 * (j & 3) + 7)) & 1 ? 1.0f : 0.0f);
+            }
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              vec8 on;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) on[j] = static_cast<T>((seen[r] >> (8 * h + j)) & 1 ? 1.0f : 0.0f);
+              hits[r] = ActTraits<T>::mfma(flag, on, hits[r]);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x.v[d][j] &= ~((nan_codes(x.v[d][j]) >> 7) * 0xffu);
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[r][d][j] = hits[r][j] > 0.0f ? NAN : acc[r][d][j];
         }
-        load_v(next_v);
-        id_v = next_v.id;
-        next_k = after_k;
-        next_v = after_v;
+      }
+      const float power = __uint_as_float((vs_now > AttnTraits<T>::kDown ? vs_now - AttnTraits<T>::kDown : 0u) << 23);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const vec8 a0 = decode8_power<T>(x.v[d].x, x.v[d].y, power), a1 = decode8_power<T>(x.v[d].z, x.v[d].w, power);
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          acc[r][d] = ActTraits<T>::mfma(a0, pf[r][0], acc[r][d]);
+          acc[r][d] = ActTraits<T>::mfma(a1, pf[r][1], acc[r][d]);
+        }
+      }
+      load_v(x, at_v);
+    };
+
+    // Loads run ahead by DEPTH tiles, and past the last one they go on at page 0:
+    // a branch around them would make the compiler wait for all loads in flight
+    // wherever it waits for any.  (Without pages there is nothing to load, and no
+    // key to attend.)
+    int t = t_begin;
+    if (p.a.seq.capacity > 0 && t < t_end) {
+      Tile tile[DEPTH];
+      Place next_k = place_of(t, col >> 2), next_v = place_of(t, g);
+#pragma unroll
+      for (int i = 0; i < DEPTH; ++i) {
+        load_k(tile[i], next_k, next_v);
+        load_v(tile[i], next_v);
+        next_k = place_of(t + i + 1, col >> 2);
+        next_v = place_of(t + i + 1, g);
+      }
+      for (; t < t_end; t += DEPTH) {
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) {
+          if (t + i < t_end) {
+            const Place after_k = place_of(t + i + DEPTH + 1, col >> 2), after_v = place_of(t + i + DEPTH + 1, g);
+            step(tile[i], t + i, next_k, next_v);
+            next_k = after_k;
+            next_v = after_v;
+          }
+        }
       }
     }
 
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-    const int out = 16 * row_tile + col, i = out / p.a.G;
-    if (i < rows_i) {
-      if (t_begin == 0 && t_end == count) {  // the whole sequence
-        const int64_t at_row = (static_cast<int64_t>(span.first_row) + i) * p.a.Hq + hk * p.a.G + (out - i * p.a.G);
 #pragma unroll
-        for (int d = 0; d < DT; ++d) store_quad<T>(p.a, at_row, D, 16 * d + 4 * g, m, l, acc[d]);
-        if (g == 0) store_lse<T>(p.a, at_row, m, l);
-      } else {
-        float* part = part_of(p, D, hk, w, t_begin == 0);
-        float* row = part + attn_part_head(p.rows) + out * D + 4 * g;
+    for (int r = 0; r < NR; ++r) {
+      l[r] += __shfl_xor(l[r], 16, 64);
+      l[r] += __shfl_xor(l[r], 32, 64);
+      const int out = 16 * (NR * row_tile + r) + col, i = out / p.a.G;
+      if (i < rows_i) {
+        if (t_begin == 0 && t_end == count) {  // the whole sequence
+          const int64_t at_row = (static_cast<int64_t>(span.first_row) + i) * p.a.Hq + hk * p.a.G + (out - i * p.a.G);
 #pragma unroll
-        for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(row + 16 * d) = acc[d];
-        if (g == 0) {
-          part[out] = m;
-          part[p.rows + out] = l;
+          for (int d = 0; d < DT; ++d) store_quad<T>(p.a, at_row, D, 16 * d + 4 * g, m[r], l[r], acc[r][d]);
+          if (g == 0) store_lse<T>(p.a, at_row, m[r], l[r]);
+        } else {
+          float* part = part_of(p, D, hk, w, t_begin == 0);
+          float* row = part + attn_part_head(p.rows) + out * D + 4 * g;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4*>(row + 16 * d) = acc[r][d];
+          if (g == 0) {
+            part[out] = m[r];
+            part[p.rows + out] = l[r];
+          }
         }
       }
     }
@@ -410,10 +480,11 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(const DecodeParams p
   if (lane == 0) store_lse<T>(p.a, row * p.a.Hq + h, m, l);
 }
 
-template <typename T, int D, int RT>
+template <typename T, int D, int RT, int NR, int DEPTH>
 int launch_rows(DecodeParams p, int64_t join_rows, hipStream_t s) {
-  p.W = attn_groups(p.a.Hk) * (kWaves / RT);
-  hipLaunchKernelGGL((attn_decode_kernel<T, D, RT>), dim3(attn_groups(p.a.Hk) * p.a.Hk), dim3(256), 0, s, p);
+  const int groups = attn_groups(p.a.Hk, DEPTH == 1 ? 2 : 1);
+  p.W = groups * (kWaves / RT);
+  hipLaunchKernelGGL((attn_decode_kernel<T, D, RT, NR, DEPTH>), dim3(groups * p.a.Hk), dim3(256), 0, s, p);
   const dim3 grid(static_cast<uint32_t>(join_rows * p.a.Hq));
   // few rows may have many partial results each, many rows have few
   const int64_t rows = join_rows * p.a.Hq, most = p.a.seq.capacity / kTile;
@@ -428,11 +499,17 @@ int launch_rows(DecodeParams p, int64_t join_rows, hipStream_t s) {
 
 template <typename T, int D>
 int launch_t(const DecodeParams& p, int64_t join_rows, hipStream_t s) {
-  switch (attn_row_tiles(p.a.max_new, p.a.G)) {
-    case 1: return launch_rows<T, D, 1>(p, join_rows, s);
-    case 2: return launch_rows<T, D, 2>(p, join_rows, s);
-    default: return launch_rows<T, D, 4>(p, join_rows, s);
-  }
+  // attn_shares() has the same choice.  With two row tiles and two steps a wave,
+  // 25 and 50 rows of D = 128 take 71 and 93 us over 131000 tokens, with one of
+  // each 75 and 108.  But 16 rows take 60 us with two steps a wave and 56 with
+  // one, on two waves a SIMD; and 28 rows of D = 64 30 us against 22 over 16
+  // windows of 4096 tokens, where the partial results weigh more.
+  const int rows = p.rows;
+  if (rows <= 16) return launch_rows<T, D, 1, 1, 1>(p, join_rows, s);
+  if constexpr (D == 64)
+    return rows <= 32 ? launch_rows<T, D, 2, 1, 1>(p, join_rows, s) : launch_rows<T, D, 4, 1, 1>(p, join_rows, s);
+  else
+    return rows <= 32 ? launch_rows<T, D, 1, 2, 2>(p, join_rows, s) : launch_rows<T, D, 2, 2, 2>(p, join_rows, s);
 }
 
 }  // namespace

@@ -307,16 +307,20 @@ int launch_qk_norm_rope(const QkNormRopeArgs& a, bool vec, const SeqArgs* seq);
 // and page_size * D <= 16384, cache codes 16-byte aligned.
 int launch_kv_append(const KvAppendArgs& a, bool vec);
 
-// The decode kernel of attention: workgroups of four waves for each key head
-// (two for each compute unit in all).  In the workspace, behind the plan of a
-// launch's sequences: two partial results for each share of a key head's tiles.
+// The decode kernel of attention: workgroups of four waves for each key head,
+// one or two for each compute unit in all.  In the workspace, behind the plan of
+// a launch's sequences: two partial results for each share of a key head's tiles.
 constexpr int kSeqsPerLaunch = 1024;
 constexpr int64_t kAttnPlanBytes = 4352;  // (kSeqsPerLaunch + 1) x 4, up to 256
-inline int attn_groups(int64_t Hk) { return Hk >= 512 ? 1 : static_cast<int>(512 / Hk); }
-// 16-row tiles of max_new tokens of G query heads: 1, 2 or 4 (up to 64 rows)
-inline int attn_row_tiles(int64_t max_new, int64_t G) {
-  const int64_t rows = max_new * G;
-  return rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+inline int attn_groups(int64_t Hk, int per_unit) {
+  const int64_t places = 256 * per_unit;
+  return Hk >= places ? 1 : static_cast<int>(places / Hk);
+}
+// shares of a key head, for up to 64 rows (max_new tokens of G query heads)
+inline int64_t attn_shares(int64_t rows, int64_t Hk, int64_t D) {
+  if (rows <= 16) return attn_groups(Hk, 2) * 4;
+  if (D == 64) return attn_groups(Hk, 2) * (rows <= 32 ? 2 : 1);
+  return attn_groups(Hk, 1) * (rows <= 32 ? 4 : 2);
 }
 // maxima and sums of `rows` rows in whole 16-byte units, then their outputs
 constexpr int64_t attn_part_head(int64_t rows) { return (2 * rows + 3) / 4 * 4; }
@@ -326,7 +330,7 @@ inline int64_t attn_decode_workspace(int64_t max_new, int64_t Hk, int64_t G, int
   int64_t most = 0;
   for (int64_t rows = 16; rows <= 64; rows *= 2) {
     const int64_t n = max_new < rows / G ? max_new : rows / G;
-    const int64_t floats = attn_groups(Hk) * 4 / attn_row_tiles(n, G) * Hk * 2 * attn_part_floats(n * G, D);
+    const int64_t floats = attn_shares(n * G, Hk, D) * Hk * 2 * attn_part_floats(n * G, D);
     most = most > floats ? most : floats;
   }
   return kAttnPlanBytes + most * 4;
