@@ -1,7 +1,8 @@
 // Attention over the paged 8-bit cache for any head size, page size, alignment
 // and number of tokens: a workgroup per row and head, 256 tokens at a time,
-// with the running maximum and sum of the softmax in FP32.  The kernels in
-// attention.hip take what is served in earnest.
+// with the running maximum and sum of the softmax in FP32.  Made to be right for
+// everything, not fast; attention.hip and attention_prompt.hip have the heads of
+// 64 and 128.
 
 #include <hip/hip_runtime.h>
 

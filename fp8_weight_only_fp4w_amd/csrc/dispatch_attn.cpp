@@ -68,7 +68,7 @@ int check_rope(const RopeArgs& r, int64_t D) {
 int check_seq(const SeqArgs& s, int64_t M) {
   if (s.B < 0 || s.B >= kMax32 || s.max_pages < 0 || s.num_pages < 0 || s.num_pages >= kMax32) return FP4W_ERR_SHAPE;
   if (s.page_size < 1 || s.page_size >= kMax32 || s.max_pages >= kMax32 || s.max_pages * s.page_size >= kMax32) return FP4W_ERR_SHAPE;
-  if (s.starts == nullptr && s.B != M) return FP4W_ERR_SHAPE;
+  if (!mul_ok(s.B, s.max_pages) || (s.starts == nullptr && s.B != M)) return FP4W_ERR_SHAPE;
   return FP4W_OK;
 }
 
@@ -209,8 +209,9 @@ int fp8w_attention_ex(const void* q, int64_t q_stride, int64_t M, int64_t Hq, in
   if (max_new < 0 || window < 0) return FP4W_ERR_SHAPE;
   if (starts == nullptr) max_new = 1;
   max_new = std::min(max_new, M);
-  const int64_t need = fp8w_attention_workspace(M, Hq, Hk, D, B, max_new), codes = cache_codes(seq, Hk, D);
+  const int64_t need = fp8w_attention_workspace(M, Hq, Hk, D, B, max_new);
   if (need < 0) return static_cast<int>(need);
+  const int64_t codes = cache_codes(seq, Hk, D);
   if (codes < 0) return FP4W_ERR_SHAPE;
   if (path != FP4W_PATH_AUTO && path != FP4W_PATH_ATTN_GENERIC && path != FP4W_PATH_ATTN_DECODE && path != FP4W_PATH_ATTN_PROMPT)
     return FP4W_ERR_PATH;
@@ -237,10 +238,12 @@ int fp8w_attention_ex(const void* q, int64_t q_stride, int64_t M, int64_t Hq, in
       if (overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return FP4W_ERR_ALIAS;
   }
   const bool fast = tiled(D) && page_size % 16 == 0 && rows_vec(qi) && aligned(k_cache, 16) && aligned(v_cache, 16) && aligned(Y, 16);
-  // (the tiles of a launch's sequences are counted in 32 bits, and so are a grid's threads)
-  const bool decode = fast && max_new * (Hq / Hk) <= kDecodeRows && M * Hq < (1 << 25) &&
-                      std::min<int64_t>(B, fp4w::kSeqsPerLaunch) * (max_pages * page_size / 64 + 2) < kMax32;
-  const bool prompt = fast && max_pages * page_size < kMax32 - 128 && mul_ok(Hk, page_size) && Hk * page_size * D < kMax32 &&
+  // (tokens with some tiles behind them, the tiles of a launch's sequences and a
+  // grid's threads are counted in 32 bits)
+  const bool counted = max_pages * page_size < kMax32 - 512;
+  const bool decode = fast && counted && max_new * (Hq / Hk) <= kDecodeRows && M * Hq < (1 << 25) &&
+                      std::min<int64_t>(B, fp4w::kSeqsPerLaunch) * (max_pages * page_size / 64 + 2) < kMax32 / 2;
+  const bool prompt = fast && counted && mul_ok(Hk, page_size) && Hk * page_size * D < kMax32 &&
                       (fp4w::attn_row_tiles_most(M, Hq / Hk, B) * Hk + 2 * fp4w::kPromptWork) * 256 < 2 * kMax32;
   if ((path == FP4W_PATH_ATTN_DECODE && !decode) || (path == FP4W_PATH_ATTN_PROMPT && !prompt)) return FP4W_ERR_PATH;
   const AttentionArgs a{q, q_stride, M, Hq, Hk, D, max_new, seq, k_cache, k_scale, v_cache, v_scale, scale, causal != 0,

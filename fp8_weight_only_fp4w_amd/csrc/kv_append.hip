@@ -116,8 +116,8 @@ __global__ __launch_bounds__(256) void kv_append_generic_kernel(const AppendPara
     if (r.lo > 0 && before > e) e = before;
     if (r.lo > 0 && e != before) {
       const float down = e8m0_to_f32(before) * e8m0_inverse(e);
-      for (int i = tid; i < r.lo * D; i += 256) {
-        const int t = value ? i % r.lo : i / D, d = value ? i / r.lo : i - t * D;
+      for (int64_t i = tid; i < static_cast<int64_t>(r.lo) * D; i += 256) {
+        const int64_t t = value ? i % r.lo : i / D, d = value ? i / r.lo : i - t * D;
         uint8_t* c = codes + t * ts + d * ds;
         const float f = e4m3_to_f32<0>(*c) * down;
         *c = static_cast<uint8_t>(e4m3_pair(f, 0.0f));

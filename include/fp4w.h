@@ -598,8 +598,9 @@ int64_t fp8w_attention_workspace(int64_t M, int64_t Hq, int64_t Hk, int64_t D, i
  * among it, does not show.  Scores, softmax and sums are FP32; the softmax's
  * numerators are rounded to T for their product with V; Y is rounded once.  The result for a
  * row does not depend on the order in which the GPU works, but its last bits
- * may on the rest of the batch (where its sum is cut).  With FP16, stored
- * values are taken up to 2^16 (whatever was appended from FP16 is in range).
+ * may on the rest of the batch (where its sum is cut).  With heads of 64
+ * and 128, a page whose value scale is above 2^8 (FP16; appended FP16 needs no
+ * more) or 2^119 (BF16) counts as NaN.
  *
  *   q        T[M, Hq, D] with a stride.   Hq is a multiple of Hk.
  *   max_new  no sequence has more new tokens (rows behind it are left as they

@@ -2,11 +2,17 @@
 block.  No call here reaches a kernel launch, and none needs a GPU."""
 
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 import torch
 
 import fp8_weight_only_fp4w_amd as fw
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+ROOT = os.path.dirname(HERE)
 
 
 def _vp(x):
@@ -170,3 +176,18 @@ def test_cache_is_what_the_header_says():
     c = fw.fp8w_kv_cache(5, 3, 16, 64, "cpu")
     assert c.k.shape == (5, 3, 16, 64) and c.v.shape == (5, 3, 64, 16) and c.k_scale.shape == c.v_scale.shape == (5, 3)
     assert all(t.dtype == torch.uint8 and t.is_contiguous() for t in c)
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
+def test_dispatch_under_asan_ubsan(tmp_path):
+    exe = tmp_path / "attn_driver"
+    cmd = ["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+           os.path.join(ROOT, "fp8_weight_only_fp4w_amd", "csrc", "dispatch_attn.cpp"),
+           os.path.join(HERE, "host_sanitize", "attn_driver.cpp"), "-o", str(exe)]
+    b = subprocess.run(cmd, capture_output=True, text=True)
+    assert b.returncode == 0, b.stderr[-4000:]
+    env = dict(os.environ, ASAN_OPTIONS="detect_leaks=0:abort_on_error=0", UBSAN_OPTIONS="print_stacktrace=1")
+    env.pop("LD_PRELOAD", None)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, env=env, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip().endswith("ok"), (r.stdout + r.stderr)[-4000:]
+    assert "runtime error" not in r.stderr and "AddressSanitizer" not in r.stderr, r.stderr[-4000:]
