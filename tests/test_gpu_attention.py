@@ -65,6 +65,9 @@ CASES = [
     ([130, 7], [1, 1], 16, 64, 1, 128, 0),         # 64 rows
     ([200, 3, 70], [2, 4, 3], 32, 28, 4, 64, 0),
     ([513, 64], [5, 3], 128, 6, 2, 128, 0),
+    ([40, 3], [4, 2], 16, 16, 2, 128, 20),         # 32 rows
+    ([60, 0, 200], [5, 7, 2], 16, 16, 2, 128, 0),  # 56 rows
+    ([700, 3], [3, 3], 64, 22, 1, 64, 0),          # 66 rows: too many
     ([400, 100], [1, 2], 16, 8, 2, 128, 50),
     ([5000], [1], 16, 4, 4, 128, 0),
     ([4100, 3], [1, 1], 64, 7, 1, 64, 1000),
@@ -107,8 +110,8 @@ def test_not_causal(D, page):
     check(q, parts, starts, lens, table, "bf16", causal=False, window=9, scale=-0.2)
 
 
-@pytest.mark.parametrize("D,page", [(128, 16), (64, 32), (40, 8)])
-def test_rows_without_a_token(D, page):
+@pytest.mark.parametrize("D,page,Hq", [(128, 16, 6), (128, 16, 10), (128, 32, 24), (64, 32, 6), (40, 8, 6)])
+def test_rows_without_a_token(D, page, Hq):
     """Sequences that hold nothing, pages that are absent in the middle or throughout, more new rows than tokens."""
     rng = np.random.default_rng(22)
     starts, lens, table, pages = batch(rng, [0, 200, 40, 0, 300], [3, 2, 4, 5, 1], page)
@@ -118,7 +121,7 @@ def test_rows_without_a_token(D, page):
     lens[3] = 2                       # five rows, two tokens
     lens[4] = 2 ** 31 - 1             # more than the table has pages for; the row is behind them all
     parts = filled(rng, starts, np.minimum(lens, 400), table, page, pages, 2, D)
-    q = rounded(rng, (15, 6, D), "bf16")
+    q = rounded(rng, (15, Hq, D), "bf16")
     check(q, parts, starts, lens, table, "bf16")
     check(q, parts, starts, lens, table, "bf16", window=2)
     # the batch without any page, and without any token
@@ -128,11 +131,11 @@ def test_rows_without_a_token(D, page):
     y = fw.fp8w_attention(on_gpu(q[:2], "bf16"), to_cache(parts), torch.zeros(2, 0, dtype=torch.int32, device="cuda"),
                           torch.full((2,), 9, dtype=torch.int32, device="cuda"))
     assert (y == 0).all()
-    assert fw.fp8w_attention(on_gpu(q[:0], "bf16"), to_cache(parts), on_gpu(table[:0]), on_gpu(lens[:0])).shape == (0, 6, D)
+    assert fw.fp8w_attention(on_gpu(q[:0], "bf16"), to_cache(parts), on_gpu(table[:0]), on_gpu(lens[:0])).shape == (0, Hq, D)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("n", [1, 3, 8, 14, 40])
 @pytest.mark.parametrize("D,page", [(128, 16), (64, 64), (24, 6)])
 def test_nan_and_infinity_where_they_are_masked(D, page, n, dtype):
     """A later token's NaN value or key, or a NaN scale of a page before the window, does not reach a row that does not
