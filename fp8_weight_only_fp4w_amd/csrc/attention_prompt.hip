@@ -365,18 +365,19 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
   }
 }
 
-// Joins the parts of every row: D / 4 lanes for a row, a workgroup for a row
-// tile and key head.
+// Joins the parts of every row: D / 4 lanes for a row, a workgroup for an eighth
+// of a row tile and key head.
 template <typename T, int D, int R>
 __global__ __launch_bounds__(256) void attn_prompt_join_kernel(const PromptParams pp) {
   constexpr int LANES = D / 4, ROWS = 256 / LANES;
   const AttnParams& p = pp.a;
-  const int64_t unit = blockIdx.x / p.Hk;
-  const int hk = static_cast<int>(blockIdx.x - unit * p.Hk), lane = threadIdx.x % LANES;
+  const int cell = blockIdx.x >> 3, first = (blockIdx.x & 7) * (R / 8), hk = cell % p.Hk, lane = threadIdx.x % LANES;
+  const int64_t unit = cell / p.Hk;
   RowTile r;
   if (!row_tile_of<R>(p, unit, r)) return;
   const float* part = pp.part + (unit * p.Hk + hk) * pp.splits * attn_part_floats(R, D);
-  for (int mine = threadIdx.x / LANES; mine < r.rows; mine += ROWS) {
+  const int end = first + R / 8 < r.rows ? first + R / 8 : r.rows;
+  for (int mine = first + threadIdx.x / LANES; mine < end; mine += ROWS) {
     float m = -INFINITY, l = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
@@ -399,7 +400,7 @@ int launch_waves(PromptParams p, int64_t M, int64_t capacity, hipStream_t s) {
   p.splits = static_cast<int32_t>(attn_prompt_splits(p.units * p.a.Hk, capacity));
   hipLaunchKernelGGL((attn_prompt_kernel<T, D, WAVES>), dim3(static_cast<uint32_t>(p.units * p.a.Hk * p.splits)), dim3(64 * WAVES), 0, s, p);
   if (p.splits > 1)
-    hipLaunchKernelGGL((attn_prompt_join_kernel<T, D, R>), dim3(static_cast<uint32_t>(p.units * p.a.Hk)), dim3(256), 0, s, p);
+    hipLaunchKernelGGL((attn_prompt_join_kernel<T, D, R>), dim3(static_cast<uint32_t>(8 * p.units * p.a.Hk)), dim3(256), 0, s, p);  // (units * Hk < kPromptPlaces)
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
