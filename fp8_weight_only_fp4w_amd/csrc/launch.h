@@ -342,8 +342,10 @@ int launch_attention_decode(const AttentionArgs& a);
 // Where there are fewer than the GPU has places for (two workgroups a compute
 // unit), their keys are cut into up to 16 parts of at least 8 key tiles, whose
 // results are in the workspace.  A part costs 133 KB of traffic for D = 128:
-// with 784 row tiles, two parts each took 85 us and whole ones 56; with 360 of
-// some 240 key tiles, one to three parts took 420, 353 and 329 us.
+// with 784 row tiles, two parts each took 85 us and whole ones 56.  With 272 over
+// ragged 5000 to 25000 tokens, 1, 2, 3, 5 and 7 parts took 420, 353, 342, 323 and
+// 320 us; with 336 over even 15000, 3, 5 and 6 parts 376, 403 and 395: two full
+// rounds of workgroups, and then parts that cost more than they even out.
 constexpr int kPromptRows = 128;
 constexpr int64_t kPromptPlaces = 512, kPromptWork = 768;  // workgroups that are wanted where there are too few
 inline int64_t attn_row_tiles_most(int64_t M, int64_t G, int64_t B) { return M * G / kPromptRows + B; }
