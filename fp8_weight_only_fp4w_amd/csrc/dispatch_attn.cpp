@@ -61,7 +61,7 @@ int check_heads(int64_t M, int64_t Hq, int64_t Hk, int64_t D) {
 int check_rope(const RopeArgs& r, int64_t D) {
   if ((r.cos == nullptr) != (r.sin == nullptr)) return FP4W_ERR_SHAPE;
   if (r.cos == nullptr) return FP4W_OK;
-  if (r.rows < 0 || r.dims < 0 || r.dims % 2 != 0 || r.dims > D || !mul_ok(r.rows, r.dims + 1)) return FP4W_ERR_SHAPE;
+  if (r.rows < 1 || r.dims < 0 || r.dims % 2 != 0 || r.dims > D || !mul_ok(r.rows, r.dims + 1)) return FP4W_ERR_SHAPE;
   return FP4W_OK;
 }
 

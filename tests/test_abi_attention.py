@@ -31,7 +31,7 @@ def _rope(q=1 * G, qs=512, Hq=4, k=2 * G, ks=256, Hk=2, M=8, D=128, qw=3 * G, kw
 def test_qk_norm_rope_refusals():
     assert _rope(dtype=fw.F32) == fw.ERR_DTYPE
     for bad in (dict(M=-1), dict(Hq=-1), dict(D=fw.MAX_HEAD_SIZE + 1), dict(M=1 << 31), dict(sin=None), dict(cos=None),
-                dict(dims=3), dict(dims=130), dict(dims=-2), dict(rows=-1), dict(qs=511), dict(ks=255), dict(qos=0),
+                dict(dims=3), dict(dims=130), dict(dims=-2), dict(rows=-1), dict(rows=0), dict(qs=511), dict(ks=255), dict(qos=0),
                 dict(kos=-256), dict(qs=1 << 61)):
         assert _rope(**bad) == fw.ERR_SHAPE, bad
     for bad in (dict(q=None), dict(k=None), dict(qo=None), dict(ko=None)):
@@ -63,7 +63,7 @@ def test_kv_append_refusals():
     assert _append(dtype=3) == fw.ERR_DTYPE
     for bad in (dict(M=-1), dict(Hk=-1), dict(D=fw.MAX_HEAD_SIZE + 1), dict(B=-1), dict(page=0), dict(pages=-1),
                 dict(columns=-1), dict(columns=1 << 28), dict(starts=None), dict(ks=100), dict(vs=100), dict(qs=100),
-                dict(qos=100), dict(dims=5), dict(sin=None), dict(pages=1 << 30, page=1 << 30, columns=1, Hk=1000)):
+                dict(qos=100), dict(dims=5), dict(rows=0), dict(sin=None), dict(pages=1 << 30, page=1 << 30, columns=1, Hk=1000)):
         assert _append(**bad) == fw.ERR_SHAPE, bad
     for bad in (dict(k=None), dict(v=None), dict(q=None), dict(qo=None), dict(lens=None), dict(table=None), dict(kc=None),
                 dict(ksc=None), dict(vc=None), dict(vsc=None)):
