@@ -488,8 +488,8 @@ int fp8w_moe_ex(const void* A, int64_t M, int64_t K, const int32_t* ids, const f
  * least 1, the tables of a token's position; the first rope_dims (even, at most D) values of a head are
  * rotated in pairs, (i, i + rope_dims / 2), or (2 i, 2 i + 1) if `interleaved`
  * is nonzero:   (a, b) -> (a cos - b sin, b cos + a sin).
- * Both NULL: no rotation.  A position outside [0, rope_rows) makes the token's
- * rotated heads NaN.
+ * Both NULL: no rotation.  A position outside [0, rope_rows) makes a token's
+ * rotated values NaN.
  *
  * Cache.  Pages of page_size tokens:
  *   k_cache  uint8[num_pages, Hk, page_size, D]   E4M3 "fn" codes
