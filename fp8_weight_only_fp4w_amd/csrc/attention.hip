@@ -26,15 +26,16 @@
 // lengths may differ as they like, the host need not know them, and the
 // workspace does not grow with them.  A sequence that lies in several shares is
 // joined by a second kernel from the shares' partial results, in order, so a
-// row's result does not depend on the order of work.
+// row's result does not depend on the order of work.  Short contexts have a
+// workgroup for each sequence and key head instead (below).
 //
 // Measured with BF16, 40 query and 8 key heads of 128, both kernels: a token after
 // 131000 (268 MB of cache) 56 us, 4.8 TB/s; 64 sequences of 300 to 8000 tokens
-// (533 MB) 105 us, 5.1 TB/s, what a large copy reaches (a read alone: 5.9); a
-// token after 900 11 us, where two launches, the scan of the lengths and loads
-// that wait for each other (pages, codes, partial results) are the time.  Of the
-// two workgroups of a compute unit the older one is served first: after 131000
-// tokens one ends at 33 us and the other at 45.
+// (533 MB) 105 us, 5.1 TB/s, what a large copy reaches (a read alone: 5.9).  Short
+// contexts are bound by loads that wait for each other (lengths, pages, codes): a
+// token after 200 takes 7.6 us, after 900 12.  Of the two workgroups of a compute
+// unit the older one is served first: after 131000 tokens one ends at 33 us and
+// the other at 45.
 
 #include <hip/hip_runtime.h>
 
@@ -44,6 +45,14 @@ namespace fp4w {
 namespace {
 
 constexpr int kWaves = 4;
+// Up to 16 rows over short contexts (by what the page table has room for), and no
+// more workgroups than compute units: a workgroup of eight waves for each sequence
+// and key head, in one launch and with nothing left to join.  With 8 key heads of
+// 128, 32 sequences of 100 to 1000 tokens take 15 us so and 26 in shares; 1
+// sequence of 200, 900 and 2000 tokens 7.6, 12.1 and 21 us against 11.1, 11.4 and
+// 12.1 (but a call from the host costs 3 us less in one launch); 128 sequences 51
+// against 42.
+constexpr int kLocalWaves = 8, kLocalTokens = 1024, kLocalPlaces = 256;
 constexpr int64_t kWideJoinRows = 128;  // up to so many rows, the join takes 1024 threads for each
 
 struct DecodeParams {
@@ -95,18 +104,22 @@ __device__ __forceinline__ u32x4 load_codes(const uint8_t* p) {
 // code once for 32 rows.  (launch_t() has the choice and its figures.)
 // What is the same on a wave's lanes goes through readfirstlane, so that it
 // stays in scalar registers (3 % with 64 rows).
-template <typename T, int D, int RT, int NR, int DEPTH>
-__global__ __launch_bounds__(256, DEPTH == 1 ? 2 : 1) void attn_decode_kernel(const DecodeParams p) {
+//
+// LOCAL: a workgroup of kLocalWaves waves has one sequence and key head to itself,
+// and joins its waves' results in LDS.
+template <typename T, int D, int RT, int NR, int DEPTH, bool LOCAL>
+__global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH == 1 ? 2 : 1) void attn_decode_kernel(const DecodeParams p) {
   constexpr int KL = D / 64, DT = D / 16, SHARES = kWaves / RT;
   typedef typename ActTraits<T>::vec8 vec8;
   __shared__ int prefix[kSeqsPerLaunch + 1];
   __shared__ int wave_total[kWaves];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, col = lane & 15, g = lane >> 4;
-  const int row_tile = wave / SHARES;
+  const int row_tile = LOCAL ? 0 : wave / SHARES;
   const int group = blockIdx.x / p.a.Hk, hk = blockIdx.x - group * p.a.Hk, w = group * SHARES + wave % SHARES;
+  int b = group, at = 0, stop = 1;
 
-  // first tile of each sequence among all
-  {
+  if constexpr (!LOCAL) {
+    // first tile of each sequence among all
     int own[kSeqsPerLaunch / 256], sum = 0;
 #pragma unroll
     for (int i = 0; i < kSeqsPerLaunch / 256; ++i) {
@@ -132,25 +145,36 @@ __global__ __launch_bounds__(256, DEPTH == 1 ? 2 : 1) void attn_decode_kernel(co
     }
     if (tid == 255 && p.a.seq.B == kSeqsPerLaunch) prefix[kSeqsPerLaunch] = before;
     __syncthreads();
+    if (blockIdx.x == 0)
+      for (int i = tid; i <= p.a.seq.B; i += 256) p.plan[i] = prefix[i];
+    const int total = __builtin_amdgcn_readfirstlane(prefix[p.a.seq.B]);
+    int share = (total + p.W - 1) / p.W;
+    share = share < 1 ? 1 : share;
+    at = static_cast<int64_t>(w) * share < total ? w * share : total;
+    stop = at + share < total ? at + share : total;
+    if (at >= stop) return;
+    b = __builtin_amdgcn_readfirstlane(last_not_above(p.a.seq.B, at, [&](int i) { return prefix[i]; }));
   }
-  if (blockIdx.x == 0)
-    for (int b = tid; b <= p.a.seq.B; b += 256) p.plan[b] = prefix[b];
-  const int total = __builtin_amdgcn_readfirstlane(prefix[p.a.seq.B]);
-  int share = (total + p.W - 1) / p.W;
-  share = share < 1 ? 1 : share;
-  int at = static_cast<int64_t>(w) * share < total ? w * share : total;
-  const int stop = at + share < total ? at + share : total;
-  if (at >= stop) return;
-  int b = __builtin_amdgcn_readfirstlane(last_not_above(p.a.seq.B, at, [&](int i) { return prefix[i]; }));
 
   const int64_t head_bytes = static_cast<int64_t>(p.a.seq.page) * D;
   for (; at < stop; ++b) {
-    const int from = __builtin_amdgcn_readfirstlane(prefix[b]), to = __builtin_amdgcn_readfirstlane(prefix[b + 1]);
-    const int t_begin = at - from, count = to - from;
-    if (count <= t_begin) continue;
-    const int t_end = (stop < to ? stop : to) - from;
-    at = from + t_end;
     const SeqSpan span = seq_span(p.a.seq, b);
+    int t_begin, t_end, count;
+    if constexpr (LOCAL) {
+      count = tiles_of(p, span).count;
+      if (count == 0) return;  // (the whole workgroup)
+      const int each = (count + kLocalWaves - 1) / kLocalWaves;
+      t_begin = wave * each < count ? wave * each : count;
+      t_end = t_begin + each < count ? t_begin + each : count;
+      at = stop;
+    } else {
+      const int from = __builtin_amdgcn_readfirstlane(prefix[b]), to = __builtin_amdgcn_readfirstlane(prefix[b + 1]);
+      t_begin = at - from;
+      count = to - from;
+      if (count <= t_begin) continue;
+      t_end = (stop < to ? stop : to) - from;
+      at = from + t_end;
+    }
     const int lo_tile = tiles_of(p, span).lo;
     const int first = span.len - span.rows, rows_i = span.rows < p.a.max_new ? span.rows : p.a.max_new;
     const int held = span.len < p.a.seq.capacity ? span.len : p.a.seq.capacity;
@@ -405,6 +429,37 @@ __global__ __launch_bounds__(256, DEPTH == 1 ? 2 : 1) void attn_decode_kernel(co
     for (int r = 0; r < NR; ++r) {
       l[r] += __shfl_xor(l[r], 16, 64);
       l[r] += __shfl_xor(l[r], 32, 64);
+    }
+    if constexpr (LOCAL) {  // pairwise, lane by lane
+      static_assert(NR == 1, "one row tile");
+      __shared__ f32x4 red_o[kLocalWaves / 2][DT][64];
+      __shared__ float red_m[kLocalWaves / 2][64], red_l[kLocalWaves / 2][64];
+#pragma unroll
+      for (int half = kLocalWaves / 2; half > 0; half >>= 1) {
+        if (wave >= half && wave < 2 * half) {
+          red_m[wave - half][lane] = m[0];
+          red_l[wave - half][lane] = l[0];
+#pragma unroll
+          for (int d = 0; d < DT; ++d) red_o[wave - half][d][lane] = acc[0][d];
+        }
+        __syncthreads();
+        if (wave < half) {
+          const float m0 = m[0], l0 = l[0];
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            m[0] = m0;
+            l[0] = l0;
+            join(m[0], l[0], acc[0][d], red_m[wave][lane], red_l[wave][lane], red_o[wave][d][lane]);
+          }
+        }
+        __syncthreads();
+      }
+      if (wave != 0) return;
+      t_begin = 0;
+      t_end = count;
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
       const int out = 16 * (NR * row_tile + r) + col, i = out / p.a.G;
       if (i < rows_i) {
         if (t_begin == 0 && t_end == count) {  // the whole sequence
@@ -486,7 +541,7 @@ template <typename T, int D, int RT, int NR, int DEPTH>
 int launch_rows(DecodeParams p, int64_t join_rows, hipStream_t s) {
   const int groups = attn_groups(p.a.Hk, DEPTH == 1 ? 2 : 1);
   p.W = groups * (kWaves / RT);
-  hipLaunchKernelGGL((attn_decode_kernel<T, D, RT, NR, DEPTH>), dim3(groups * p.a.Hk), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((attn_decode_kernel<T, D, RT, NR, DEPTH, false>), dim3(groups * p.a.Hk), dim3(256), 0, s, p);
   const dim3 grid(static_cast<uint32_t>(join_rows * p.a.Hq));
   // few rows may have many partial results each, many rows have few
   const int64_t rows = join_rows * p.a.Hq, most = p.a.seq.capacity / kTile;
@@ -507,6 +562,10 @@ int launch_t(const DecodeParams& p, int64_t join_rows, hipStream_t s) {
   // one, on two waves a SIMD; and 28 rows of D = 64 30 us against 22 over 16
   // windows of 4096 tokens, where the partial results weigh more.
   const int rows = p.rows;
+  if (rows <= 16 && p.a.seq.capacity <= kLocalTokens && p.a.seq.B * p.a.Hk <= kLocalPlaces) {
+    hipLaunchKernelGGL((attn_decode_kernel<T, D, 1, 1, 1, true>), dim3(p.a.seq.B * p.a.Hk), dim3(64 * kLocalWaves), 0, s, p);
+    return hipGetLastError() == hipSuccess ? 0 : -1;
+  }
   if (rows <= 16) return launch_rows<T, D, 1, 1, 1>(p, join_rows, s);
   if constexpr (D == 64)
     return rows <= 32 ? launch_rows<T, D, 2, 1, 1>(p, join_rows, s) : launch_rows<T, D, 4, 1, 1>(p, join_rows, s);

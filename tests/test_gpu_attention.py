@@ -35,12 +35,15 @@ def check(q, parts, starts, lens, table, dtype, scale=None, causal=True, window=
         scale = D ** -0.5
     Y, L, tol, tol_l = oa.attention(q, *parts, starts, lens, table, scale, causal, window, dtype)
     behind = int(starts[-1])
-    c, g, t, n = to_cache(parts), on_gpu(q, dtype), on_gpu(table), on_gpu(lens)
+    c, g, n = to_cache(parts), on_gpu(q, dtype), on_gpu(lens)
+    # the decode kernel has a form of its own for tables with room for up to 1024 tokens
+    wide = np.pad(table, ((0, 0), (0, -(-1040 // page))), constant_values=-1)
     st = on_gpu(starts) if use_starts else None
     got = []
     for path in which or paths(D, page, int(new.max(initial=0)) * Hq // Hk):
         out = torch.full_like(g, 9.0)
         lse = torch.full((M, Hq), 9.0, device="cuda")
+        t = on_gpu(wide if path == fw.PATH_ATTN_DECODE else table)
         fw.fp8w_attention(g, c, t, n, starts=st, max_new=int(new.max(initial=0)) if max_new is None else max_new, scale=scale,
                           causal=causal, window=window, out=out, lse=lse, path=path)
         torch.cuda.synchronize()
