@@ -557,10 +557,11 @@ int launch_rows(DecodeParams p, int64_t join_rows, hipStream_t s) {
 template <typename T, int D>
 int launch_t(const DecodeParams& p, int64_t join_rows, hipStream_t s) {
   // attn_shares() has the same choice.  With two row tiles and two steps a wave,
-  // 25 and 50 rows of D = 128 take 71 and 93 us over 131000 tokens, with one of
-  // each 75 and 108.  But 16 rows take 60 us with two steps a wave and 56 with
-  // one, on two waves a SIMD; and 28 rows of D = 64 30 us against 22 over 16
-  // windows of 4096 tokens, where the partial results weigh more.
+  // 25 and 50 rows of D = 128 take 71 and 93 us over 8 times 16000 tokens, with
+  // one of each 75 and 108.  But 5 rows take 60 us over 131000 tokens with two
+  // steps a wave and 56 with one, on two waves a SIMD; and up to 28 rows of D = 64
+  // 30 us against 22 over 16 windows of 4096 tokens, where the partial results
+  // weigh more.
   const int rows = p.rows;
   if (rows <= 16 && p.a.seq.capacity <= kLocalTokens && p.a.seq.B * p.a.Hk <= kLocalPlaces) {
     hipLaunchKernelGGL((attn_decode_kernel<T, D, 1, 1, 1, true>), dim3(p.a.seq.B * p.a.Hk), dim3(64 * kLocalWaves), 0, s, p);
