@@ -96,6 +96,11 @@ __device__ __forceinline__ uint32_t byte_mask(int lo, int hi) {
   return below_hi & ~below_lo;
 }
 
+// A row's maximum is -inf until it attends a token, and kLowest at least from then
+// on.  A row whose every score is -inf has a sum of 0 like one without a token, but
+// it is 0 / 0, and only the maximum tells them apart.
+constexpr float kLowest = -__FLT_MAX__;
+
 // (m, l, o) and (m2, l2, o2): maximum, sum and output of two sets of tokens.
 __device__ __forceinline__ void join(float& m, float& l, f32x4& o, float m2, float l2, f32x4 o2) {
   const float now = fmaxf(m, m2), base = now > -INFINITY ? now : 0.0f;
@@ -105,22 +110,22 @@ __device__ __forceinline__ void join(float& m, float& l, f32x4& o, float m2, flo
   o = o * a + o2 * c;
 }
 
-// Four values of a row's output; no token attended: a sum of 0 and zeros.
+// Four values of a row's output; no token attended: zeros.
 template <typename T>
 __device__ __forceinline__ void store_quad(const AttnParams& p, int64_t at_row, int D, int d, float m, float l, f32x4 o) {
   typedef T t4 __attribute__((ext_vector_type(4)));
-  const bool any = !(l == 0.0f);
-  const float inv = any ? static_cast<float>(1 << AttnTraits<T>::kDown) / l : 0.0f;
+  const bool none = l == 0.0f && m < kLowest;
+  const float inv = static_cast<float>(1 << AttnTraits<T>::kDown) / l;
   t4 y;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) y[j] = round_to<T>(any ? o[j] * inv : 0.0f);
+  for (int j = 0; j < 4; ++j) y[j] = round_to<T>(none ? 0.0f : o[j] * inv);  // (0 x inf where all scores are -inf)
   *reinterpret_cast<t4*>(static_cast<T*>(p.Y) + at_row * D + d) = y;
 }
 
 template <typename T>
 __device__ __forceinline__ void store_lse(const AttnParams& p, int64_t at_row, float m, float l) {
   constexpr float kLn2 = 0.693147180559945309f;
-  if (p.lse) p.lse[at_row] = !(l == 0.0f) ? (m + log2f(l) - AttnTraits<T>::kLift) * kLn2 : -INFINITY;
+  if (p.lse) p.lse[at_row] = !(l == 0.0f) ? (m + log2f(l) - AttnTraits<T>::kLift) * kLn2 : m < kLowest ? -INFINITY : NAN;
 }
 
 }  // namespace fp4w

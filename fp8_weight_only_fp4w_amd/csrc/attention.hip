@@ -316,7 +316,7 @@ __global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH =
       bool grown = false;
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
-        top[r] = -INFINITY;
+        top[r] = whole || seen[r] != 0 ? kLowest : -INFINITY;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll

@@ -79,7 +79,8 @@ __global__ __launch_bounds__(256) void attention_generic_kernel(const AttnParams
         vs = e8m0_to_f32(p.v_scale[cell]);
         at[tid] = cell * D * page + slot;
       }
-      const float now = fmaxf(top, block_reduce(score, red, false));
+      // (-inf until a token is attended)
+      const float now = fmaxf(top, block_reduce(id >= 0 ? fmaxf(score, -__FLT_MAX__) : -INFINITY, red, false));
       const float base = now > -INFINITY ? now : 0.0f;
       const float w = id >= 0 ? expf(score - base) : 0.0f;
       const float shrink = expf(top - base);
@@ -100,14 +101,14 @@ __global__ __launch_bounds__(256) void attention_generic_kernel(const AttnParams
       top = now;
       __syncthreads();
     }
-    // no token attended: a sum of 0, and 0 / 1
-    const bool any = !(sum == 0.0f);
+    // a sum of 0: no token attended, and 0 is stored; or every score is -inf, and 0 / 0
+    const bool none = sum == 0.0f && top == -INFINITY;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int d = tid + j * 256;
-      if (d < D) static_cast<T*>(p.Y)[u * D + d] = round_to<T>(any ? acc[j] / sum : 0.0f);
+      if (d < D) static_cast<T*>(p.Y)[u * D + d] = round_to<T>(none ? 0.0f : acc[j] / sum);
     }
-    if (p.lse != nullptr && tid == 0) p.lse[u] = any ? top + logf(sum) : -INFINITY;
+    if (p.lse != nullptr && tid == 0) p.lse[u] = none ? -INFINITY : sum == 0.0f ? NAN : top + logf(sum);
   }
 }
 

@@ -282,7 +282,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
           factor[i] = 1.0f;
         }
       }
-      float top = -INFINITY;
+      float top = seen != 0 ? kLowest : -INFINITY;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float most = s[i][0];

@@ -594,7 +594,8 @@ int64_t fp8w_attention_workspace(int64_t M, int64_t Hq, int64_t Hk, int64_t D, i
  *   lse[m, h] = log sum_t exp(s_t)
  * over the tokens t of the sequence that are held (t < seq_lens[b], their page
  * present), with t <= p if `causal` is nonzero and t > p - window if window >
- * 0.  Without any, Y is 0 and lse -inf.  What slots of other tokens hold, NaN
+ * 0.  Without any, Y is 0 and lse -inf; where every score is -inf (an infinite
+ * query) both are NaN, as 0 / 0 is.  What slots of other tokens hold, NaN
  * among it, does not show.  Scores, softmax and sums are FP32; the softmax's
  * numerators are rounded to T for their product with V; Y is rounded once.  The result for a
  * row does not depend on the order in which the GPU works, but its last bits

@@ -1,0 +1,51 @@
+"""Attention at the ends of the numbers' range, on the GPU, through every kernel
+that takes the case: against the float64 oracle."""
+
+import numpy as np
+import pytest
+
+from attention_cases import batch, filled, rounded
+from gpu_helpers import require_gpu
+from oracle import attention as oa
+from test_gpu_attention import check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    require_gpu()
+
+
+# held before, new, page, Hq, Hk, D, window
+ENDLESS = [
+    ([0], [1], 16, 1, 1, 64, 0),                  # one token attended
+    ([900, 3], [1, 1], 16, 5, 1, 128, 0),
+    ([3000, 0, 40], [2, 1, 3], 16, 8, 2, 128, 0),  # joined from several shares
+    ([9000, 100], [1, 1], 64, 40, 8, 64, 0),
+    ([200, 3, 70], [2, 4, 3], 32, 28, 4, 64, 30),
+    ([70], [150], 16, 3, 1, 128, 64),
+    ([5000], [40], 16, 8, 1, 64, 0),              # joined from several parts
+    ([33, 0], [2, 30], 10, 2, 1, 48, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("case", ENDLESS, ids=lambda c: f"{max(c[0])}+{max(c[1])}-{c[3]}/{c[4]}x{c[5]}-w{c[6]}")
+def test_rows_whose_every_score_is_minus_infinity(case, dtype):
+    """An infinity in a query whose keys all have the other sign there: 0 / 0, and not the zeros of a row without a token."""
+    held, new, page, Hq, Hk, D, window = case
+    rng = np.random.default_rng(70 + D)
+    starts, lens, table, pages = batch(rng, held + [20], new + [1], page)
+    table[-1] = -1  # a sequence without a page: its rows attend nothing, whatever their queries hold
+    parts = filled(rng, starts, lens, table, page, pages, Hk, D)
+    parts[0][..., 5] = 0x38  # 1
+    q = rounded(rng, (int(starts[-1]), Hq, D), dtype, 1.5)
+    hit = [(int(s), 0) for s in starts[:-1]] + [(int(starts[1]) - 1, Hq - 1)]
+    for m, h in hit:
+        q[m, h, 5] = -np.inf
+    Y, L, _, _ = oa.attention(q, *parts, starts, lens, table, 1.0, True, window)
+    lone = int(starts[-2])
+    assert all(np.isnan(Y[m, h]).all() and np.isnan(L[m, h]) for m, h in hit if m != lone)
+    assert (Y[lone] == 0).all() and np.isnan(Y).any(-1).sum() == len({x for x in hit if x[0] != lone})
+    check(q, parts, starts, lens, table, dtype, scale=1.0, window=window)
