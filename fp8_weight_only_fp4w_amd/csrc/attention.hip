@@ -269,7 +269,7 @@ __global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH =
           }
         }
       }
-      const float factor = e8m0_to_f32(x.ks) * p.a.c;
+      const float factor = finite_factor(e8m0_to_f32(x.ks) * p.a.c);
       uint32_t vs_now = x.vs;
       const int id_v = x.id;
       load_k(x, at_k, at_v);

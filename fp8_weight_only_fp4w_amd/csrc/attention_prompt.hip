@@ -209,7 +209,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
     }
     power = __uint_as_float((byte > AttnTraits<T>::kDown ? byte - AttnTraits<T>::kDown : 0u) << 23);
     if (wave == 0) {
-      if ((lane & 15) == 0) scale_lds[buf][chunk] = id < 0 ? 0.0f : e8m0_to_f32(k_byte) * p.c;
+      if ((lane & 15) == 0) scale_lds[buf][chunk] = id < 0 ? 0.0f : finite_factor(e8m0_to_f32(k_byte) * p.c);
       const uint64_t absent = __ballot(id < 0);
       if (tid == 0) absent_lds[buf] = static_cast<int>((absent & 1) | (absent >> 15 & 2) | (absent >> 30 & 4) | (absent >> 45 & 8));
     }

@@ -32,6 +32,10 @@ __device__ __forceinline__ float e8m0_inverse(uint32_t b) {
   return b == 254 ? __uint_as_float(0x00400000u) : __uint_as_float((254u - b) << 23);
 }
 
+// A page's scale times the call's may pass FP32, but times a key of 0 it has to
+// be 0.  NaN stays.
+__device__ __forceinline__ float finite_factor(float f) { return f > __FLT_MAX__ ? __FLT_MAX__ : f; }
+
 // ------------------------------------------------------------------ sequences
 
 // SeqArgs for the device, in 32 bits.  capacity: the tokens that a row of the

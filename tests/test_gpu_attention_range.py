@@ -49,3 +49,17 @@ def test_rows_whose_every_score_is_minus_infinity(case, dtype):
     assert all(np.isnan(Y[m, h]).all() and np.isnan(L[m, h]) for m, h in hit if m != lone)
     assert (Y[lone] == 0).all() and np.isnan(Y).any(-1).sum() == len({x for x in hit if x[0] != lone})
     check(q, parts, starts, lens, table, dtype, scale=1.0, window=window)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 16), (24, 6)])
+def test_keys_of_zero_under_the_largest_scale(D, page, n):
+    """2^127 times the call's own scale passes FP32; times a key of 0 it is 0."""
+    rng = np.random.default_rng(72)
+    starts, lens, table, pages = batch(rng, [100, 20], [n, n], page)
+    parts = filled(rng, starts, lens, table, page, pages, 1, D)
+    for b in range(2):
+        parts[2][table[b, 1]] = 254
+        parts[0][table[b, 1]] = 0
+    q = rounded(rng, (2 * n, 3, D), "bf16", 0.1)
+    check(q, parts, starts, lens, table, "bf16", scale=3.0)
