@@ -57,6 +57,7 @@ struct AttnTraits<__bf16> {
   static constexpr float kLift = 0.0f;      // numerators are 2^(s - m + kLift)
   static constexpr float kLag = 8.0f;       // and m may be smaller than the largest s so far by kLag
   static constexpr uint32_t kDown = 0;      // V is held times 2^-kDown
+  static constexpr bool kFarQueries = true;
   static constexpr uint32_t kMostV = 246;   // 448 * 2^119 is below BF16's largest value
   __device__ __forceinline__ static bf16x2 cvt(uint32_t w, float s, bool hi) {
     return hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true) : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false);
@@ -69,6 +70,7 @@ struct AttnTraits<_Float16> {
   static constexpr float kLift = 8.0f;
   static constexpr float kLag = 6.0f;
   static constexpr uint32_t kDown = 1;
+  static constexpr bool kFarQueries = false;  // 65504 * 448 * 128 is far from FP32's end
   static constexpr uint32_t kMostV = 135;
   __device__ __forceinline__ static f16x2 cvt(uint32_t w, float s, bool hi) {
     return hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, true) : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, false);

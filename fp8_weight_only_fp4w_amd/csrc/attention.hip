@@ -217,6 +217,38 @@ __global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH =
       for (int d = 0; d < DT; ++d) acc[r][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
+    float c[NR];  // scale * log2(e), and kFarUp where the row's queries are held smaller
+    auto hold_far_rows = [&]() {
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        c[r] = p.a.c;
+        if constexpr (AttnTraits<T>::kFarQueries) {
+          uint32_t far = 0;
+#pragma unroll
+          for (int j = 0; j < KL; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const u32x4 v = __builtin_bit_cast(u32x4, qf[r][j][e]);
+              far |= (far_pair(v.x) | far_pair(v.y)) | (far_pair(v.z) | far_pair(v.w));
+            }
+          if (__ballot(far != 0) != 0) {
+            far |= __shfl_xor(far, 16, 64);
+            far |= __shfl_xor(far, 32, 64);
+            if (far != 0) {
+              c[r] *= kFarUp;
+#pragma unroll
+              for (int j = 0; j < KL; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const u32x4 v = __builtin_bit_cast(u32x4, qf[r][j][e]);
+                  qf[r][j][e] = __builtin_bit_cast(vec8, u32x4{down_pair(v.x), down_pair(v.y), down_pair(v.z), down_pair(v.w)});
+                }
+            }
+          }
+        }
+      }
+    };
+
     // pages of this lane's 16 keys as rows of a tile of K (chunk col / 4) and as keys of V (chunk g)
     struct Place {
       int id;         // -1: none
@@ -269,7 +301,7 @@ __global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH =
           }
         }
       }
-      const float factor = finite_factor(e8m0_to_f32(x.ks) * p.a.c);
+      const float k_scale = e8m0_to_f32(x.ks);
       uint32_t vs_now = x.vs;
       const int id_v = x.id;
       load_k(x, at_k, at_v);
@@ -278,11 +310,13 @@ __global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH =
       const int my0 = key0 + 16 * g;  // this lane's 16 keys
       const bool whole = key0 >= all_lo && key0 + kTile <= all_hi && __ballot(id_v < 0 || vs_now > AttnTraits<T>::kMostV) == 0;
 #pragma unroll
-      for (int r = 0; r < NR; ++r)
+      for (int r = 0; r < NR; ++r) {
+        const float factor = finite_factor(k_scale * c[r]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[r][i][j] *= factor;
+      }
       uint32_t nan_any = 0, seen[NR];
 #pragma unroll
       for (int r = 0; r < NR; ++r) seen[r] = 0;
@@ -412,6 +446,7 @@ __global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH =
         next_k = place_of(t + i + 1, col >> 2);
         next_v = place_of(t + i + 1, g);
       }
+      hold_far_rows();  // (behind the first loads: it waits for the queries)
       for (; t < t_end; t += DEPTH) {
 #pragma unroll
         for (int i = 0; i < DEPTH; ++i) {

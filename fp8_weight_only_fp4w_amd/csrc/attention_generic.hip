@@ -61,7 +61,10 @@ __global__ __launch_bounds__(256) void attention_generic_kernel(const AttnParams
     hi = hi < p.seq.capacity ? hi : p.seq.capacity;
     const T* q = static_cast<const T*>(p.q) + m * p.q_stride + static_cast<int64_t>(h) * D;
     __syncthreads();
-    for (int d = tid; d < D; d += 256) qs[d] = static_cast<float>(q[d]);
+    float most = 0.0f;
+    for (int d = tid; d < D; d += 256) most = fmaxf(most, fabsf(static_cast<float>(q[d])));
+    const bool far = block_reduce(most, red, false) >= kFar;
+    for (int d = tid; d < D; d += 256) qs[d] = static_cast<float>(q[d]) * (far ? kFarDown : 1.0f);
     __syncthreads();
     float top = -INFINITY, sum = 0.0f, acc[kPer] = {};
     for (int64_t t0 = lo; t0 < hi; t0 += 256) {
@@ -75,7 +78,7 @@ __global__ __launch_bounds__(256) void attention_generic_kernel(const AttnParams
         const uint8_t* k = p.k_cache + (cell * page + slot) * D;
         float dot = 0.0f;
         for (int d = 0; d < D; ++d) dot = fmaf(qs[d], e4m3_to_f32<0>(k[d]), dot);
-        score = dot * e8m0_to_f32(p.k_scale[cell]) * p.scale;
+        score = dot * e8m0_to_f32(p.k_scale[cell]) * p.scale * (far ? kFarUp : 1.0f);
         vs = e8m0_to_f32(p.v_scale[cell]);
         at[tid] = cell * D * page + slot;
       }

@@ -133,7 +133,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
   const int w_rows = r.rows - 32 * wave < 32 ? r.rows - 32 * wave : 32;
   const int w_low = r.first + (r.row0 + 32 * wave) / p.G, w_high = r.first + (r.row0 + 32 * wave + w_rows - 1) / p.G;
   const int all_lo = p.window > 0 && w_high >= p.window ? w_high - p.window + 1 : 0;
-  const int all_hi = w_rows <= 0 ? 0 : p.causal && w_low + 1 < r.held ? w_low + 1 : r.held;
+  int all_hi = w_rows <= 0 ? 0 : p.causal && w_low + 1 < r.held ? w_low + 1 : r.held;
   const int g_low = r.first + r.row0 / p.G, g_high = r.first + (r.row0 + r.rows - 1) / p.G;
   const int every_lo = p.window > 0 && g_high >= p.window ? g_high - p.window + 1 : 0;
   const int every_hi = p.causal && g_low + 1 < r.held ? g_low + 1 : r.held;
@@ -242,6 +242,26 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
     if (tid < 2) nan_tile[tid] = 0;
     load(place_of(t_begin));
     Place next = place_of(t_begin + 1);
+    uint64_t far_lanes = 0;  // whose queries are held smaller
+    if constexpr (AttnTraits<T>::kFarQueries) {
+      uint32_t far = 0;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        const u32x4 v = __builtin_bit_cast(u32x4, qf[i]);
+        far |= (far_pair(v.x) | far_pair(v.y)) | (far_pair(v.z) | far_pair(v.w));
+      }
+      far_lanes = __ballot(far != 0);
+      if (far_lanes != 0) {  // (lanes l and l + 32 have a row)
+        all_hi = 0;          // no tile goes without the masks, which scale the scores up
+        far_lanes |= far_lanes << 32 | far_lanes >> 32;
+        if (far_lanes >> lane & 1)
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            const u32x4 v = __builtin_bit_cast(u32x4, qf[i]);
+            qf[i] = __builtin_bit_cast(vec8, u32x4{down_pair(v.x), down_pair(v.y), down_pair(v.z), down_pair(v.w)});
+          }
+      }
+    }
     __syncthreads();
     prepare(t_begin, 0);
     convert(0);
@@ -273,6 +293,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
           const bool here = ((absent >> (2 * i + h)) & 1) == 0;
           const int my0 = key0 + 32 * i + 16 * h;
           const int from = here ? k_lo - my0 : 16, to = k_hi - my0;  // this lane's 16 keys: [from, to) are attended
+          if (far_lanes >> lane & 1) factor[i] = finite_factor(factor[i] * kFarUp);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const bool on = j >= from && j < to;

@@ -119,6 +119,23 @@ __device__ __forceinline__ int last_not_above(int B, int64_t u, F&& at) {
   return lo;
 }
 
+// ------------------------------------------------------------------ far queries
+//
+// Scores are summed over codes of up to 448, and take the page's scale behind the
+// sum.  A row with a query of kFar or more (BF16 reaches 2^128) is held times
+// 2^-24 for the products, which then stay below 2^104 * 448 * 1024, and its scores
+// are scaled up again.
+constexpr float kFar = 0x1p104f, kFarUp = 0x1p24f, kFarDown = 0x1p-24f;
+
+// Nonzero if one of a pair of BF16 values is kFar or more (or no number).
+__device__ __forceinline__ uint32_t far_pair(uint32_t w) {
+  return ((w & 0x7fff7fffu) + 0x0c800c80u) & 0x80008000u;  // 0x7380 is 2^104
+}
+__device__ __forceinline__ uint32_t down_pair(uint32_t w) {
+  const uint32_t lo = __float_as_uint(__uint_as_float(w << 16) * kFarDown), hi = __float_as_uint(__uint_as_float(w & 0xffff0000u) * kFarDown);
+  return (hi & 0xffff0000u) | lo >> 16;
+}
+
 // ------------------------------------------------------------------ norm and rotation
 
 struct Rope {

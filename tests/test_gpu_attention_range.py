@@ -51,6 +51,39 @@ def test_rows_whose_every_score_is_minus_infinity(case, dtype):
     check(q, parts, starts, lens, table, dtype, scale=1.0, window=window)
 
 
+# held before, new, page, Hq, Hk, D
+FAR = [
+    ([900, 3], [1, 1], 16, 5, 1, 128),
+    ([3000, 0, 40], [2, 1, 3], 16, 8, 2, 128),
+    ([500, 20], [5, 4], 32, 8, 2, 128),   # 20 rows of a key head
+    ([200, 3, 70], [2, 4, 3], 32, 28, 4, 64),
+    ([70], [150], 16, 3, 1, 128),
+    ([5000], [40], 16, 8, 1, 64),         # joined from several parts
+    ([33, 0], [2, 30], 10, 2, 1, 48),
+]
+
+
+@pytest.mark.parametrize("case", FAR, ids=lambda c: f"{max(c[0])}+{max(c[1])}-{c[3]}/{c[4]}x{c[5]}")
+def test_queries_near_the_end_of_bf16_and_small_keys(case):
+    """q times the codes passes FP32, q times the keys does not; rows of ordinary queries stand beside."""
+    held, new, page, Hq, Hk, D = case
+    rng = np.random.default_rng(71 + D)
+    starts, lens, table, pages = batch(rng, held, new, page)
+    parts = filled(rng, starts, lens, table, page, pages, Hk, D)
+    parts[2][:] = rng.integers(1, 4, parts[2].shape)
+    M = int(starts[-1])
+    q = rounded(rng, (M, Hq, D), "bf16", 1.2)
+    up = rng.integers(104, 126, (M, Hq, 1))
+    up[rng.random((M, Hq, 1)) < 0.3] = 0
+    up[0, 0], up[-1, -1] = 125, 104
+    q = q * 2.0 ** up
+    assert np.abs(q).max() * 448 * 16 > np.finfo(np.float32).max > np.abs(q).max()
+    Y, L, _, _ = oa.attention(q, *parts, starts, lens, table, 0.125)
+    assert np.isfinite(Y).all() and np.isfinite(L).all()
+    check(q, parts, starts, lens, table, "bf16", scale=0.125)
+    check(q, parts, starts, lens, table, "bf16", scale=-0.125)
+
+
 @pytest.mark.parametrize("n", [1, 40])
 @pytest.mark.parametrize("D,page", [(64, 16), (128, 16), (24, 6)])
 def test_keys_of_zero_under_the_largest_scale(D, page, n):
