@@ -58,7 +58,7 @@ struct AttnTraits<__bf16> {
   static constexpr float kLag = 8.0f;       // and m may be smaller than the largest s so far by kLag
   static constexpr uint32_t kDown = 0;      // V is held times 2^-kDown
   static constexpr bool kFarQueries = true;
-  static constexpr uint32_t kMostV = 246;   // 448 * 2^119 is below BF16's largest value
+  static constexpr uint32_t kMostV = 246;   // the largest scale under which T holds every value: 448 * 2^119
   __device__ __forceinline__ static bf16x2 cvt(uint32_t w, float s, bool hi) {
     return hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true) : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false);
   }
@@ -85,6 +85,17 @@ __device__ __forceinline__ typename ActTraits<T>::vec8 decode8_power(uint32_t lo
   r[0] = a[0]; r[1] = a[1]; r[2] = b[0]; r[3] = b[1];
   r[4] = c[0]; r[5] = c[1]; r[6] = d[0]; r[7] = d[1];
   return r;
+}
+
+// Codes of V under scale byte `scale`, with the NaN code for what T does not hold:
+// under kMostV + x that is a code of (16 - x) * 8 or more (a value of 2^128 for BF16,
+// as for FP32; of 2^17 for FP16, which holds halves), from x = 16 on any but 0,
+// and all where the scale is no number.
+template <typename T>
+__device__ __forceinline__ uint32_t codes_held(uint32_t w, uint32_t scale) {
+  const uint32_t x = scale - AttnTraits<T>::kMostV;
+  const uint32_t step = scale <= AttnTraits<T>::kMostV ? 0u : scale == 255 ? 0x80808080u : x < 16 ? x * 0x08080808u : 0x7f7f7f7fu;
+  return w | ((((w & 0x7f7f7f7fu) + step) & 0x80808080u) >> 7) * 0x7fu;
 }
 
 // 0x80 in each byte of w that is a NaN code.

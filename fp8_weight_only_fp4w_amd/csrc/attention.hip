@@ -321,7 +321,12 @@ __global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH =
 #pragma unroll
       for (int r = 0; r < NR; ++r) seen[r] = 0;
       if (!whole) {
-        const bool bad = vs_now > AttnTraits<T>::kMostV;
+        if (__ballot(vs_now > AttnTraits<T>::kMostV) != 0) {
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x.v[d][j] = codes_held<T>(x.v[d][j], vs_now);
+        }
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           const int lo = id_v < 0 ? 16 : k_lo[r] - my0, hi = k_hi[r] - my0;  // of this lane's keys, [lo, hi) are attended
@@ -339,12 +344,12 @@ __global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH =
           const uint32_t keep = id_v < 0 ? 0 : byte_mask(any_lo - (my0 + 4 * j), any_hi - (my0 + 4 * j));
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
-            const uint32_t word = (bad ? 0x7f7f7f7fu : x.v[d][j]) & keep;
+            const uint32_t word = x.v[d][j] & keep;
             x.v[d][j] = word;
             nan_any |= nan_codes(word);
           }
         }
-        if (bad || id_v < 0) vs_now = 127;
+        if (vs_now == 255 || id_v < 0) vs_now = 127;
       }
       float top[NR];
       bool grown = false;

@@ -41,7 +41,7 @@ __device__ __forceinline__ float block_reduce(float v, float* red, bool sum) {
 
 template <typename T>
 __global__ __launch_bounds__(256) void attention_generic_kernel(const AttnParams p) {
-  __shared__ float qs[kMaxHead], weight[256], red[4];
+  __shared__ float qs[kMaxHead], weight[256], v_scale[256], red[4];
   __shared__ int64_t at[256];  // of a token's values in the cache; -1: not attended
   const int tid = threadIdx.x, D = p.D, page = p.seq.page;
   const int64_t units = static_cast<int64_t>(p.seq.M) * p.Hq;
@@ -88,7 +88,8 @@ __global__ __launch_bounds__(256) void attention_generic_kernel(const AttnParams
       const float w = id >= 0 ? expf(score - base) : 0.0f;
       const float shrink = expf(top - base);
       sum = sum * shrink + block_reduce(w, red, true);
-      weight[tid] = w * vs;
+      weight[tid] = w;
+      v_scale[tid] = vs;
       __syncthreads();
       const int n = static_cast<int>(hi - t0 < 256 ? hi - t0 : 256);
 #pragma unroll
@@ -97,7 +98,10 @@ __global__ __launch_bounds__(256) void attention_generic_kernel(const AttnParams
         if (d < D) {
           float a = acc[j] * shrink;
           for (int i = 0; i < n; ++i)
-            if (at[i] >= 0) a = fmaf(weight[i], e4m3_to_f32<0>(p.v_cache[at[i] + static_cast<int64_t>(d) * page]), a);
+            if (at[i] >= 0) {
+              const float v = e4m3_to_f32<0>(p.v_cache[at[i] + static_cast<int64_t>(d) * page]) * v_scale[i];
+              a = fmaf(weight[i], fabsf(v) < INFINITY ? v : NAN, a);  // (2^128 and more: NaN, as in the other kernels)
+            }
           acc[j] = a;
         }
       }

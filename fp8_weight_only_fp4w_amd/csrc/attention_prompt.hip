@@ -177,14 +177,19 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
   // What the rows of a tile's edge, absent pages and odd scales need, for the
   // tile in the registers, which goes to buffer buf.
   auto prepare = [&](int t, int buf) {
-    const bool bad = v_byte > AttnTraits<T>::kMostV;
-    const uint64_t odd = __ballot(id < 0 || bad);  // (every wave has all four chunks)
+    const uint64_t odd = __ballot(id < 0 || v_byte > AttnTraits<T>::kMostV);  // (every wave has all four chunks)
     uint32_t byte = v_byte;
     if (t * kTile < every_lo || t * kTile + kTile > every_hi || odd != 0) {
       // Not every row attends all of the tile.  Values that none does become 0,
-      // whatever they hold; those of a page whose scale is no number (or too
-      // large for T) become NaN; and NaN is noted apart, with 0 in its place.
+      // whatever they hold; those that T does not hold, and of a page whose scale
+      // is no number, become NaN; and NaN is noted apart, with 0 in its place.
       asm volatile("" ::: "memory");
+      if (__ballot(byte > AttnTraits<T>::kMostV) != 0) {
+#pragma unroll
+        for (int i = 0; i < CHUNKS; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) vreg[i][j] = codes_held<T>(vreg[i][j], byte);
+      }
       const int key0 = t * kTile + 16 * chunk;
       uint32_t nans[CHUNKS], any = 0;
 #pragma unroll
@@ -194,12 +199,12 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
         const uint32_t keep = id < 0 ? 0u : byte_mask(any_lo - (key0 + 4 * j), any_hi - (key0 + 4 * j));
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i) {
-          const uint32_t word = (bad ? 0x7f7f7f7fu : vreg[i][j]) & keep, n = nan_codes(word) >> 7;
+          const uint32_t word = vreg[i][j] & keep, n = nan_codes(word) >> 7;
           vreg[i][j] = word & ~(n * 0xffu);
           nans[i] |= ((n & 1) | (n >> 7 & 2) | (n >> 14 & 4) | (n >> 21 & 8)) << (4 * j);
         }
       }
-      if (bad || id < 0) byte = 127;
+      if (byte == 255 || id < 0) byte = 127;
 #pragma unroll
       for (int i = 0; i < CHUNKS; ++i) {
         nan_lds[buf][piece + STEP * i][chunk] = static_cast<uint16_t>(nans[i]);

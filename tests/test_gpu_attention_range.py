@@ -4,10 +4,11 @@ that takes the case: against the float64 oracle."""
 import numpy as np
 import pytest
 
-from attention_cases import batch, filled, rounded
+import fp8_weight_only_fp4w_amd as fw
+from attention_cases import batch, filled, on_gpu, rounded, to_cache, within
 from gpu_helpers import require_gpu
 from oracle import attention as oa
-from test_gpu_attention import check
+from test_gpu_attention import check, paths
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +97,65 @@ def test_keys_of_zero_under_the_largest_scale(D, page, n):
         parts[0][table[b, 1]] = 0
     q = rounded(rng, (2 * n, 3, D), "bf16", 0.1)
     check(q, parts, starts, lens, table, "bf16", scale=3.0)
+
+
+# held before, new, page, Hq, Hk, D
+LARGE = [
+    ([0], [1], 16, 2, 1, 64),
+    ([40, 3], [1, 1], 16, 5, 1, 128),
+    ([30, 9], [20, 7], 16, 4, 2, 64),
+    ([8], [40], 32, 20, 2, 128),
+    ([20, 5], [4, 2], 10, 2, 1, 48),
+]
+
+
+@pytest.mark.parametrize("byte", [245, 246, 247, 250, 254])
+@pytest.mark.parametrize("case", LARGE, ids=lambda c: f"{max(c[0])}+{max(c[1])}-{c[3]}/{c[4]}x{c[5]}")
+def test_values_near_the_end_of_bf16(case, byte):
+    """Pages of BF16 values with a scale of up to 2^127: an appended value above 1.75 * 2^127 leads to 2^120."""
+    held, new, page, Hq, Hk, D = case
+    rng = np.random.default_rng(73 + D)
+    starts, lens, table, pages = batch(rng, held, new, page)
+    parts = filled(rng, starts, lens, table, page, pages, Hk, D)
+    last = 0.5 * 2.0 ** 127  # half the end: sums in FP32 stay below it
+    for b in range(len(lens)):
+        p = table[b, 0]
+        v = rng.choice([0.0, 2.0 ** -9, 2.0 ** -6, 3.0, 104.0], (Hk, D))
+        parts[1][p] = oa.encode(rng.choice([0.0, 2.0 ** -9, -(2.0 ** -9)], (Hk, D, page)))
+        parts[1][p, :, :, 0] = oa.encode(np.minimum(v, last / 2.0 ** (byte - 127)))  # one large token
+        parts[3][p] = byte
+    q = rounded(rng, (int(starts[-1]), Hq, D), "bf16")
+    Y, _, tol, _ = oa.attention(q, *parts, starts, lens, table, 0.05)
+    assert np.isfinite(Y).all() and np.isfinite(tol).all() and np.abs(Y).max() > 2.0 ** 110
+    check(q, parts, starts, lens, table, "bf16", scale=0.05)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 32), (48, 10)])
+@pytest.mark.parametrize("dtype,byte,code,below", [("bf16", 247, 0x78, 0x77), ("bf16", 247, 0xFE, 0xF7), ("bf16", 254, 0x40, 0x3F), ("fp16", 136, 0x78, 0x01),
+                                                   ("fp16", 150, 0xF8, 0x00), ("fp16", 170, 0x01, 0x00), ("fp16", 254, 0x31, 0x80)])
+def test_values_that_the_type_does_not_hold(dtype, byte, code, below, D, page, n):
+    """Stored values of 2^128 and more, and for FP16 of 2^17 and more in the kernels for heads of 64 and 128, count as
+    NaN each for itself: rows that do not attend them and the values beside them stay as they are."""
+    if dtype == "fp16" and (D == 48 or page % 16):
+        pytest.skip("another kernel, with FP32 values")
+    rng = np.random.default_rng(75)
+    starts, lens, table, pages = batch(rng, [3, 20], [n, n], page)
+    parts = filled(rng, starts, lens, table, page, pages, 1, D)
+    t = 3 + n // 2
+    p, slot = table[0, t // page], t % page
+    parts[1][p] = 0
+    parts[1][p, 0, 1, slot] = below
+    parts[3][p] = byte
+    want = [x.copy() for x in parts]
+    want[1][p, 0, 2, slot] = 0x7F
+    parts[1][p, 0, 2, slot] = code
+    q = rounded(rng, (2 * n, 4, D), dtype)
+    Y, _, tol, _ = oa.attention(q, *want, starts, lens, table, 0.05, dtype=dtype)
+    assert np.isnan(Y[n // 2: n, :, 2]).all() and np.isnan(Y).sum() == 4 * (n - n // 2)  # the token's own row and those behind it
+    c, g, ids, st, ln = to_cache(parts), on_gpu(q, dtype), on_gpu(table), on_gpu(starts), on_gpu(lens)
+    for path in paths(D, page, 4 * n):
+        if dtype == "fp16" and path == fw.PATH_ATTN_GENERIC:
+            continue
+        got = fw.fp8w_attention(g, c, ids, ln, starts=st, max_new=n, scale=0.05, path=path)
+        within(got, Y, tol, dtype, f"path {fw.fp4w_path_name(path)}")
