@@ -56,9 +56,12 @@ template <>
 struct AttnTraits<__bf16> {
   static constexpr float kLift = 0.0f;      // numerators are 2^(s - m + kLift)
   static constexpr float kLag = 8.0f;       // and m may be smaller than the largest s so far by kLag
-  static constexpr uint32_t kDown = 0;      // V is held times 2^-kDown
+  // V is held times 2^-kDown.  BF16 values reach FP32's end, and numerators of up to
+  // 2^kLag, or a sum over many tokens, would pass it where their average does not.
+  // Of that, values below 2^-102 lose bits (down to steps of 2^-109).
+  static constexpr uint32_t kDown = 24;
   static constexpr bool kFarQueries = true;
-  static constexpr uint32_t kMostV = 246;   // the largest scale under which T holds every value: 448 * 2^119
+  static constexpr uint32_t kLeastV = 25, kMostV = 254;  // the scales under which T holds every value so
   __device__ __forceinline__ static bf16x2 cvt(uint32_t w, float s, bool hi) {
     return hi ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true) : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false);
   }
@@ -71,7 +74,7 @@ struct AttnTraits<_Float16> {
   static constexpr float kLag = 6.0f;
   static constexpr uint32_t kDown = 1;
   static constexpr bool kFarQueries = false;  // 65504 * 448 * 128 is far from FP32's end
-  static constexpr uint32_t kMostV = 135;
+  static constexpr uint32_t kLeastV = 0, kMostV = 135;
   __device__ __forceinline__ static f16x2 cvt(uint32_t w, float s, bool hi) {
     return hi ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, true) : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, false);
   }
@@ -87,15 +90,26 @@ __device__ __forceinline__ typename ActTraits<T>::vec8 decode8_power(uint32_t lo
   return r;
 }
 
-// Codes of V under scale byte `scale`, with the NaN code for what T does not hold:
-// under kMostV + x that is a code of (16 - x) * 8 or more (a value of 2^128 for BF16,
-// as for FP32; of 2^17 for FP16, which holds halves), from x = 16 on any but 0,
-// and all where the scale is no number.
+// Whether T holds every value under scale byte `scale`.
+template <typename T>
+__device__ __forceinline__ bool held_scale(uint32_t scale) {
+  return scale - AttnTraits<T>::kLeastV <= AttnTraits<T>::kMostV - AttnTraits<T>::kLeastV;
+}
+// Codes of V under a scale byte: those that mean the same under kLeastV where it is
+// below that, and the NaN code for what T does not hold.  Under kMostV + x that is
+// a code of (16 - x) * 8 or more (for FP16, which holds halves, a value of 2^17),
+// from x = 16 on any but 0, and all where the scale is no number.
 template <typename T>
 __device__ __forceinline__ uint32_t codes_held(uint32_t w, uint32_t scale) {
-  const uint32_t x = scale - AttnTraits<T>::kMostV;
-  const uint32_t step = scale <= AttnTraits<T>::kMostV ? 0u : scale == 255 ? 0x80808080u : x < 16 ? x * 0x08080808u : 0x7f7f7f7fu;
+  constexpr uint32_t kLeast = AttnTraits<T>::kLeastV, kMost = AttnTraits<T>::kMostV;
+  if constexpr (kLeast > 0) w = scale_codes(w, __uint_as_float((127 - (scale < kLeast ? kLeast - scale : 0)) << 23));
+  const uint32_t x = scale - kMost, step = scale <= kMost ? 0u : scale == 255 ? 0x80808080u : x < 16 ? x * 0x08080808u : 0x7f7f7f7fu;
   return w | ((((w & 0x7f7f7f7fu) + step) & 0x80808080u) >> 7) * 0x7fu;
+}
+// The scale that goes with them.
+template <typename T>
+__device__ __forceinline__ uint32_t scale_held(uint32_t scale) {
+  return scale == 255 ? 127 : scale < AttnTraits<T>::kLeastV ? AttnTraits<T>::kLeastV : scale;
 }
 
 // 0x80 in each byte of w that is a NaN code.

@@ -308,7 +308,7 @@ __global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH =
 
       const int key0 = (lo_tile + t) * kTile;
       const int my0 = key0 + 16 * g;  // this lane's 16 keys
-      const bool whole = key0 >= all_lo && key0 + kTile <= all_hi && __ballot(id_v < 0 || vs_now > AttnTraits<T>::kMostV) == 0;
+      const bool whole = key0 >= all_lo && key0 + kTile <= all_hi && __ballot(id_v < 0 || !held_scale<T>(vs_now)) == 0;
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         const float factor = finite_factor(k_scale * c[r]);
@@ -321,7 +321,7 @@ __global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH =
 #pragma unroll
       for (int r = 0; r < NR; ++r) seen[r] = 0;
       if (!whole) {
-        if (__ballot(vs_now > AttnTraits<T>::kMostV) != 0) {
+        if (__ballot(!held_scale<T>(vs_now)) != 0) {
 #pragma unroll
           for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -349,7 +349,7 @@ __global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH =
             nan_any |= nan_codes(word);
           }
         }
-        if (vs_now == 255 || id_v < 0) vs_now = 127;
+        vs_now = id_v < 0 ? 127 : scale_held<T>(vs_now);
       }
       float top[NR];
       bool grown = false;

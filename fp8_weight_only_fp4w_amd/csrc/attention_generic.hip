@@ -27,6 +27,9 @@ struct AttnParams {
   float* lse;
 };
 
+// Values are summed times 2^-24: BF16 ones reach FP32's end, and their sum passes it.
+constexpr float kHoldDown = 0x1p-24f;
+
 __device__ __forceinline__ float block_reduce(float v, float* red, bool sum) {
   for (int off = 32; off > 0; off >>= 1) {
     const float o = __shfl_xor(v, off, 64);
@@ -89,7 +92,7 @@ __global__ __launch_bounds__(256) void attention_generic_kernel(const AttnParams
       const float shrink = expf(top - base);
       sum = sum * shrink + block_reduce(w, red, true);
       weight[tid] = w;
-      v_scale[tid] = vs;
+      v_scale[tid] = vs * kHoldDown;
       __syncthreads();
       const int n = static_cast<int>(hi - t0 < 256 ? hi - t0 : 256);
 #pragma unroll
@@ -100,7 +103,7 @@ __global__ __launch_bounds__(256) void attention_generic_kernel(const AttnParams
           for (int i = 0; i < n; ++i)
             if (at[i] >= 0) {
               const float v = e4m3_to_f32<0>(p.v_cache[at[i] + static_cast<int64_t>(d) * page]) * v_scale[i];
-              a = fmaf(weight[i], fabsf(v) < INFINITY ? v : NAN, a);  // (2^128 and more: NaN, as in the other kernels)
+              a = fmaf(weight[i], v, a);
             }
           acc[j] = a;
         }
@@ -113,7 +116,7 @@ __global__ __launch_bounds__(256) void attention_generic_kernel(const AttnParams
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int d = tid + j * 256;
-      if (d < D) static_cast<T*>(p.Y)[u * D + d] = round_to<T>(none ? 0.0f : acc[j] / sum);
+      if (d < D) static_cast<T*>(p.Y)[u * D + d] = round_to<T>(none ? 0.0f : acc[j] / (sum * kHoldDown));
     }
     if (p.lse != nullptr && tid == 0) p.lse[u] = none ? -INFINITY : sum == 0.0f ? NAN : top + logf(sum);
   }

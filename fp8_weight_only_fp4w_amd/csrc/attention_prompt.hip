@@ -177,14 +177,14 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
   // What the rows of a tile's edge, absent pages and odd scales need, for the
   // tile in the registers, which goes to buffer buf.
   auto prepare = [&](int t, int buf) {
-    const uint64_t odd = __ballot(id < 0 || v_byte > AttnTraits<T>::kMostV);  // (every wave has all four chunks)
+    const uint64_t odd = __ballot(id < 0 || !held_scale<T>(v_byte));  // (every wave has all four chunks)
     uint32_t byte = v_byte;
     if (t * kTile < every_lo || t * kTile + kTile > every_hi || odd != 0) {
       // Not every row attends all of the tile.  Values that none does become 0,
       // whatever they hold; those that T does not hold, and of a page whose scale
       // is no number, become NaN; and NaN is noted apart, with 0 in its place.
       asm volatile("" ::: "memory");
-      if (__ballot(byte > AttnTraits<T>::kMostV) != 0) {
+      if (__ballot(!held_scale<T>(byte)) != 0) {
 #pragma unroll
         for (int i = 0; i < CHUNKS; ++i)
 #pragma unroll
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
           nans[i] |= ((n & 1) | (n >> 7 & 2) | (n >> 14 & 4) | (n >> 21 & 8)) << (4 * j);
         }
       }
-      if (byte == 255 || id < 0) byte = 127;
+      byte = id < 0 ? 127 : scale_held<T>(byte);
 #pragma unroll
       for (int i = 0; i < CHUNKS; ++i) {
         nan_lds[buf][piece + STEP * i][chunk] = static_cast<uint16_t>(nans[i]);

@@ -292,6 +292,12 @@ __device__ __forceinline__ uint32_t e4m3_pair(float a, float b) {
   return na | nb;
 }
 
+// Four codes times a power of two of 1 or less.
+__device__ __forceinline__ uint32_t scale_codes(uint32_t w, float down) {
+  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false), b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
+  return e4m3_pair(a.x * down, a.y * down) | e4m3_pair(b.x * down, b.y * down) << 16;
+}
+
 __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);
   return a < INFINITY ? a : 0.0f;

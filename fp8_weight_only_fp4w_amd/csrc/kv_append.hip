@@ -142,12 +142,6 @@ __global__ __launch_bounds__(256) void kv_append_generic_kernel(const AppendPara
   }
 }
 
-// The old codes of slots [0, lo) times 2^-x, x = e - before.
-__device__ __forceinline__ uint32_t scale_codes(uint32_t w, float down) {
-  const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), false), b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(w), true);
-  return e4m3_pair(a.x * down, a.y * down) | e4m3_pair(b.x * down, b.y * down) << 16;
-}
-
 // Eight values as codes.
 __device__ __forceinline__ u32x2 codes8(const float* v, float inv) {
   u32x2 c;

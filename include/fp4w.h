@@ -599,11 +599,11 @@ int64_t fp8w_attention_workspace(int64_t M, int64_t Hq, int64_t Hk, int64_t D, i
  * among it, does not show.  Scores, softmax and sums are FP32; the softmax's
  * numerators are rounded to T for their product with V; Y is rounded once.  The result for a
  * row does not depend on the order in which the GPU works, but its last bits
- * may on the rest of the batch (where its sum is cut).  A stored value of
- * 2^128 or more, which FP32 does not hold, counts as NaN (appended BF16 leads
- * to one from 31 * 2^123 up); so does, in the decode and prompt kernels, for
- * FP16 one of 2^17 or more, or any but 0 in a page with a value scale of 2^24
- * or more (appended FP16 stays below).
+ * may on the rest of the batch (where its sum is cut).  Values are held in T
+ * for their product, FP16 in steps of 2^-23 and BF16 of 2^-109 at the least
+ * (the generic kernel: in FP32).  FP16 in the decode and prompt kernels: a
+ * stored value of 2^17 or more counts as NaN, as does any but 0 in a page with
+ * a value scale of 2^24 or more (appended FP16 stays below both).
  *
  *   q        T[M, Hq, D] with a stride.   Hq is a multiple of Hk.
  *   max_new  no sequence has more new tokens (rows behind it are left as they

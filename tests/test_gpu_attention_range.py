@@ -131,14 +131,12 @@ def test_values_near_the_end_of_bf16(case, byte):
 
 
 @pytest.mark.parametrize("n", [1, 40])
-@pytest.mark.parametrize("D,page", [(64, 16), (128, 32), (48, 10)])
-@pytest.mark.parametrize("dtype,byte,code,below", [("bf16", 247, 0x78, 0x77), ("bf16", 247, 0xFE, 0xF7), ("bf16", 254, 0x40, 0x3F), ("fp16", 136, 0x78, 0x01),
-                                                   ("fp16", 150, 0xF8, 0x00), ("fp16", 170, 0x01, 0x00), ("fp16", 254, 0x31, 0x80)])
-def test_values_that_the_type_does_not_hold(dtype, byte, code, below, D, page, n):
-    """Stored values of 2^128 and more, and for FP16 of 2^17 and more in the kernels for heads of 64 and 128, count as
-    NaN each for itself: rows that do not attend them and the values beside them stay as they are."""
-    if dtype == "fp16" and (D == 48 or page % 16):
-        pytest.skip("another kernel, with FP32 values")
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 32)])
+@pytest.mark.parametrize("byte,code,below", [(136, 0x78, 0x01), (150, 0xF8, 0x00), (170, 0x01, 0x00), (254, 0x31, 0x80)])
+def test_values_that_fp16_does_not_hold(byte, code, below, D, page, n):
+    """In the decode and prompt kernels, stored values of 2^17 and more count as NaN each for itself: rows that do not
+    attend them and the values beside them stay as they are."""
+    dtype = "fp16"
     rng = np.random.default_rng(75)
     starts, lens, table, pages = batch(rng, [3, 20], [n, n], page)
     parts = filled(rng, starts, lens, table, page, pages, 1, D)
@@ -155,7 +153,61 @@ def test_values_that_the_type_does_not_hold(dtype, byte, code, below, D, page, n
     assert np.isnan(Y[n // 2: n, :, 2]).all() and np.isnan(Y).sum() == 4 * (n - n // 2)  # the token's own row and those behind it
     c, g, ids, st, ln = to_cache(parts), on_gpu(q, dtype), on_gpu(table), on_gpu(starts), on_gpu(lens)
     for path in paths(D, page, 4 * n):
-        if dtype == "fp16" and path == fw.PATH_ATTN_GENERIC:
+        if path == fw.PATH_ATTN_GENERIC:
             continue
         got = fw.fp8w_attention(g, c, ids, ln, starts=st, max_new=n, scale=0.05, path=path)
         within(got, Y, tol, dtype, f"path {fw.fp4w_path_name(path)}")
+
+
+@pytest.mark.parametrize("byte", [222, 223, 240, 246, 247])
+@pytest.mark.parametrize("D,page,n", [(64, 16, 2), (128, 64, 40), (64, 32, 130), (40, 8, 3)])
+def test_a_growing_score_with_a_large_value(D, page, n, byte):
+    """A token behind several tiles that scores 2^6 times the ones before, and whose values reach 2^126."""
+    rng = np.random.default_rng(74)
+    starts, lens, table, pages = batch(rng, [300], [n], page)
+    parts = filled(rng, starts, lens, table, page, pages, 1, D)
+    parts[0][:] = oa.encode(rng.choice([0.0, 0.125, -0.125], parts[0].shape))
+    parts[2][:], parts[3][:] = 127, 127
+    t = 200
+    p = table[0, t // page]
+    parts[0][p, 0, t % page] = oa.encode(np.full(D, 4.0))
+    parts[1][p] = oa.encode(rng.choice([0.0, 2.0 ** -9, -(2.0 ** -9)], (1, D, page)))
+    parts[1][p, 0, :, t % page] = oa.encode(np.minimum(rng.uniform(100, 400, D), 2.0 ** (126 + 127 - byte)))
+    parts[3][p] = byte
+    q = np.ones((n, 2, D))
+    Y, _, tol, _ = oa.attention(q, *parts, starts, lens, table, 1.0 / D)
+    assert np.isfinite(Y).all() and np.isfinite(tol).all()
+    check(q, parts, starts, lens, table, "bf16", scale=1.0 / D)
+
+
+@pytest.mark.parametrize("held,n,page,D", [(400, 1, 16, 64), (5000, 3, 16, 128), (400, 60, 16, 128), (6000, 50, 64, 64), (300, 2, 6, 40)])
+def test_sums_of_values_near_the_end_of_bf16(held, n, page, D):
+    """Values near 2^128, and stored ones above: their sum is not FP32's, their average is."""
+    rng = np.random.default_rng(76)
+    starts, lens, table, pages = batch(rng, [held], [n], page)
+    parts = filled(rng, starts, lens, table, page, pages, 1, D)
+    q = rounded(rng, (n, 2, D), "bf16")
+    parts[3][:] = 247
+    for codes in (np.where(rng.random((1, 1, D, 1)) < 0.5, 0x77, 0xF6),             # 240 and -224
+                  np.where(rng.random(parts[1].shape) < 0.45, 0x7E, 0x00)):         # 448 now and then
+        parts[1][:] = codes
+        Y, _, tol, _ = oa.attention(q, *parts, starts, lens, table, 0.01)
+        assert (np.abs(Y) > 2.0 ** 126).all() and (np.abs(Y) < 2.0 ** 128).all()
+        check(q, parts, starts, lens, table, "bf16", scale=0.01)
+
+
+@pytest.mark.parametrize("lo,hi", [(24, 27), (14, 30)])
+@pytest.mark.parametrize("held,n,page,D", [(100, 1, 16, 64), (3000, 2, 16, 128), (100, 60, 16, 128), (90, 2, 6, 40)])
+def test_smallest_values(held, n, page, D, lo, hi):
+    """Page scales down to 2^-113, of FP32's smallest numbers times 2^13: right to the steps of 2^-109 that values are held in."""
+    rng = np.random.default_rng(77)
+    starts, lens, table, pages = batch(rng, [held], [n], page)
+    parts = filled(rng, starts, lens, table, page, pages, 1, D)
+    parts[3][:] = rng.integers(lo, hi, parts[3].shape)
+    q = rounded(rng, (n, 4, D), "bf16")
+    Y, _, tol, _ = oa.attention(q, *parts, starts, lens, table, 0.05)
+    assert np.abs(Y).max() > 2.0 ** -106
+    c, g, ids, st, ln = to_cache(parts), on_gpu(q, "bf16"), on_gpu(table), on_gpu(starts), on_gpu(lens)
+    for path in paths(D, page, 4 * n):
+        got = fw.fp8w_attention(g, c, ids, ln, starts=st, max_new=n, scale=0.05, path=path)
+        within(got, Y, tol + 2.0 ** -109, "bf16", f"path {fw.fp4w_path_name(path)}")
