@@ -33,7 +33,7 @@ namespace {
 struct PromptParams {
   AttnParams a;
   float* part;      // splits > 1: partial results
-  int32_t splits;   // parts that a row tile's keys are cut into
+  int32_t splits;   // parts that a row tile's keys are cut into at most
   int64_t units;    // row tiles at most
 };
 
@@ -88,6 +88,12 @@ __device__ __forceinline__ bool row_tile_of(const AttnParams& p, int64_t unit, R
   return true;
 }
 
+// Parts that a row tile's keys are cut into.
+__device__ __forceinline__ int row_parts(const RowTile& r, int splits) {
+  const int most = (r.hi - r.lo) / kPromptPart;
+  return most < 1 ? 1 : most < splits ? most : splits;
+}
+
 template <typename T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kernel(const PromptParams pp) {
   constexpr int R = 32 * WAVES, KP = D + 8, VP = kTile + 8, KS = D / 16, DT = D / 32;
@@ -108,7 +114,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
   const int split = static_cast<int>(block % pp.splits);
   RowTile r;
   if (!row_tile_of<R>(p, unit, r)) return;
-  const int share = (r.hi - r.lo + pp.splits - 1) / pp.splits;
+  const int parts = row_parts(r, pp.splits), share = (r.hi - r.lo + parts - 1) / parts;
+  if (split >= parts) return;
   const int t_begin = r.lo + share * split < r.hi ? r.lo + share * split : r.hi;
   const int t_end = t_begin + share < r.hi ? t_begin + share : r.hi;
 
@@ -377,7 +384,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
   }
   l += __shfl_xor(l, 32, 64);
   if (!valid) return;
-  if (pp.splits == 1) {
+  if (parts == 1) {
     const int64_t at_row = (static_cast<int64_t>(r.token0) + token) * p.Hq + head;
 #pragma unroll
     for (int d = 0; d < DT; ++d)
@@ -400,7 +407,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
   }
 }
 
-// Joins the parts of every row: D / 4 lanes for a row, a workgroup for an eighth
+// Joins the parts of every row that has several: D / 4 lanes for a row, a workgroup for an eighth
 // of a row tile and key head.
 template <typename T, int D, int R>
 __global__ __launch_bounds__(256) void attn_prompt_join_kernel(const PromptParams pp) {
@@ -410,13 +417,15 @@ __global__ __launch_bounds__(256) void attn_prompt_join_kernel(const PromptParam
   const int64_t unit = cell / p.Hk;
   RowTile r;
   if (!row_tile_of<R>(p, unit, r)) return;
+  const int parts = row_parts(r, pp.splits);
+  if (parts == 1) return;
   const float* part = pp.part + (unit * p.Hk + hk) * pp.splits * attn_part_floats(R, D);
   const int end = first + R / 8 < r.rows ? first + R / 8 : r.rows;
   for (int mine = first + threadIdx.x / LANES; mine < end; mine += ROWS) {
     float m = -INFINITY, l = 0.0f;
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-    for (int i = 0; i < pp.splits; ++i) {
+    for (int i = 0; i < parts; ++i) {
       const float* one = part + i * attn_part_floats(R, D);
       join(m, l, o, one[mine], one[R + mine], *reinterpret_cast<const f32x4*>(one + attn_part_head(R) + mine * D + 4 * lane));
     }

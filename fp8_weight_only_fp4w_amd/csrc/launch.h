@@ -339,19 +339,22 @@ inline int64_t attn_decode_workspace(int64_t max_new, int64_t Hk, int64_t G, int
 // codes, Y and work 16-byte aligned, q_stride % 8 == 0.
 int launch_attention_decode(const AttentionArgs& a);
 // The prompt kernel: row tiles of kPromptRows rows of a sequence and key head.
-// Where there are fewer than the GPU has places for (two workgroups a compute
-// unit), their keys are cut into up to 16 parts of at least 8 key tiles, whose
-// results are in the workspace.  A part costs 133 KB of traffic for D = 128:
+// Where there are fewer than kPromptPlaces (heads of 128 have two workgroups a
+// compute unit, those of 64 three), their keys are cut into up to 16 parts, whose
+// results are in the workspace.  The host knows a row tile's keys only by what the
+// page table has room for; the kernel takes fewer parts, so that each has at least
+// kPromptPart key tiles: 200 tokens of 40 heads in a table with room for 32768
+// take 16 us so, with empty parts 31, and in a table cut to their length 14.  A part costs 133 KB of traffic for D = 128:
 // with 784 row tiles, two parts each took 85 us and whole ones 56.  With 272 over
 // ragged 5000 to 25000 tokens, 1, 2, 3, 5 and 7 parts took 420, 353, 342, 323 and
 // 320 us; with 336 over even 15000, 3, 5 and 6 parts 376, 403 and 395: two full
 // rounds of workgroups, and then parts that cost more than they even out.
-constexpr int kPromptRows = 128;
+constexpr int kPromptRows = 128, kPromptPart = 8;
 constexpr int64_t kPromptPlaces = 512, kPromptWork = 768;  // workgroups that are wanted where there are too few
 inline int64_t attn_row_tiles_most(int64_t M, int64_t G, int64_t B) { return M * G / kPromptRows + B; }
 inline int64_t attn_prompt_splits(int64_t tiles, int64_t capacity) {
   if (tiles >= kPromptPlaces) return 1;
-  const int64_t want = (kPromptWork + tiles - 1) / tiles, most = capacity / (8 * 64);
+  const int64_t want = (kPromptWork + tiles - 1) / tiles, most = capacity / (kPromptPart * 64);
   const int64_t n = want < most ? want : most;
   return n < 1 ? 1 : n < 16 ? n : 16;
 }
