@@ -439,7 +439,13 @@ __global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH =
     // Loads run ahead by DEPTH tiles, and past the last one they go on at page 0:
     // a branch around them would make the compiler wait for all loads in flight
     // wherever it waits for any.  (Without pages there is nothing to load, and no
-    // key to attend.)
+    // key to attend.)  No branch belongs there in the LOCAL form either, though it
+    // takes 0.8 us of 12 after 900 tokens: this compiler (ROCm 7.2) then loses the
+    // live ranges of the last value rows' codes in its scheduler and gives their
+    // registers to the softmax, and outputs are wrong (-verify-machineinstrs says
+    // so, "no live subrange at use"; without the scheduler the same source is
+    // right).  build.py has the verifier on for this file and attention_prompt.hip,
+    // whose branch around its loads passes.
     int t = t_begin;
     if (p.a.seq.capacity > 0 && t < t_end) {
       Tile tile[DEPTH];
