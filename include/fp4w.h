@@ -596,18 +596,23 @@ int64_t fp8w_attention_workspace(int64_t M, int64_t Hq, int64_t Hk, int64_t D, i
  * present), with t <= p if `causal` is nonzero and t > p - window if window >
  * 0.  Without any, Y is 0 and lse -inf; where every score is -inf (an infinite
  * query) both are NaN, as 0 / 0 is.  What slots of other tokens hold, NaN
- * among it, does not show.  Scores, softmax and sums are FP32; the softmax's
- * numerators are rounded to T for their product with V; Y is rounded once.  The result for a
- * row does not depend on the order in which the GPU works, but its last bits
- * may on the rest of the batch (where its sum is cut).  Values are held in T
- * for their product, FP16 in steps of 2^-23 and BF16 of 2^-109 at the least
- * (the generic kernel: in FP32).  FP16 in the decode and prompt kernels: a
- * stored value of 2^17 or more counts as NaN, as does any but 0 in a page with
- * a value scale of 2^24 or more (appended FP16 stays below both).
+ * among it, does not show.  Scores, softmax and sums are FP32; Y is rounded
+ * once.  The result for a row does not depend on the order in which the GPU
+ * works, but its last bits may on the rest of the batch (where its sum is cut).
+ * The decode and prompt kernels (heads of 64 and 128 in pages of a multiple of
+ * 16 tokens, everything 16-byte aligned) take both sides of the second product
+ * in T: the softmax's numerators, rounded, and the values, in steps of 2^-23
+ * (FP16) or 2^-109 (BF16) at the least.  There, for FP16, a stored value of 2^17
+ * or more counts as NaN, as does any but 0 in a page with a value scale of 2^24
+ * or more (appended FP16 stays below both).  The generic kernel has no such
+ * rounding and no such limit.
  *
  *   q        T[M, Hq, D] with a stride.   Hq is a multiple of Hk.
  *   max_new  no sequence has more new tokens (rows behind it are left as they
  *            were); it chooses the kernel.  1 if starts is NULL.
+ *   max_pages  how far the table reaches has a part in the choice too: up to 16
+ *            rows (new tokens x Hq / Hk) over tables with room for at most 1024
+ *            tokens take one launch, wider ones two, whatever the lengths are.
  *   workspace  at least fp8w_attention_workspace(...) bytes, 16-byte aligned;
  *            what it holds before does not matter.  Calls that may run at once
  *            (two streams, two replayed graphs) need one each.
