@@ -49,7 +49,11 @@ inline AttnParams make_attn(const AttentionArgs& a) {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// What differs by the type: P's range and V's exponent.
+// What differs by the type: P's range and V's exponent.  Numerators are rounded to T
+// between the products, as the matrix instructions take both operands in T (at a
+// sixteenth of the rate in FP32); their sum is taken before.  With the output's own
+// rounding the error against 64 bits, relative and RMS, is 1.9 to 2.1e-3 in BF16 and
+// 2.3 to 2.9e-4 in FP16; of the output's rounding alone 1.6 to 1.7e-3 and 2.0 to 2.1e-4.
 template <typename T>
 struct AttnTraits;
 template <>

@@ -15,13 +15,13 @@
 // in row 8 a + 4 h + b of K's tile.
 //
 // The matrix units, the LDS that feeds them and the vector units are the bound
-// together: of 722 us for a prompt of 8192 tokens with 40 query and 8 key heads
-// of 128 (BF16, 687 GFLOP) the products with their LDS reads take 461 alone;
-// 509 without the staging, 647 without the loads, 711 without the conversions and
-// 650 without the softmax.  It now takes 695 to 710 us, 0.98 PFLOP/s, where a
-// large library product reaches 1.28; 28 heads of 64 take 316.  Rows of 64 a
-// wave (one wave a SIMD) took 1110 us and more, 256 rows a workgroup no less than
-// 128.
+// together: of 722 us that an earlier form took for a prompt of 8192 tokens with
+// 40 query and 8 key heads of 128 (BF16, 687 GFLOP) the products with their LDS
+// reads took 461 alone; 509 without the staging, 647 without the loads, 711 without
+// the conversions and 650 without the softmax.  It now takes 685 to 718 us on
+// different cards, 0.96 to 1.0 PFLOP/s, where a large library product reaches 1.28;
+// 28 heads of 64 take 303 to 322.  Rows of 64 a wave (one wave a SIMD) took 1110 us
+// and more, 256 rows a workgroup no less than 128.
 
 #include <hip/hip_runtime.h>
 
