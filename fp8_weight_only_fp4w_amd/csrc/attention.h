@@ -110,6 +110,14 @@ __device__ __forceinline__ uint32_t codes_held(uint32_t w, uint32_t scale) {
   const uint32_t x = scale - kMost, step = scale <= kMost ? 0u : scale == 255 ? 0x80808080u : x < 16 ? x * 0x08080808u : 0x7f7f7f7fu;
   return w | ((((w & 0x7f7f7f7fu) + step) & 0x80808080u) >> 7) * 0x7fu;
 }
+// A page of zeros has the smallest scale: N words of codes that are all 0 go with any.
+template <typename T, int N>
+__device__ __forceinline__ uint32_t scale_of_zeros(const u32x4 (&v)[N], uint32_t scale) {
+  u32x4 any = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < N; ++i) any |= v[i];
+  return scale < AttnTraits<T>::kLeastV && (((any.x | any.y) | (any.z | any.w)) & 0x7f7f7f7fu) == 0 ? 127 : scale;
+}
 // The scale that goes with them.
 template <typename T>
 __device__ __forceinline__ uint32_t scale_held(uint32_t scale) {

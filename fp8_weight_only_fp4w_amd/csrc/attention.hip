@@ -308,6 +308,7 @@ __global__ __launch_bounds__(LOCAL ? 64 * kLocalWaves : 256, LOCAL ? 1 : DEPTH =
 
       const int key0 = (lo_tile + t) * kTile;
       const int my0 = key0 + 16 * g;  // this lane's 16 keys
+      if (AttnTraits<T>::kLeastV > 0 && __ballot(vs_now < AttnTraits<T>::kLeastV) != 0) vs_now = scale_of_zeros<T>(x.v, vs_now);
       const bool whole = key0 >= all_lo && key0 + kTile <= all_hi && __ballot(id_v < 0 || !held_scale<T>(vs_now)) == 0;
 #pragma unroll
       for (int r = 0; r < NR; ++r) {

@@ -184,8 +184,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 64 ? 3 : 2) void attn_prompt_kerne
   // What the rows of a tile's edge, absent pages and odd scales need, for the
   // tile in the registers, which goes to buffer buf.
   auto prepare = [&](int t, int buf) {
-    const uint64_t odd = __ballot(id < 0 || !held_scale<T>(v_byte));  // (every wave has all four chunks)
     uint32_t byte = v_byte;
+    if (AttnTraits<T>::kLeastV > 0 && __ballot(byte < AttnTraits<T>::kLeastV) != 0) byte = scale_of_zeros<T>(vreg, byte);
+    const uint64_t odd = __ballot(id < 0 || !held_scale<T>(byte));  // (every wave has all four chunks)
     if (t * kTile < every_lo || t * kTile + kTile > every_hi || odd != 0) {
       // Not every row attends all of the tile.  Values that none does become 0,
       // whatever they hold; those that T does not hold, and of a page whose scale

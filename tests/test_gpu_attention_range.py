@@ -211,3 +211,19 @@ def test_smallest_values(held, n, page, D, lo, hi):
     for path in paths(D, page, 4 * n):
         got = fw.fp8w_attention(g, c, ids, ln, starts=st, max_new=n, scale=0.05, path=path)
         within(got, Y, tol + 2.0 ** -109, "bf16", f"path {fw.fp4w_path_name(path)}")
+
+
+@pytest.mark.parametrize("held,n,page,D", [(900, 1, 16, 64), (3000, 2, 16, 128), (100, 60, 16, 128), (500, 40, 64, 64), (90, 2, 6, 40)])
+def test_pages_of_zeros(held, n, page, D):
+    """As the append leaves them: codes of 0 of either sign under the smallest scale, beside pages of ordinary and of the
+    smallest values."""
+    rng = np.random.default_rng(78)
+    starts, lens, table, pages = batch(rng, [held], [n], page)
+    parts = filled(rng, starts, lens, table, page, pages, 1, D)
+    kind = rng.integers(0, 4, pages)
+    parts[1][kind == 0] = rng.choice([0x00, 0x80], parts[1][kind == 0].shape)
+    parts[3][kind == 0], parts[3][kind == 1] = 1, 20
+    q = rounded(rng, (n, 4, D), "bf16")
+    check(q, parts, starts, lens, table, "bf16", scale=0.05)
+    parts[1][:], parts[3][:] = 0, 1
+    check(q, parts, starts, lens, table, "bf16", scale=0.05)
